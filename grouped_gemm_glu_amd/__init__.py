@@ -25,7 +25,9 @@ _lib = ctypes.CDLL(LIB_PATH)
 # ----------------------------------------------------------------------------- ABI mirror
 MOE_OK = 0
 ACT = {"swiglu": 0, "geglu": 1, "geglu_tanh": 2, "srelu": 3}
-DT_BF16, DT_MXFP8, DT_MXFP8_E5M2 = 0, 1, 2
+DT_BF16, DT_MXFP8, DT_MXFP8_E5M2, DT_MXFP4, DT_FP32 = 0, 1, 2, 3, 4
+SCORE = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORE = {"max": 0, "top2": 1}
 B_KN, B_NK, B_PACKED = 0, 1, 2
 
 
@@ -55,8 +57,16 @@ class OperandT(ctypes.Structure):
                 ("data", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+class RouterT(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_F = ctypes.c_float
+_Z = ctypes.c_size_t
 _SIGS = {
     "moe_init": ([_I], _I),
     "moe_status_string": ([_I], ctypes.c_char_p),
@@ -85,6 +95,15 @@ _SIGS = {
     "moe_glu_unfused": ([_P, ctypes.POINTER(GroupsT), _I, ctypes.POINTER(EpilogueT), _P, _P], _I),
     "moe_dglu_unfused": ([_P, _P, ctypes.POINTER(GroupsT), _I, ctypes.POINTER(EpilogueT), _P, _P], _I),
     "moe_mxfp8_quantize": ([_P, _I, _I, ctypes.POINTER(GroupsT), ctypes.POINTER(MxOutT), _P], _I),
+    "moe_router_topk": ([_P, _I, _I, _I, _I, ctypes.POINTER(RouterT), _P, _P, _P], _I),
+    "moe_router_topk_bwd": ([_P, _I, _I, _I, _I, ctypes.POINTER(RouterT), _P, _P, _P, _P], _I),
+    "moe_combine": ([_P, _I, _I, _P, _P, _I, _I, _P, _P, _P], _I),
+    "moe_combine_bwd": ([_P, _P, _I, _I, _P, _P, _I, _I, _P, _P, _P], _I),
+    "moe_add_rmsnorm": ([_P, _P, _P, _I, _I, _F, _P, _P, _P, ctypes.POINTER(MxOutT), _P], _I),
+    "moe_add_rmsnorm_bwd_workspace_bytes": ([_I, _I], _Z),
+    "moe_add_rmsnorm_bwd": ([_P, _P, _P, _P, _P, _I, _I, _P, _P, _I, _P, _Z, _P], _I),
+    "moe_mxfp4_quantize": ([_P, _I, _I, ctypes.POINTER(GroupsT), _P, _P, _P], _I),
+    "moe_pack_weight_mxfp4": ([_P, _I, _I, _I, _I, _P, _P, _P], _I),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -170,6 +189,26 @@ def mx_col_slots(M_cap: int, E: int, blocked: bool = False) -> int:
 
 def operand(data, dtype: int = DT_BF16, layout: int = 0, scales=None) -> OperandT:
     return _keep(OperandT(dtype, layout, _ptr(data), _ptr(scales)), data, scales)
+
+
+def router(score: str = "softmax", bias=None, n_groups: int = 1, topk_groups: int = 1,
+           group_score: str = "max", renorm: bool = True, scale: float = 1.0) -> RouterT:
+    """Builds the moe_router_t struct; ``bias`` is a float32 [E] tensor added
+    to the scores for the choice alone."""
+    return _keep(RouterT(SCORE[score], n_groups, topk_groups, GROUP_SCORE[group_score],
+                         1 if renorm else 0, scale, _ptr(bias)), bias)
+
+
+def _logits_dtype(logits, dtype: Optional[int]) -> int:
+    """The moe_dtype_t of a logits tensor (float32, or bfloat16 also as int16 storage)."""
+    if dtype is not None:
+        return dtype
+    name = str(logits.dtype)
+    if name == "torch.float32":
+        return DT_FP32
+    if name in ("torch.bfloat16", "torch.int16"):
+        return DT_BF16
+    raise TypeError(f"router logits are float32 or bfloat16, not {name}")
 
 
 def _ref(x):
@@ -293,6 +332,66 @@ def moe_dglu_unfused(g, z, grp: GroupsT, I, ep: EpilogueT, dgu, stream=None):
 def moe_mxfp8_quantize(v, R, C, grp: Optional[GroupsT], mx: MxOutT, stream=None):
     _check("moe_mxfp8_quantize",
            _lib.moe_mxfp8_quantize(_ptr(v), R, C, _ref(grp), ctypes.byref(mx), _stream(stream)))
+
+
+def moe_router_topk(logits, T, E, k, r: RouterT, ids, weights, stream=None, logits_dtype=None):
+    """``logits_dtype`` (DT_FP32 or DT_BF16) is taken from the tensor unless given."""
+    _check("moe_router_topk",
+           _lib.moe_router_topk(_ptr(logits), _logits_dtype(logits, logits_dtype), T, E, k,
+                                ctypes.byref(r), _ptr(ids), _ptr(weights), _stream(stream)))
+
+
+def moe_router_topk_bwd(logits, T, E, k, r: RouterT, ids, dweights, dlogits, stream=None,
+                        logits_dtype=None):
+    _check("moe_router_topk_bwd",
+           _lib.moe_router_topk_bwd(_ptr(logits), _logits_dtype(logits, logits_dtype), T, E, k,
+                                    ctypes.byref(r), _ptr(ids), _ptr(dweights), _ptr(dlogits),
+                                    _stream(stream)))
+
+
+def moe_combine(y, M_cap, H, dst, T, k, out, weights=None, residual=None, stream=None):
+    _check("moe_combine",
+           _lib.moe_combine(_ptr(y), M_cap, H, _ptr(dst), _ptr(weights), T, k, _ptr(residual),
+                            _ptr(out), _stream(stream)))
+
+
+def moe_combine_bwd(dout, y, M_cap, H, dst, T, k, weights=None, dy=None, dweights=None, stream=None):
+    _check("moe_combine_bwd",
+           _lib.moe_combine_bwd(_ptr(dout), _ptr(y), M_cap, H, _ptr(dst), _ptr(weights), T, k,
+                                _ptr(dy), _ptr(dweights), _stream(stream)))
+
+
+def moe_add_rmsnorm(x, weight, T, H, eps, residual=None, h=None, y=None, rstd=None,
+                    mx: Optional[MxOutT] = None, stream=None):
+    _check("moe_add_rmsnorm",
+           _lib.moe_add_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), T, H, eps, _ptr(h), _ptr(y),
+                                _ptr(rstd), _ref(mx), _stream(stream)))
+
+
+def moe_add_rmsnorm_bwd_workspace_bytes(T: int, H: int) -> int:
+    return _lib.moe_add_rmsnorm_bwd_workspace_bytes(T, H)
+
+
+def moe_add_rmsnorm_bwd(dy, h, weight, rstd, T, H, dh=None, dx=None, dweight=None,
+                        accumulate: bool = False, workspace=None, stream=None):
+    """``workspace``: a tensor of at least moe_add_rmsnorm_bwd_workspace_bytes(T, H)
+    bytes, needed for ``dweight``."""
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("moe_add_rmsnorm_bwd",
+           _lib.moe_add_rmsnorm_bwd(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dh), T, H,
+                                    _ptr(dx), _ptr(dweight), 1 if accumulate else 0,
+                                    _ptr(workspace), nbytes, _stream(stream)))
+
+
+def moe_mxfp4_quantize(v, R, C, grp: Optional[GroupsT], q, s, stream=None):
+    _check("moe_mxfp4_quantize",
+           _lib.moe_mxfp4_quantize(_ptr(v), R, C, _ref(grp), _ptr(q), _ptr(s), _stream(stream)))
+
+
+def moe_pack_weight_mxfp4(src, E, N, K, src_layout, dst_q, dst_s, stream=None):
+    _check("moe_pack_weight_mxfp4",
+           _lib.moe_pack_weight_mxfp4(_ptr(src), E, N, K, src_layout, _ptr(dst_q), _ptr(dst_s),
+                                      _stream(stream)))
 
 
 def raw_call(name: str, *args) -> int:

@@ -407,6 +407,37 @@ moe_status_t moe_group_gemm_dglu_bwd(const void* dy2, const moe_operand_t* w2, i
   return launch_activation_kernel(kind, a, grid, (hipStream_t)stream);
 }
 
+static moe_status_t group_gemm_mxfp4(const moe_operand_t* a_op, const moe_operand_t* b_op, int N, int K,
+                                     const moe_groups_t* groups, void* c_bf16, const moe_mx_out_t* mx,
+                                     int cu_margin, hipStream_t stream) {
+  const bool a4 = a_op->dtype == MOE_DT_MXFP4;
+  if ((!a4 && a_op->dtype != MOE_DT_MXFP8) || b_op->layout != MOE_B_NK) return MOE_ERR_UNSUPPORTED;
+  if (mx && (mx->row_q || mx->col_q)) return MOE_ERR_UNSUPPORTED;
+  if (!a_op->scales || !b_op->scales || !c_bf16) return MOE_ERR_NULL;
+  if (K % 32 != 0) return MOE_ERR_SHAPE;
+  if (!aligned16(a_op->data) || !aligned16(b_op->data) || !aligned16(c_bf16)) return MOE_ERR_ALIGN;
+  int cus;
+  moe_status_t st = ensure_init(&cus);
+  if (st != MOE_OK) return st;
+  Mx4Args a;
+  memset(&a, 0, sizeof(a));
+  a.A = static_cast<const uint8_t*>(a_op->data);
+  a.a_scales = a_op->scales;
+  a.B = static_cast<const uint8_t*>(b_op->data);
+  a.b_scales = b_op->scales;
+  a.M_cap = groups->M_cap;
+  a.N = N;
+  a.K = K;
+  a.counts = groups->counts;
+  a.E = groups->E;
+  a.offsets_out = groups->offsets_out;
+  a.status_out = groups->status_out;
+  a.C = static_cast<uint16_t*>(c_bf16);
+  int usable = cus - (cu_margin > 0 ? cu_margin : 0);
+  if (usable < 1) usable = 1;
+  return launch_mx4_gemm(a, a4, usable, stream);
+}
+
 moe_status_t moe_group_gemm_quant(const moe_operand_t* a_op, const moe_operand_t* b_op, int N,
                                   int K, const moe_groups_t* groups, void* c_bf16,
                                   const moe_mx_out_t* mx, int cu_margin, void* stream) {
@@ -414,7 +445,10 @@ moe_status_t moe_group_gemm_quant(const moe_operand_t* a_op, const moe_operand_t
   if (st != MOE_OK) return st;
   if (!a_op || !b_op || !a_op->data || !b_op->data) return MOE_ERR_NULL;
   if ((st = check_mx(mx)) != MOE_OK) return st;
-  if (N < 64 || N % 64 != 0 || K < 64 || K % 64 != 0) return MOE_ERR_SHAPE;
+  if (N < 64 || N % 64 != 0 || K < 32) return MOE_ERR_SHAPE;
+  if (b_op->dtype == MOE_DT_MXFP4)   // MXFP4 weights (K % 32 == 0, checked there)
+    return group_gemm_mxfp4(a_op, b_op, N, K, groups, c_bf16, mx, cu_margin, (hipStream_t)stream);
+  if (K < 64 || K % 64 != 0) return MOE_ERR_SHAPE;
   const bool a_e5 = a_op->dtype == MOE_DT_MXFP8_E5M2;
   const bool mx_in = a_op->dtype == MOE_DT_MXFP8 || a_e5 || b_op->dtype != MOE_DT_BF16;
   if (mx_in) {   // MXFP8 (A e4m3 or e5m2) x MXFP8 e4m3 only, weight from moe_pack_weight_mx
@@ -604,6 +638,196 @@ moe_status_t moe_mxfp8_quantize(const void* v, int R, int C, const moe_groups_t*
     }
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+static moe_status_t check_router(const void* logits, int logits_dtype, int T, int E, int k,
+                                 const moe_router_t* r, RouterArgs* out) {
+  if (!logits || !r) return MOE_ERR_NULL;
+  if (T < 0 || T > kMaxRouterTokens || E < 1 || E > kMaxExperts || k < 1 || k > kMaxTopk || k > E)
+    return MOE_ERR_SHAPE;
+  if (logits_dtype != MOE_DT_BF16 && logits_dtype != MOE_DT_FP32) return MOE_ERR_UNSUPPORTED;
+  if ((r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) ||
+      (r->group_score != MOE_GROUP_MAX && r->group_score != MOE_GROUP_TOP2) ||
+      (r->renorm != 0 && r->renorm != 1))
+    return MOE_ERR_UNSUPPORTED;
+  if (r->n_groups < 1 || r->n_groups > kMaxRouterGroups || E % r->n_groups != 0 || r->topk_groups < 1 ||
+      r->topk_groups > r->n_groups || k > r->topk_groups * (E / r->n_groups))
+    return MOE_ERR_SHAPE;
+  const bool top2 = r->n_groups > 1 && r->group_score == MOE_GROUP_TOP2;
+  if ((top2 && E / r->n_groups < 2) || !isfinite(r->scale)) return MOE_ERR_SHAPE;
+  if (!aligned16(logits) || (r->bias && !aligned4(r->bias))) return MOE_ERR_ALIGN;
+  out->logits = logits;
+  out->bias = r->bias;
+  out->T = T;
+  out->E = E;
+  out->k = k;
+  out->sigmoid = r->score == MOE_SCORE_SIGMOID;
+  out->n_groups = r->n_groups;
+  out->topk_groups = r->topk_groups;
+  out->top2 = top2;
+  out->renorm = r->renorm;
+  out->scale = r->scale;
+  return MOE_OK;
+}
+
+moe_status_t moe_router_topk(const void* logits, int logits_dtype, int T, int E, int k,
+                             const moe_router_t* router, int32_t* ids, float* weights, void* stream) {
+  RouterArgs a;
+  moe_status_t st = check_router(logits, logits_dtype, T, E, k, router, &a);
+  if (st != MOE_OK) return st;
+  if (!ids || !weights) return MOE_ERR_NULL;
+  if (!aligned4(ids) || !aligned4(weights)) return MOE_ERR_ALIGN;
+  int cus;
+  if ((st = ensure_init(&cus)) != MOE_OK) return st;
+  return launch_router(a, logits_dtype == MOE_DT_BF16, ids, weights, (hipStream_t)stream);
+}
+
+moe_status_t moe_router_topk_bwd(const void* logits, int logits_dtype, int T, int E, int k,
+                                 const moe_router_t* router, const int32_t* ids, const float* dweights,
+                                 void* dlogits, void* stream) {
+  RouterArgs a;
+  moe_status_t st = check_router(logits, logits_dtype, T, E, k, router, &a);
+  if (st != MOE_OK) return st;
+  if (!ids || !dweights || !dlogits) return MOE_ERR_NULL;
+  if (!aligned4(ids) || !aligned4(dweights) || !aligned16(dlogits)) return MOE_ERR_ALIGN;
+  int cus;
+  if ((st = ensure_init(&cus)) != MOE_OK) return st;
+  return launch_router_bwd(a, logits_dtype == MOE_DT_BF16, ids, dweights, dlogits, (hipStream_t)stream);
+}
+
+static moe_status_t check_combine(int M_cap, int H, const int32_t* dst, int T, int k, const float* weights) {
+  if (!dst) return MOE_ERR_NULL;
+  if (M_cap < 0 || T < 0 || k < 1 || k > kMaxTopk || H < 8 || H % 8 != 0) return MOE_ERR_SHAPE;
+  if (!aligned4(dst) || (weights && !aligned4(weights))) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+moe_status_t moe_combine(const void* y, int M_cap, int H, const int32_t* dst, const float* weights, int T,
+                         int k, const void* residual, void* out, void* stream) {
+  moe_status_t st = check_combine(M_cap, H, dst, T, k, weights);
+  if (st != MOE_OK) return st;
+  if (!y || !out) return MOE_ERR_NULL;
+  if (!aligned16(y) || !aligned16(out) || (residual && !aligned16(residual))) return MOE_ERR_ALIGN;
+  int cus;
+  if ((st = ensure_init(&cus)) != MOE_OK) return st;
+  return launch_combine(static_cast<const uint16_t*>(y), M_cap, H, dst, weights, T, k,
+                        static_cast<const uint16_t*>(residual), static_cast<uint16_t*>(out),
+                        (hipStream_t)stream);
+}
+
+moe_status_t moe_combine_bwd(const void* dout, const void* y, int M_cap, int H, const int32_t* dst,
+                             const float* weights, int T, int k, void* dy, float* dweights, void* stream) {
+  moe_status_t st = check_combine(M_cap, H, dst, T, k, weights);
+  if (st != MOE_OK) return st;
+  if (!dout || (!dy && !dweights) || (dweights && !y)) return MOE_ERR_NULL;
+  if (!aligned16(dout) || (y && !aligned16(y)) || (dy && !aligned16(dy)) ||
+      (dweights && !aligned4(dweights)))
+    return MOE_ERR_ALIGN;
+  if (dy && (dy == dout || dy == y)) return MOE_ERR_UNSUPPORTED;
+  int cus;
+  if ((st = ensure_init(&cus)) != MOE_OK) return st;
+  return launch_combine_bwd(static_cast<const uint16_t*>(dout), static_cast<const uint16_t*>(y), M_cap, H,
+                            dst, weights, T, k, static_cast<uint16_t*>(dy), dweights, (hipStream_t)stream);
+}
+
+moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* weight, int T, int H,
+                             float eps, void* h, void* y, float* rstd, const moe_mx_out_t* mx, void* stream) {
+  if (!x || !weight) return MOE_ERR_NULL;
+  moe_status_t st = check_mx(mx);
+  if (st != MOE_OK) return st;
+  if (mx && mx->col_q) return MOE_ERR_UNSUPPORTED;
+  const bool q = mx && mx->row_q;
+  if (!h && !y && !rstd && !q) return MOE_ERR_NULL;
+  if (T < 0 || H < 8 || H % 8 != 0 || H > kNormMaxH || (q && H % 32 != 0)) return MOE_ERR_SHAPE;
+  if (!(eps >= 0.0f) || !isfinite(eps)) return MOE_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(weight) || (residual && !aligned16(residual)) || (h && !aligned16(h)) ||
+      (y && !aligned16(y)) || (rstd && !aligned4(rstd)))
+    return MOE_ERR_ALIGN;
+  int cus;
+  if ((st = ensure_init(&cus)) != MOE_OK) return st;
+  NormArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = static_cast<const uint16_t*>(x);
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.weight = static_cast<const uint16_t*>(weight);
+  a.T = T;
+  a.H = H;
+  a.eps = eps;
+  a.h = static_cast<uint16_t*>(h);
+  a.y = static_cast<uint16_t*>(y);
+  a.rstd = rstd;
+  a.q = q ? mx->row_q : nullptr;
+  a.s = q ? mx->row_s : nullptr;
+  a.e5 = q ? mx->e5m2 : 0;
+  return launch_add_rmsnorm(a, (hipStream_t)stream);
+}
+
+size_t moe_add_rmsnorm_bwd_workspace_bytes(int T, int H) {
+  if (T <= 0 || H <= 0) return 0;
+  return (size_t)norm_bwd_parts(T) * (size_t)H * sizeof(float);
+}
+
+moe_status_t moe_add_rmsnorm_bwd(const void* dy, const void* h, const void* weight, const float* rstd,
+                                 const void* dh, int T, int H, void* dx, float* dweight, int accumulate,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dy || !h || !weight || !rstd || (!dx && !dweight)) return MOE_ERR_NULL;
+  if (T < 0 || H < 8 || H % 8 != 0 || H > kNormMaxH) return MOE_ERR_SHAPE;
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_UNSUPPORTED;
+  if (dweight && T > 0) {
+    if (!workspace) return MOE_ERR_NULL;
+    if (workspace_bytes < moe_add_rmsnorm_bwd_workspace_bytes(T, H)) return MOE_ERR_SHAPE;
+  }
+  if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned4(rstd) || (dh && !aligned16(dh)) ||
+      (dx && !aligned16(dx)) || (dweight && !aligned4(dweight)) || (workspace && !aligned16(workspace)))
+    return MOE_ERR_ALIGN;
+  int cus;
+  moe_status_t st = ensure_init(&cus);
+  if (st != MOE_OK) return st;
+  NormBwdArgs a;
+  memset(&a, 0, sizeof(a));
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.h = static_cast<const uint16_t*>(h);
+  a.weight = static_cast<const uint16_t*>(weight);
+  a.rstd = rstd;
+  a.dh = static_cast<const uint16_t*>(dh);
+  a.T = T;
+  a.H = H;
+  a.dx = static_cast<uint16_t*>(dx);
+  a.part = dweight ? static_cast<float*>(workspace) : nullptr;
+  return launch_add_rmsnorm_bwd(a, dweight, accumulate, (hipStream_t)stream);
+}
+
+moe_status_t moe_mxfp4_quantize(const void* v, int R, int C, const moe_groups_t* groups, uint8_t* q,
+                                uint8_t* s, void* stream) {
+  if (!v || !q || !s) return MOE_ERR_NULL;
+  moe_status_t st;
+  if (groups && (st = check_groups(groups)) != MOE_OK) return st;
+  if (groups && groups->M_cap != R) return MOE_ERR_SHAPE;
+  if (R < 0 || C < 32 || C % 32 != 0) return MOE_ERR_SHAPE;
+  if (!aligned16(v) || !aligned16(q)) return MOE_ERR_ALIGN;
+  int cus;
+  if ((st = ensure_init(&cus)) != MOE_OK) return st;
+  return launch_mx4_rows(static_cast<const uint16_t*>(v), R, C, groups ? groups->counts : nullptr,
+                         groups ? groups->E : 0, q, s, cus, (hipStream_t)stream);
+}
+
+moe_status_t moe_pack_weight_mxfp4(const void* src, int E, int N, int K, int src_layout, void* dst_q,
+                                   void* dst_s, void* stream) {
+  if (!src || !dst_q || !dst_s) return MOE_ERR_NULL;
+  if (E < 1 || E > 65535 || N < 64 || N % 64 != 0 || K < 32 || K % 32 != 0 || K / 32 > 65535)
+    return MOE_ERR_SHAPE;
+  if ((long long)E * N >= (1LL << 31)) return MOE_ERR_SHAPE;
+  if (src_layout != MOE_B_NK && src_layout != MOE_B_KN) return MOE_ERR_UNSUPPORTED;
+  if (!aligned16(src) || !aligned16(dst_q)) return MOE_ERR_ALIGN;
+  int cus;
+  moe_status_t st = ensure_init(&cus);
+  if (st != MOE_OK) return st;
+  const uint16_t* w = static_cast<const uint16_t*>(src);
+  uint8_t* q = static_cast<uint8_t*>(dst_q);
+  uint8_t* sc = static_cast<uint8_t*>(dst_s);
+  if (src_layout == MOE_B_NK)
+    return launch_mx4_rows(w, E * N, K, nullptr, 0, q, sc, cus, (hipStream_t)stream);
+  return launch_mx4_weight_kn(w, E, N, K, q, sc, (hipStream_t)stream);
 }
 
 }  // extern "C"

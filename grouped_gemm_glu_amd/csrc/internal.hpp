@@ -5,6 +5,7 @@
 
 #include "group_gemm.hpp"
 #include "moe_glu.h"
+#include "operator_args.hpp"
 
 namespace moe {
 
@@ -48,5 +49,27 @@ moe_status_t launch_group_gemm_wgrad(const GemmArgs& args, int grid, hipStream_t
 // the same on K-tiled MXFP8 column copies; a_e5 / b_e5: e5m2 codes
 moe_status_t launch_group_gemm_wgrad_mx(const GemmArgs& args, bool a_e5, bool b_e5, int grid,
                                         hipStream_t stream);
+
+// Router, combine and norm (token_ops.hip); T = 0 launches nothing
+moe_status_t launch_router(const RouterArgs& a, bool bf16, int* ids, float* weights, hipStream_t s);
+moe_status_t launch_router_bwd(const RouterArgs& a, bool bf16, const int* ids, const float* dw,
+                               void* dlogits, hipStream_t s);
+moe_status_t launch_combine(const uint16_t* y, int M_cap, int H, const int* dst, const float* weights,
+                            int T, int k, const uint16_t* residual, uint16_t* out, hipStream_t s);
+moe_status_t launch_combine_bwd(const uint16_t* dout, const uint16_t* y, int M_cap, int H, const int* dst,
+                                const float* weights, int T, int k, uint16_t* dy, float* dweights,
+                                hipStream_t s);
+moe_status_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s);
+// rows of partial dweight sums that the backward writes (its workgroups)
+constexpr int kNormBwdParts = 512;
+int norm_bwd_parts(int T);
+moe_status_t launch_add_rmsnorm_bwd(const NormBwdArgs& a, float* dweight, int accumulate, hipStream_t s);
+
+// MXFP4 (mxfp4.hip); a4: e2m1 rows, else e4m3
+moe_status_t launch_mx4_rows(const uint16_t* v, int R, int C, const int* counts, int E, uint8_t* q,
+                             uint8_t* s, int cus, hipStream_t st);
+moe_status_t launch_mx4_weight_kn(const uint16_t* src, int E, int N, int K, uint8_t* q, uint8_t* s,
+                                  hipStream_t st);
+moe_status_t launch_mx4_gemm(const Mx4Args& a, bool a4, int cus, hipStream_t st);
 
 }  // namespace moe

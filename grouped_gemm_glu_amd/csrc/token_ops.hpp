@@ -1,0 +1,511 @@
+// Kernels over tokens around the expert GEMMs: the router (scores, balance
+// bias, expert groups, top-k, weights) and its gradient, the combine of a
+// token's expert rows and its gradients, and the residual addition +
+// root-mean-square norm with an MXFP8 copy and its gradients.  All but the
+// router read and write each byte once and are bound by memory; the router is
+// bound by the instructions of its selection.
+#pragma once
+
+#include "device_common.hpp"
+#include "operator_args.hpp"
+
+namespace moe {
+
+// ---------------------------------------------------------------- router
+// A value's rank as an unsigned integer: larger means earlier in the order.
+// NaN ranks below every number (1); 0 is kept for what is out of the choice.
+// The two zeros are the same value (v + 0.0 turns -0.0 into +0.0).
+__device__ __forceinline__ unsigned long long rank_key(double v) {
+  const unsigned long long b = __builtin_bit_cast(unsigned long long, v + 0.0);
+  const unsigned long long s = (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+  return v != v ? 1ull : s;
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* p, long long i) {
+  if constexpr (BF16) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
+  else return static_cast<const float*>(p)[i];
+}
+
+// One token per wave, experts lane, lane + 64, ...: k rounds of a wave-wide
+// maximum.  Scores and choice values are kept in 64 bits, so that the choice
+// is the one that the formulas make: in 32 bits the scores of neighbouring
+// logits round to one value and the order is lost.
+template <int VPL, bool BF16>
+__global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restrict__ ids,
+                                                     float* __restrict__ weights) {
+  __shared__ double choice_lds[4][64 * VPL];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const long long tok = (long long)blockIdx.x * 4 + wave;
+  const bool tv = tok < p.T;
+  float x[VPL];
+  float m = -INFINITY;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 64 * i;
+    x[i] = tv && e < p.E ? load_logit<BF16>(p.logits, tok * p.E + e) : -INFINITY;
+    m = fmaxf(m, x[i]);
+    nan = nan || x[i] != x[i];
+  }
+  // softmax: the maximum and the sum over the row (a NaN logit makes the sum
+  // NaN; a row of -inf alone has no softmax, its scores are 0)
+  m = wave_max(m);
+  const bool empty = m == -INFINITY && !__any(nan);
+  double sum = 1.0;
+  if (!p.sigmoid) {
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (lane + 64 * i < p.E) sum += exp((double)x[i] - (double)m);
+    sum = wave_sum(sum);
+  }
+  auto score = [&](float v) -> double {
+    if (p.sigmoid) return 1.0 / (1.0 + exp(-(double)v));
+    return empty ? 0.0 : exp((double)v - (double)m) / sum;
+  };
+  // the choice value: score + bias, or without a bias the logit itself (the
+  // same order without the scores' rounding)
+  const bool by_score = p.bias != nullptr || (p.n_groups > 1 && p.top2);
+  double c[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 64 * i;
+    c[i] = -INFINITY;
+    if (e < p.E) c[i] = by_score ? score(x[i]) + (p.bias ? (double)p.bias[e] : 0.0) : (double)x[i];
+  }
+  unsigned long long open = ~0ull;   // bit g: group g takes part
+  if (p.n_groups > 1) {
+    const int gsz = p.E / p.n_groups;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) choice_lds[wave][lane + 64 * i] = c[i];
+    __syncthreads();
+    unsigned long long key = 0;
+    if (lane < p.n_groups) {
+      double b0 = -INFINITY, b1 = -INFINITY;
+      bool num = false, num2 = false;   // a first and a second number in the group
+      for (int i = 0; i < gsz; ++i) {
+        const double v = choice_lds[wave][lane * gsz + i];
+        if (v != v) continue;
+        num2 = num2 || num;
+        num = true;
+        if (v > b0) { b1 = b0; b0 = v; } else if (v > b1) b1 = v;
+      }
+      if (p.top2) key = num2 ? rank_key(b0 + b1) : 1ull;
+      else key = num ? rank_key(b0) : 1ull;
+    }
+    int before = 0;
+    for (int g = 0; g < p.n_groups; ++g) {
+      const unsigned long long o = __shfl(key, g, 64);
+      before += o > key || (o == key && g < lane);
+    }
+    open = __ballot(lane < p.n_groups && before < p.topk_groups);
+    if (!p.bias && p.top2) {   // without a bias the experts' order is the logits'
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) c[i] = (double)x[i];
+    }
+  }
+  unsigned long long key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 64 * i;
+    const bool in = e < p.E && (p.n_groups == 1 || ((open >> (e / (p.E / p.n_groups))) & 1ull));
+    key[i] = in ? rank_key(c[i]) : 0ull;
+  }
+  int my_id = 0;
+  float my_x = 0.0f;
+  for (int j = 0; j < p.k; ++j) {
+    unsigned long long bk = 0;
+    int be = 0x7FFFFFFF;
+    float bx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (key[i] > bk) { bk = key[i]; be = lane + 64 * i; bx = x[i]; }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      const unsigned long long ok = __shfl_xor(bk, d, 64);
+      const int oe = __shfl_xor(be, d, 64);
+      const float ox = __shfl_xor(bx, d, 64);
+      if (ok > bk || (ok == bk && oe < be)) { bk = ok; be = oe; bx = ox; }
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (lane + 64 * i == be) key[i] = 0;
+    if (lane == j) { my_id = be; my_x = bx; }
+  }
+  double s = lane < p.k ? score(my_x) : 0.0;
+  const double total = p.renorm ? wave_sum(s) : 1.0;
+  if (tv && lane < p.k) {
+    ids[tok * p.k + lane] = my_id;
+    weights[tok * p.k + lane] = total == 0.0 ? 0.0f : (float)((double)p.scale * s / total);
+  }
+}
+
+// d(logits) from d(weights) and the ids that were chosen.  With s the scores,
+// S = sum of the chosen ones (1 without renormalisation) and g = dw scale / S:
+//   ds_j = g_j - renorm (sum_i g_i s_i) / S
+//   sigmoid: dx = ds_j s_j (1 - s_j) at the chosen experts, 0 elsewhere
+//   softmax: dx_e = s_e (ds_e [e chosen] - sum_i ds_i s_i); renormalised
+//   softmax is the softmax over the chosen logits, so only those count.
+// An id outside [0, E) takes no part; an id that stands twice counts twice.
+template <int VPL, bool BF16>
+__global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs p, const int* __restrict__ ids,
+                                                         const float* __restrict__ dw,
+                                                         void* __restrict__ dlogits) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const long long tok = (long long)blockIdx.x * 4 + wave;
+  if (tok >= p.T) return;   // (no barrier below)
+  int id = -1;
+  float xs = 0.0f, g = 0.0f;
+  if (lane < p.k) {
+    id = ids[tok * p.k + lane];
+    g = dw[tok * p.k + lane] * p.scale;
+    if (id < 0 || id >= p.E) id = -1;
+    else xs = load_logit<BF16>(p.logits, tok * p.E + id);
+  }
+  const bool in = id >= 0;
+  float x[VPL];
+  float m = -INFINITY, sum = 1.0f;
+  bool nan = in && xs != xs;
+  const bool full = !p.sigmoid && !p.renorm;   // softmax over the whole row
+  if (full) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane + 64 * i;
+      x[i] = e < p.E ? load_logit<BF16>(p.logits, tok * p.E + e) : -INFINITY;
+      m = fmaxf(m, x[i]);
+      nan = nan || x[i] != x[i];
+    }
+    m = wave_max(m);
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (lane + 64 * i < p.E) sum += expf(x[i] - m);
+    sum = wave_sum(sum);
+  } else if (!p.sigmoid) {
+    m = wave_max(in ? xs : -INFINITY);
+  }
+  float s = 0.0f;
+  if (in) s = p.sigmoid ? 1.0f / (1.0f + expf(-xs)) : expf(xs - m) / sum;
+  const bool empty = !p.sigmoid && m == -INFINITY && !__any(nan);   // no softmax: constant weights
+  if (empty) s = 0.0f;
+  const float S = p.renorm ? wave_sum(s) : 1.0f;
+  const float inv = S == 0.0f ? 0.0f : 1.0f / S;
+  float ds = in ? g * inv : 0.0f;
+  if (p.renorm) ds -= wave_sum(in ? ds * s : 0.0f) * inv;
+  float d = 0.0f, dot = 0.0f;
+  if (in && S != 0.0f && !empty)
+    d = p.sigmoid ? ds * s * (1.0f / (1.0f + expf(xs))) : ds * s;
+  if (full) dot = wave_sum(d);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 64 * i;
+    float v = full && !empty && e < p.E ? -(expf(x[i] - m) / sum) * dot : 0.0f;
+    for (int j = 0; j < p.k; ++j) {
+      const int ej = __shfl(id, j, 64);
+      const float dj = __shfl(d, j, 64);
+      v += ej == e ? dj : 0.0f;
+    }
+    if (e < p.E) {
+      if constexpr (BF16) static_cast<uint16_t*>(dlogits)[tok * p.E + e] = f32_to_bf16(v);
+      else static_cast<float*>(dlogits)[tok * p.E + e] = v;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- combine
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
+// out[t] = residual[t] + sum_j w[t][j] y[dst[t][j]], the terms added in slot
+// order in fp32 and rounded once.  One thread per 8 columns of a token.
+__global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict__ y, int M_cap, int H,
+                                                      const int* __restrict__ dst,
+                                                      const float* __restrict__ weights, int T, int k,
+                                                      const uint16_t* __restrict__ residual,
+                                                      uint16_t* __restrict__ out) {
+  const int ch = blockIdx.y * 256 + threadIdx.x;
+  if (ch * 8 >= H) return;
+  for (long long t = blockIdx.x; t < T; t += gridDim.x) {
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (residual) unpack8(*reinterpret_cast<const uint4*>(residual + t * H + ch * 8), acc);
+    for (int j = 0; j < k; ++j) {
+      const int r = dst[t * k + j];
+      if (r < 0 || r >= M_cap) continue;
+      const float w = weights ? weights[t * k + j] : 1.0f;
+      float v[8];
+      unpack8(*reinterpret_cast<const uint4*>(y + (long long)r * H + ch * 8), v);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) acc[q] = fmaf(w, v[q], acc[q]);
+    }
+    *reinterpret_cast<uint4*>(out + t * H + ch * 8) = pack8(acc);
+  }
+}
+
+// dy[dst[t][j]] = w[t][j] dout[t] and dweights[t][j] = <dout[t], y[dst[t][j]]>.
+// One workgroup per token.  A row that stands twice among a token's slots
+// gets the sum of their weights, written once.
+__global__ __launch_bounds__(256) void combine_bwd_kernel(const uint16_t* __restrict__ dout,
+                                                          const uint16_t* __restrict__ y, int M_cap, int H,
+                                                          const int* __restrict__ dst,
+                                                          const float* __restrict__ weights, int T, int k,
+                                                          uint16_t* __restrict__ dy,
+                                                          float* __restrict__ dweights) {
+  __shared__ int row_s[kMaxTopk];
+  __shared__ float w_s[kMaxTopk];
+  __shared__ float part[4][kMaxTopk];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (long long t = blockIdx.x; t < T; t += gridDim.x) {
+    __syncthreads();
+    if ((int)threadIdx.x < k) {
+      const int j = threadIdx.x;
+      const int r = dst[t * k + j];
+      bool first = true;
+      float w = 0.0f;
+      for (int i = 0; i < k; ++i)
+        if (dst[t * k + i] == r) {
+          if (i < j) first = false;
+          w += weights ? weights[t * k + i] : 1.0f;
+        }
+      row_s[j] = r < 0 || r >= M_cap ? -1 : (first ? r : r | (int)0x80000000);   // top bit: not written
+      w_s[j] = w;
+    }
+    __syncthreads();
+    float dot[kMaxTopk];
+#pragma unroll
+    for (int j = 0; j < kMaxTopk; ++j) dot[j] = 0.0f;
+    for (int ch = threadIdx.x; ch * 8 < H; ch += 256) {
+      float d[8];
+      unpack8(*reinterpret_cast<const uint4*>(dout + t * H + ch * 8), d);
+#pragma unroll
+      for (int j = 0; j < kMaxTopk; ++j) {
+        if (j >= k) break;
+        const int rs = row_s[j];
+        if (rs == -1) continue;
+        const long long at = (long long)(rs & 0x7FFFFFFF) * H + ch * 8;
+        if (dweights) {
+          float v[8];
+          unpack8(*reinterpret_cast<const uint4*>(y + at), v);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) dot[j] = fmaf(d[q], v[q], dot[j]);
+        }
+        if (dy && rs >= 0) {
+          float v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = w_s[j] * d[q];
+          *reinterpret_cast<uint4*>(dy + at) = pack8(v);
+        }
+      }
+    }
+    if (dweights) {
+#pragma unroll
+      for (int j = 0; j < kMaxTopk; ++j) {
+        if (j >= k) break;
+        const float s = wave_sum(dot[j]);
+        if (lane == 0) part[wave][j] = s;
+      }
+      __syncthreads();
+      if ((int)threadIdx.x < k) {
+        const int j = threadIdx.x;
+        dweights[t * k + j] = part[0][j] + part[1][j] + part[2][j] + part[3][j];
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- add + RMS norm
+// Sum over the workgroup's NW waves; every thread gets it.  The partial sums
+// are added in wave order.
+template <int NW>
+__device__ __forceinline__ float block_sum(float v, float* tmp) {
+  v = wave_sum(v);
+  if constexpr (NW == 1) return v;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) s += tmp[w];
+  return s;
+}
+
+// One workgroup of 256 threads per row, NC chunks of 8 columns per thread.
+// h = bf16(x + residual) is what the residual stream keeps and what the norm
+// is taken of, so that the backward pass sees the same values; y is rounded
+// once, and the MXFP8 copy is the rounded y's (as the GEMM epilogues do).
+template <int NC>
+__global__ __launch_bounds__(256) void add_rmsnorm_kernel(NormArgs p) {
+  __shared__ float tmp[4];
+  const int nch = p.H >> 3;
+  for (long long r = blockIdx.x; r < p.T; r += gridDim.x) {
+    float v[NC][8];
+    float sq = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int ch = c * 256 + threadIdx.x;
+      if (ch >= nch) continue;
+      const long long at = r * p.H + ch * 8;
+      unpack8(*reinterpret_cast<const uint4*>(p.x + at), v[c]);
+      if (p.residual) {
+        float w[8];
+        unpack8(*reinterpret_cast<const uint4*>(p.residual + at), w);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[c][q] += w[q];
+        const uint4 hv = pack8(v[c]);
+        if (p.h) *reinterpret_cast<uint4*>(p.h + at) = hv;
+        unpack8(hv, v[c]);
+      } else if (p.h) {
+        *reinterpret_cast<uint4*>(p.h + at) = pack8(v[c]);
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sq = fmaf(v[c][q], v[c][q], sq);
+    }
+    const float rstd = 1.0f / sqrtf(block_sum<4>(sq, tmp) / (float)p.H + p.eps);
+    if (p.rstd && threadIdx.x == 0) p.rstd[r] = rstd;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int ch = c * 256 + threadIdx.x;
+      if (ch >= nch) continue;   // (with p.q a row is whole blocks of 4 lanes)
+      const long long at = r * p.H + ch * 8;
+      float w[8];
+      unpack8(*reinterpret_cast<const uint4*>(p.weight + ch * 8), w);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) w[q] = v[c][q] * rstd * w[q];
+      const uint4 yv = pack8(w);
+      if (p.y) *reinterpret_cast<uint4*>(p.y + at) = yv;
+      if (p.q) {
+        unpack8(yv, w);
+        float amax = 0.0f;
+        int nan = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          amax = fmaxf(amax, fabsf(w[q]));
+          nan |= w[q] != w[q];
+        }
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+          amax = fmaxf(amax, __shfl_xor(amax, d, 64));
+          nan |= __shfl_xor(nan, d, 64);
+        }
+        const int E = nan ? 128 : mx_scale_exponent(amax, p.e5 ? 15 : 8);
+        uint32_t lo = 0x7F7F7F7Fu, hi = 0x7F7F7F7Fu;
+        if (E != 128) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) w[q] = ldexpf(w[q], -E);
+          lo = p.e5 ? e5m2x4(w[0], w[1], w[2], w[3]) : e4m3x4(w[0], w[1], w[2], w[3]);
+          hi = p.e5 ? e5m2x4(w[4], w[5], w[6], w[7]) : e4m3x4(w[4], w[5], w[6], w[7]);
+        }
+        // (row_q may have any alignment)
+        uint8_t* q8 = p.q + at;
+        if ((reinterpret_cast<uintptr_t>(p.q) & 7) == 0) {
+          *reinterpret_cast<uint2*>(q8) = make_uint2(lo, hi);
+        } else {
+          for (int i = 0; i < 4; ++i) {
+            q8[i] = (uint8_t)(lo >> (8 * i));
+            q8[4 + i] = (uint8_t)(hi >> (8 * i));
+          }
+        }
+        if ((threadIdx.x & 3) == 0) p.s[(r * p.H >> 5) + (ch >> 2)] = e8m0_byte(E);
+      }
+    }
+  }
+}
+
+// With n = h rstd and g = dy weight: dx = rstd (g - n mean(g n)) + dh, and
+// dweight = sum over rows of dy n.  Each workgroup takes rows blockIdx.x +
+// i gridDim.x and keeps its columns' share of dweight in registers; the
+// shares are added in a fixed order by the kernel below.
+template <int NC>
+__global__ __launch_bounds__(256) void add_rmsnorm_bwd_kernel(NormBwdArgs p) {
+  __shared__ float tmp[4];
+  const int nch = p.H >> 3;
+  float dwt[NC][8];
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) dwt[c][q] = 0.0f;
+  for (long long r = blockIdx.x; r < p.T; r += gridDim.x) {
+    const float rstd = p.rstd[r];
+    float n[NC][8], g[NC][8];
+    float dot = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int ch = c * 256 + threadIdx.x;
+      if (ch >= nch) continue;
+      const long long at = r * p.H + ch * 8;
+      float w[8];
+      unpack8(*reinterpret_cast<const uint4*>(p.dy + at), g[c]);
+      unpack8(*reinterpret_cast<const uint4*>(p.h + at), n[c]);
+      unpack8(*reinterpret_cast<const uint4*>(p.weight + ch * 8), w);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        n[c][q] *= rstd;
+        dwt[c][q] = fmaf(g[c][q], n[c][q], dwt[c][q]);
+        g[c][q] *= w[q];
+        dot = fmaf(g[c][q], n[c][q], dot);
+      }
+    }
+    if (!p.dx) continue;
+    const float mean = block_sum<4>(dot, tmp) / (float)p.H;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int ch = c * 256 + threadIdx.x;
+      if (ch >= nch) continue;
+      const long long at = r * p.H + ch * 8;
+      float d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (p.dh) unpack8(*reinterpret_cast<const uint4*>(p.dh + at), d);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) d[q] += rstd * (g[c][q] - n[c][q] * mean);
+      *reinterpret_cast<uint4*>(p.dx + at) = pack8(d);
+    }
+  }
+  if (p.part) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int ch = c * 256 + threadIdx.x;
+      if (ch >= nch) continue;
+      float4* o = reinterpret_cast<float4*>(p.part + (long long)blockIdx.x * p.H + ch * 8);
+      o[0] = make_float4(dwt[c][0], dwt[c][1], dwt[c][2], dwt[c][3]);
+      o[1] = make_float4(dwt[c][4], dwt[c][5], dwt[c][6], dwt[c][7]);
+    }
+  }
+}
+
+// dweight[col] (+)= the sum of nparts partial rows, in a fixed order.
+__global__ __launch_bounds__(256) void norm_dweight_kernel(const float* __restrict__ part, int nparts,
+                                                           int H, float* __restrict__ dweight,
+                                                           int accumulate) {
+  const int col = blockIdx.x * 256 + threadIdx.x;
+  if (col >= H) return;
+  float s = accumulate ? dweight[col] : 0.0f;
+  for (int i = 0; i < nparts; ++i) s += part[(long long)i * H + col];
+  dweight[col] = s;
+}
+
+}  // namespace moe

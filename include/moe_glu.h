@@ -153,8 +153,12 @@ typedef struct {
 typedef enum {
   MOE_DT_BF16 = 0,
   MOE_DT_MXFP8 = 1,         /* e4m3fn bytes + E8M0 scales, 32-blocks along K */
-  MOE_DT_MXFP8_E5M2 = 2     /* e5m2 bytes + E8M0 scales (a gradient, e.g. dgu for dX); the A operand
+  MOE_DT_MXFP8_E5M2 = 2,    /* e5m2 bytes + E8M0 scales (a gradient, e.g. dgu for dX); the A operand
                                of moe_group_gemm_quant, either operand of moe_group_gemm_wgrad_mx */
+  MOE_DT_MXFP4 = 3,         /* e2m1 codes, two per byte (the lower nibble first), + E8M0 scales,
+                               32-blocks along K: see moe_mxfp4_quantize; either operand of
+                               moe_group_gemm_quant */
+  MOE_DT_FP32 = 4           /* logits of the router; no GEMM operand */
 } moe_dtype_t;
 
 typedef enum {
@@ -168,8 +172,9 @@ typedef struct {
   int32_t dtype;            /* moe_dtype_t */
   int32_t layout;           /* A: ignored (always [M_cap][K] row-major); B: moe_b_layout_t */
   const void* data;         /* bf16 or e4m3 elements */
-  const uint8_t* scales;    /* MXFP8 only: A [M_cap][K/32] E8M0 (block b of row r covers K
-                               values 32b..32b+31); B from moe_pack_weight_mx */
+  const uint8_t* scales;    /* MXFP8 and MXFP4: A [M_cap][K/32] E8M0 (block b of row r covers K
+                               values 32b..32b+31); MXFP8 B from moe_pack_weight_mx; MXFP4 B
+                               [E][N][K/32] */
 } moe_operand_t;
 
 /* Reads the device's compute-unit count once; call before graph capture.
@@ -340,7 +345,17 @@ moe_status_t moe_group_gemm_dglu_bwd(const void* dy2, const moe_operand_t* w2, i
  *     out_e = sum_k (q_a * 2^(s_a - 127)) (q_b * 2^(s_b - 127))
  * accumulated in fp32 by the block-scaled MFMA.  Mixed bf16 / MXFP8 inputs
  * are MOE_ERR_UNSUPPORTED.  Requires K % 64 == 0 (K % 128 == 0 for MXFP8),
- * N % 64 == 0. */
+ * N % 64 == 0.
+ * MXFP4 weights (4-bit floating point, the weight format of GPT-OSS-like
+ * models): B = e2m1 codes [E][N][K/2] in the plain MOE_B_NK layout (K
+ * contiguous, the layout such checkpoints hold) with E8M0 scales [E][N][K/32],
+ * e.g. from moe_pack_weight_mxfp4; A = e2m1 codes [M_cap][K/2] (MOE_DT_MXFP4,
+ * moe_mxfp4_quantize) or e4m3fn codes [M_cap][K] (MOE_DT_MXFP8), with scales
+ * [M_cap][K/32]: the same sum over the codes' values.  A scale byte 0xFF (NaN)
+ * makes every product with its block NaN.  c_bf16 is required, MXFP8 outputs
+ * are MOE_ERR_UNSUPPORTED.  Requires K % 32 == 0, N % 64 == 0; codes and c
+ * 16-byte aligned, scales any.  The call takes any group sizes, from one row
+ * per expert (decoding, where it streams the active experts' weights once) up. */
 moe_status_t moe_group_gemm_quant(const moe_operand_t* a, const moe_operand_t* b, int N, int K,
                                   const moe_groups_t* groups, void* c_bf16,
                                   const moe_mx_out_t* mx, int cu_margin, void* stream);
@@ -413,6 +428,132 @@ moe_status_t moe_dglu_unfused(const void* g, const void* z, const moe_groups_t* 
  * MOE_B_NK expects.  Requires C % 32 == 0. */
 moe_status_t moe_mxfp8_quantize(const void* v, int R, int C, const moe_groups_t* groups,
                                 const moe_mx_out_t* mx, void* stream);
+
+/* Router ([MEGA] §2.1: scores p = Softmax(W_r x), the k best experts of each
+ * token, and their scores as the weights of the expert outputs).  From a
+ * token's logits x [E]:
+ *   s_e = softmax(x)_e or sigmoid(x_e)                       the scores
+ *   c_e = s_e + bias_e                                       the choice values
+ * bias is a balance term for the choice alone (an offset that training moves
+ * up for underused experts): the weights are the scores without it.  Without a
+ * bias the experts are ordered by their logits, which is the same order.
+ * n_groups > 1: the experts form n_groups groups of E / n_groups consecutive
+ * ids; a group's value is its best choice value (MOE_GROUP_MAX) or the sum of
+ * its two best (MOE_GROUP_TOP2; without a bias of its two best scores), and
+ * only the topk_groups best groups take part.  The k largest choice values
+ * are taken, in that order; ties go to the lower id, of groups too, and the
+ * choice is made in 64 bits.  With S = the sum of the chosen scores (renorm =
+ * 1) or 1 (renorm = 0):
+ *   w_j = scale * s_j / S
+ * NaN logits (and choice values) rank below every number; a NaN logit makes
+ * the softmax of its row NaN.  Where S is 0, or every logit of a softmax row
+ * is -inf, the weights are 0.  (host struct) */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score_t;
+typedef struct {
+  int32_t score;            /* moe_score_t */
+  int32_t n_groups;         /* 1 .. 64, divides E; 1 = no groups */
+  int32_t topk_groups;      /* 1 .. n_groups */
+  int32_t group_score;      /* moe_group_score_t */
+  int32_t renorm;           /* 1: weights divided by their sum */
+  float scale;              /* finite; multiplies the weights */
+  const float* bias;        /* nullable device fp32 [E] */
+} moe_router_t;
+
+/* ids [T][k] int32 and weights [T][k] fp32 from logits [T][E] (fp32:
+ * MOE_DT_FP32, or MOE_DT_BF16).  The ids feed moe_route_group (as topk_ids),
+ * the weights moe_combine (or, grouped, the epilogue's row_scale).  Requires
+ * 1 <= k <= 16, k <= E <= 1024, k <= topk_groups * E / n_groups (groups of at
+ * least 2 experts for MOE_GROUP_TOP2), T <= 2^25; logits 16-byte, ids, weights
+ * and bias 4-byte aligned.  T = 0 does nothing. */
+moe_status_t moe_router_topk(const void* logits, int logits_dtype, int T, int E, int k,
+                             const moe_router_t* router, int32_t* ids, float* weights, void* stream);
+
+/* Gradient of the router's weights: dlogits [T][E] (the logits' type) from
+ * dweights [T][k] fp32, for the ids that moe_router_topk chose from the same
+ * logits (the choice itself and the bias have no gradient).  Every entry of
+ * dlogits is written.  Ids outside [0, E) take no part; an id that stands
+ * twice in a token counts twice.  Where the weights are 0 by the rule above,
+ * so is the gradient.  A renormalised softmax is the softmax over the chosen
+ * logits and reads only those.  dlogits 16-byte aligned, else as above;
+ * dlogits must not overlap the logits. */
+moe_status_t moe_router_topk_bwd(const void* logits, int logits_dtype, int T, int E, int k,
+                                 const moe_router_t* router, const int32_t* ids, const float* dweights,
+                                 void* dlogits, void* stream);
+
+/* Combine ([MEGA] §2.1: y = E_shared(x) + sum_j p_j E_j(x)): a token's expert
+ * rows back to the token,
+ *   out[t] = residual[t] + sum_{j < k} weights[t][j] y[dst[t][j]]
+ * added in slot order in fp32 and rounded once to bf16.  y: bf16 [M_cap][H]
+ * grouped rows (FC2's output), dst [T][k] from moe_route_group (a pair whose
+ * dst lies outside [0, M_cap) adds nothing: preset dst to -1 if ids may be
+ * dropped), weights fp32 [T][k] (NULL: all 1, which makes this call the
+ * gradient of the row gather), residual bf16 [T][H] (NULL: none; the shared
+ * expert's output or the residual stream), out bf16 [T][H], which may be the
+ * residual itself but not overlap y.  Requires H % 8 == 0, 1 <= k <= 16; y,
+ * residual and out 16-byte, dst and weights 4-byte aligned. */
+moe_status_t moe_combine(const void* y, int M_cap, int H, const int32_t* dst, const float* weights, int T,
+                         int k, const void* residual, void* out, void* stream);
+
+/* Gradients of moe_combine (the residual's is dout itself):
+ *   dy[dst[t][j]] = bf16(weights[t][j] dout[t])      bf16 [M_cap][H], nullable
+ *   dweights[t][j] = sum_h dout[t][h] y[dst[t][j]][h]  fp32 [T][k], nullable
+ * with 0 in dweights for a pair without a row.  Rows of dy that no pair names
+ * are not written.  A row belongs to one token (as moe_route_group's do); if
+ * two slots of a token name it, it gets the sum of their gradients.  y is
+ * needed for dweights only.  dy must not overlap dout or y. */
+moe_status_t moe_combine_bwd(const void* dout, const void* y, int M_cap, int H, const int32_t* dst,
+                             const float* weights, int T, int k, void* dy, float* dweights, void* stream);
+
+/* Residual addition + root-mean-square norm, the pass in front of the expert
+ * MLP, with the MXFP8 rows that its GEMMs read:
+ *   h = bf16(x + residual)                 residual NULL: h = x
+ *   rstd = 1 / sqrt(mean(h^2) + eps)       per row, fp32
+ *   y = bf16(h * rstd * weight)
+ *   mx: row-wise MXFP8 copy of y (mx->row_q, row_s; byte-identical to
+ *       moe_mxfp8_quantize of y; the transposed copy is MOE_ERR_UNSUPPORTED)
+ * x, residual, h, y: bf16 [T][H]; weight bf16 [H]; rstd fp32 [T].  Each output
+ * may be NULL, one is required.  h may be x or residual itself.  Requires
+ * H % 8 == 0, 8 <= H <= 16384 (H % 32 == 0 with mx), eps >= 0. */
+moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* weight, int T, int H,
+                             float eps, void* h, void* y, float* rstd, const moe_mx_out_t* mx, void* stream);
+
+/* Its gradients from dy (bf16 [T][H]), the saved h and rstd, and dh (bf16
+ * [T][H], nullable: the gradient that reaches h past the norm).  With n = h
+ * rstd and g = dy weight:
+ *   dx = bf16(rstd (g - n mean(g n)) + dh)   bf16 [T][H], nullable: the
+ *                                            gradient of x and of residual
+ *   dweight = sum_t dy n                     fp32 [H], nullable; accumulate = 1
+ *                                            adds to it
+ * dweight needs the workspace (moe_add_rmsnorm_bwd_workspace_bytes(T, H)
+ * bytes, 16-byte aligned, contents of no meaning before or after; calls that
+ * may run at the same time, replays of captured ones too, need one each); its
+ * sums are added in a fixed order.  dx may be dh itself, not dy or h. */
+size_t moe_add_rmsnorm_bwd_workspace_bytes(int T, int H);
+moe_status_t moe_add_rmsnorm_bwd(const void* dy, const void* h, const void* weight, const float* rstd,
+                                 const void* dh, int T, int H, void* dx, float* dweight, int accumulate,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* MXFP4 quantisation of a bf16 [R][C] matrix along its rows (OCP MX: blocks
+ * of 32 values, one E8M0 scale X = 2^E, E the smallest integer with amax/X <=
+ * 6, the largest e2m1 value, as moe_mx_out_t's rule has it for 448; elements
+ * e2m1(v / X), round-to-nearest-even):
+ *   q [R][C/2]: value c of a row in byte c / 2, the lower nibble for even c
+ *   s [R][C/32] E8M0
+ * A block holding a NaN or an infinity gets scale 0xFF (NaN) and zero codes.
+ * With groups (M_cap = R) only the routed rows are read and written.  Requires
+ * C % 32 == 0; v and q 16-byte aligned. */
+moe_status_t moe_mxfp4_quantize(const void* v, int R, int C, const moe_groups_t* groups, uint8_t* q,
+                                uint8_t* s, void* stream);
+
+/* Offline MXFP4 quantisation of a bf16 weight along its reduction dimension
+ * K, into the plain MOE_B_NK layout that moe_group_gemm_quant reads: dst_q
+ * [E][N][K/2], dst_s [E][N][K/32].  src_layout MOE_B_NK: src is [E][N][K];
+ * MOE_B_KN: src is [E][K][N] (FC1's plain W1 [E][H][2I]: N = 2I, K = H; FC2's
+ * W2 [E][I][H]: N = H, K = I).  Requires N % 64 == 0, K % 32 == 0, E <= 65535,
+ * E * N < 2^31. */
+moe_status_t moe_pack_weight_mxfp4(const void* src, int E, int N, int K, int src_layout, void* dst_q,
+                                   void* dst_s, void* stream);
 
 #ifdef __cplusplus
 }
