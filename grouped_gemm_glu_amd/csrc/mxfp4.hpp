@@ -2,7 +2,7 @@
 // quantisation and their grouped product on the block-scaled MFMA.
 #pragma once
 
-#include "device_common.hpp"
+#include "group_gemm.hpp"
 #include "operator_args.hpp"
 
 namespace moe {
@@ -184,6 +184,330 @@ __global__ __launch_bounds__(256) void mx4_gemm_small_kernel(Mx4Args p) {
             make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
       }
     }
+  }
+}
+
+// ---------------------------------------------------------------- tiles
+// Row and m-tile prefixes of the device counts for tiles of BM rows: the part
+// of GroupScan that these kernels need, at half its LDS.
+struct RowScan {
+  int row_off[kMaxExperts + 1];
+  int tile_off[kMaxExperts + 1];
+  long long wave_tmp[16];
+};
+
+// As build_group_scan: counts are clamped (a negative one to 0, rows past
+// M_cap dropped); the writer workgroup stores the offsets and status bits.
+template <int NT, int BM>
+__device__ void build_row_scan(RowScan& rs, const int* __restrict__ counts, int E, int M_cap,
+                               int* offsets_out, int* status_out, bool writer) {
+  const int t = threadIdx.x;
+  constexpr int PER = (kMaxExperts + NT - 1) / NT;
+  int c[PER];
+  long long sum = 0;
+  int neg = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = t * PER + i;
+    c[i] = e < E ? counts[e] : 0;
+    if (c[i] < 0) { neg = 1; c[i] = 0; }
+    sum += c[i];
+  }
+  const long long incl = block_incl_scan<NT, long long>(sum, rs.wave_tmp);
+  long long run = incl - sum;
+  int tiles = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = t * PER + i;
+    const long long o0 = run < M_cap ? run : M_cap;
+    run += c[i];
+    const long long o1 = run < M_cap ? run : M_cap;
+    if (e < E) rs.row_off[e] = (int)o0;
+    c[i] = ((int)(o1 - o0) + BM - 1) / BM;
+    tiles += c[i];
+  }
+  if (t == NT - 1) rs.row_off[E] = run < M_cap ? (int)run : M_cap;   // (threads past E add nothing)
+  const bool over = run > M_cap;
+  int trun = block_incl_scan<NT, int>(tiles, rs.wave_tmp) - tiles;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = t * PER + i;
+    if (e < E) rs.tile_off[e] = trun;
+    trun += c[i];
+  }
+  if (t == NT - 1) rs.tile_off[E] = trun;
+  const int st = __syncthreads_or((neg ? 1 : 0) | (over ? 2 : 0));
+  if (writer) {
+    if (offsets_out)
+      for (int e = t; e <= E; e += NT) offsets_out[e] = rs.row_off[e];
+    if (status_out && t == 0 && st) atomicOr(status_out, st);
+  }
+}
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// The 16 bytes of an e2m1 fragment as an operand of the f8f6f4 MFMA, whose
+// other 16 bytes the 4-bit format does not read.
+__device__ __forceinline__ i32x8 mx4_frag(i32x4 v) {
+  return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
+}
+
+constexpr int MX4_BM = 256, MX4_BN = 256;
+
+// Tile column (weight row) that row rho of a staged 32-row block holds.  The 32
+// x 32 MFMA leaves lane half h with rows 8 a + 4 h .. + 3, a = 0 .. 3: dealt out
+// in fours like this, half h holds 8 consecutive columns over a = 0, 1 and 8
+// over a = 2, 3, each 16 bytes of bf16.
+__device__ __forceinline__ int mx4_col(int rho) {
+  return (rho & ~31) + 16 * ((rho >> 4) & 1) + 8 * ((rho >> 2) & 1) + 4 * ((rho >> 3) & 1) + (rho & 3);
+}
+
+// v_permlane16_swap: in each half of the wave, lanes 16..31 of x change places
+// with lanes 0..15 of y.
+__device__ __forceinline__ void swap16(uint32_t& x, uint32_t& y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+  x = r[0];
+  y = r[1];
+}
+
+// Grouped product of e2m1 rows and e2m1 weights on 256 x 256 tiles: 8 waves in
+// a 4 x 2 grid of 64 x 128, v_mfma_scale_f32_32x32x64_f8f6f4.  A K-tile is 256
+// values, 128 bytes of each row, staged by LDS-DMA in two stages (swz_off
+// layout: the fragment reads are free of bank conflicts); the barrier that frees
+// a stage sits before the last of a K-tile's four k-steps, whose fragments are
+// in registers, as in group_gemm_kernel.  A block of 32 values is one 16-byte
+// chunk, so a K that ends inside a K-tile masks whole chunks: their DMA is sent
+// out of the descriptor's range and reads zeros, their scales are set to 1.
+// Scales go through registers (their rows, K / 32 bytes long, have any
+// alignment): thread t fetches the 8 of row t % 256 of A or B and stores the
+// even ones and the odd ones as a dword each, lane half h's scales of the four
+// k-steps.
+__global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
+  // Four arrays (A and B of the two stages), so that the compiler can tell the
+  // DMA of one stage from the reads of the other.
+  __shared__ __attribute__((aligned(16))) uint8_t a0[32768], a1[32768], b0[32768], b1[32768];
+  __shared__ __attribute__((aligned(16))) uint32_t sc0[1024], sc1[1024];
+  __shared__ RowScan gs;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  build_row_scan<512, MX4_BM>(gs, p.counts, p.E, p.M_cap, p.offsets_out, p.status_out, blockIdx.x == 0);
+  const int NT = (p.N + MX4_BN - 1) / MX4_BN;
+  const int nblk = p.K >> 5;              // blocks of 32 values
+  const int nk = (nblk + 7) >> 3;         // K-tiles
+  const uint32_t ld = (uint32_t)p.K >> 1; // bytes per row of A and of B
+  const long long total = (long long)gs.tile_off[p.E] * NT;
+  const int P = gridDim.x;
+  // workgroups are dealt to the 8 XCDs in turn: each XCD gets a run of tiles
+  const int slot = (P % 8 == 0) ? ((blockIdx.x & 7) * (P >> 3) + (blockIdx.x >> 3)) : blockIdx.x;
+  for (long long tile = slot; tile < total; tile += P) {
+    int lo = 0, hi = p.E;   // the last e with tile_off[e] * NT <= tile
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((long long)gs.tile_off[mid] * NT <= tile) lo = mid; else hi = mid;
+    }
+    const int e = lo;
+    const int local = (int)(tile - (long long)gs.tile_off[e] * NT);
+    const int MT = gs.tile_off[e + 1] - gs.tile_off[e];
+    // blocks of 4 m-tiles x 8 n-tiles, m fastest: the run of tiles that an
+    // XCD works on together shares few panels of either operand
+    constexpr int BHT = 4, BWT = 8;
+    const int band = local / (BHT * NT);
+    const int bh = min(BHT, MT - band * BHT);
+    const int l2 = local - band * BHT * NT;
+    const int nb = l2 / (bh * BWT);
+    const int l3 = l2 - nb * bh * BWT;
+    const int mt = band * BHT + l3 % bh, nt = nb * BWT + l3 / bh;
+    const int row0 = gs.row_off[e] + mt * MX4_BM;
+    const int rows = min(MX4_BM, gs.row_off[e + 1] - row0);
+    const int n0 = nt * MX4_BN, cols = min(MX4_BN, p.N - n0);
+    const long long brow0 = (long long)e * p.N + n0;
+
+    auto tile_body = [&](auto mic) {
+      constexpr int MI = decltype(mic)::value;      // 32-row blocks per wave: 2, or 1 for up to 128 rows
+      constexpr int NJA = 2 * MI;                   // A DMA pieces (8 rows each) per wave
+      const int lane_t = lane + opaque_zero();
+      const rsrc_t rsA = make_rsrc(p.A + (long long)row0 * ld, (long long)rows * ld);
+      const rsrc_t rsB = make_rsrc(p.B + brow0 * ld, (long long)cols * ld);
+      // DMA piece: 8 LDS rows; lane (rl, pc) lands on row rl, physical chunk
+      // pc, and fetches logical chunk pc ^ key of its row.  Both parts of the
+      // address are linear in the piece's row and the lane's: mx4_col(8 x + y) =
+      // mx4_col(8 x) + mx4_col(y) for y < 8.
+      const int rl = lane_t >> 3, ck = (lane_t & 7) ^ rl;
+      const uint32_t la = (uint32_t)rl * ld, lb = (uint32_t)mx4_col(rl) * ld;
+      auto dma = [&](const rsrc_t& rs, uint8_t* base, int piece, uint32_t lrow, int urow, int kt) {
+        const int c = ck ^ swz_hi(piece & 3);
+        const uint32_t off = lrow + (uint32_t)(c * 16) + ((uint32_t)urow * ld + (uint32_t)(kt * 128));
+        lds_dma16(rs, base + piece * 1024, c < nblk - 8 * kt ? off : 0xFFFFFFF0u, 0);
+      };
+      auto dmaA = [&](int kt, uint8_t* st, int j) {
+        const int piece = wave * NJA + j;
+        dma(rsA, st, piece, la, piece * 8, kt);
+      };
+      auto dmaB = [&](int kt, uint8_t* st, int j) {
+        const int piece = wave * 4 + j;
+        dma(rsB, st, piece, lb, mx4_col(piece * 8), kt);
+      };
+      // scales of K-tile kt: row tid % 256 of A (threads 0..255) or B.  Loads
+      // stay inside the row: the last K-tile's 8 bytes end with the row and are
+      // shifted down; rows and K-tiles past the end load what is there and
+      // drop it.  No branch: with one in the loop the compiler sinks a k-step's
+      // MFMAs below it and spills the fragments.  The bytes are worked on when
+      // they are stored, a K-tile after their load.
+      const int srow = tid & 255;
+      const bool isA = tid < 256;
+      const bool s_in = isA ? srow < rows : mx4_col(srow) < cols;
+      const uint8_t* sp = (isA ? p.a_scales : p.b_scales) +
+                          ((isA ? row0 : brow0) + (!s_in ? 0 : isA ? srow : mx4_col(srow))) * (long long)nblk;
+      unsigned long long sv = 0;
+      auto scale_load = [&](int kt) { __builtin_memcpy(&sv, sp + min(8 * kt, nblk - 8), 8); };
+      auto scale_load_short = [&]() {   // a row of less than 8 blocks: its bytes at the end of the 8
+        sv = 0;
+        for (int i = 0; i < nblk; ++i) sv |= (unsigned long long)sp[i] << (8 * (8 - nblk + i));
+      };
+      auto scale_store = [&](uint32_t* sc, int kt) {
+        const int past = max(0, min(8 * kt + 8 - nblk, 7));   // blocks past the end of K: 1 (byte 127)
+        const unsigned long long v = (sv >> (8 * past)) | ((0x7F7F7F7F7F7F7F7Full << 1) << (63 - 8 * past));
+        const uint32_t lo4 = s_in ? (uint32_t)v : 0x7F7F7F7Fu, hi4 = s_in ? (uint32_t)(v >> 32) : 0x7F7F7F7Fu;
+        *reinterpret_cast<uint2*>(sc + tid * 2) = make_uint2(__builtin_amdgcn_perm(hi4, lo4, 0x06040200u),
+                                                             __builtin_amdgcn_perm(hi4, lo4, 0x07050301u));
+      };
+      const int h = lane_t >> 5;
+      const int ra = wm * 32 * MI + (lane_t & 31), rb = wn * 128 + (lane_t & 31);
+      auto rdA = [&](const uint8_t* st, int ks, int i) {
+        return *reinterpret_cast<const i32x4*>(st + swz_off(ra + 32 * i, 2 * ks + h));
+      };
+      auto rdB = [&](const uint8_t* st, int ks, int j) {
+        return *reinterpret_cast<const i32x4*>(st + swz_off(rb + 32 * j, 2 * ks + h));
+      };
+      auto rdSA = [&](const uint32_t* sc, int i) { return (int)sc[(ra + 32 * i) * 2 + h]; };
+      auto rdSB = [&](const uint32_t* sc, int j) { return (int)sc[(256 + rb + 32 * j) * 2 + h]; };
+      f32x16 acc[MI][4];
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+      i32x4 aF[2][MI], bF[4];
+      int sA[2][MI], sB[2][4];
+      // one k-step, B block j outer: fragment j is dead after its MI MFMAs and
+      // is read again for the next k-step at once; the next A fragments go
+      // into the other buffer.  KS: this k-step of its K-tile; SS: the K-tile's
+      // scale set.  The last k-step reads the next K-tile's fragments and
+      // scales, and issues the DMA of the K-tile after that, two per block.
+      auto kstep = [&](auto ksc, auto ssc, auto dmac, const uint8_t* na, const uint8_t* nbt, const uint32_t* nsc,
+                       int dkt, uint8_t* da, uint8_t* db) {
+        constexpr int KS = decltype(ksc)::value, SS = decltype(ssc)::value, NK = (KS + 1) & 3;
+        constexpr bool DMA = decltype(dmac)::value;
+        static_for<4>([&](auto jc) {
+          constexpr int j = decltype(jc)::value;
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (j < MI) aF[(KS + 1) & 1][j] = rdA(na, NK, j);
+          if constexpr (KS == 3) {
+            if constexpr (j < MI) sA[SS ^ 1][j] = rdSA(nsc, j);
+            sB[SS ^ 1][j] = rdSB(nsc, j);
+          }
+          if constexpr (DMA) {
+            if constexpr (j < MI) {
+              dmaA(dkt, da, 2 * j);
+              dmaA(dkt, da, 2 * j + 1);
+            } else if constexpr (j < MI + 2) {
+              dmaB(dkt, db, 2 * (j - MI));
+              dmaB(dkt, db, 2 * (j - MI) + 1);
+            }
+          }
+          static_for<MI>([&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                mx4_frag(bF[j]), mx4_frag(aF[KS & 1][i]), acc[i][j], 4, 4, KS, sB[SS][j], KS, sA[SS][i]);
+          });
+          bF[j] = rdB(nbt, NK, j);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      auto issue = [&](int kt, uint8_t* da, uint8_t* db) {
+#pragma unroll
+        for (int j = 0; j < NJA; ++j) dmaA(kt, da, j);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dmaB(kt, db, j);
+      };
+      // K-tile kt (in the other stage) has landed, its scales are stored, and
+      // every wave's reads of this stage are done
+      auto stage_barrier = [&](uint32_t* sc, int kt) {
+        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+        scale_store(sc, kt);
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        __syncthreads();
+      };
+      using I0 = std::integral_constant<int, 0>;
+      using I1 = std::integral_constant<int, 1>;
+      using I2 = std::integral_constant<int, 2>;
+      using I3 = std::integral_constant<int, 3>;
+      using No = std::false_type;
+      using Yes = std::true_type;
+      // k-steps 0 .. 2 of the K-tile in (a, b)
+      auto first_steps = [&](auto ssc, const uint8_t* a, const uint8_t* b) {
+        kstep(I0{}, ssc, No{}, a, b, nullptr, 0, nullptr, nullptr);
+        kstep(I1{}, ssc, No{}, a, b, nullptr, 0, nullptr, nullptr);
+        kstep(I2{}, ssc, No{}, a, b, nullptr, 0, nullptr, nullptr);
+      };
+      __syncthreads();            // the previous tile's reads are done
+      issue(0, a0, b0);
+      if (nblk >= 8) scale_load(0);
+      else scale_load_short();
+      stage_barrier(sc0, 0);
+      issue(1, a1, b1);
+      if (nk > 1) scale_load(1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) { aF[0][i] = rdA(a0, 0, i); sA[0][i] = rdSA(sc0, i); }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) { bF[j] = rdB(b0, 0, j); sB[0][j] = rdSB(sc0, j); }
+      const int nk2 = nk & ~1;
+      for (int kt = 0; kt < nk2; kt += 2) {
+        first_steps(I0{}, a0, b0);
+        stage_barrier(sc1, kt + 1);
+        scale_load(kt + 2);
+        kstep(I3{}, I0{}, Yes{}, a1, b1, sc1, kt + 2, a0, b0);
+        first_steps(I1{}, a1, b1);
+        stage_barrier(sc0, kt + 2);
+        scale_load(kt + 3);
+        kstep(I3{}, I1{}, Yes{}, a0, b0, sc0, kt + 3, a1, b1);
+      }
+      if (nk & 1) {
+        first_steps(I0{}, a0, b0);
+        kstep(I3{}, I0{}, No{}, a0, b0, sc0, 0, nullptr, nullptr);
+      }
+      // (the DMA past the end, zeros, must land before the next tile's)
+      __builtin_amdgcn_s_waitcnt(0x0F70);
+      // lane (r, h) holds, of row r, columns 8 h .. + 7 of the first and of the
+      // second 16 of each 32; the swap gives lanes r and r + 16 the two halves
+      // of one row, so that a store covers 64 bytes of each of 16 rows
+      const int z = opaque_zero(), le = lane + z;
+      const int er = le & 15, eo = 16 * ((le >> 4) & 1) + 8 * (le >> 5);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int m = wm * 32 * MI + 32 * i + er;
+        uint16_t* crow = p.C + (long long)(row0 + m) * p.N + n0 + eo;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int n = wn * 128 + 32 * j;
+          uint32_t w[8];
+#pragma unroll
+          for (int d = 0; d < 8; ++d) w[d] = pack_bf16x2(acc[i][j][2 * d], acc[i][j][2 * d + 1]);
+#pragma unroll
+          for (int d = 0; d < 4; ++d) swap16(w[d], w[4 + d]);
+          if (n < cols) {
+            if (m < rows) *reinterpret_cast<uint4*>(crow + n) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (m + 16 < rows)
+              *reinterpret_cast<uint4*>(crow + 16LL * p.N + n) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+      }
+    };
+    if (rows > 128) tile_body(std::integral_constant<int, 2>{});
+    else tile_body(std::integral_constant<int, 1>{});
   }
 }
 
