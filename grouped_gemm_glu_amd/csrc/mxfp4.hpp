@@ -270,23 +270,33 @@ __device__ __forceinline__ void swap16(uint32_t& x, uint32_t& y) {
   y = r[1];
 }
 
-// Grouped product of e2m1 rows and e2m1 weights on 256 x 256 tiles: 8 waves in
-// a 4 x 2 grid of 64 x 128, v_mfma_scale_f32_32x32x64_f8f6f4.  A K-tile is 256
-// values, 128 bytes of each row, staged by LDS-DMA in two stages (swz_off
-// layout: the fragment reads are free of bank conflicts); the barrier that frees
-// a stage sits before the last of a K-tile's four k-steps, whose fragments are
-// in registers, as in group_gemm_kernel.  A block of 32 values is one 16-byte
-// chunk, so a K that ends inside a K-tile masks whole chunks: their DMA is sent
-// out of the descriptor's range and reads zeros, their scales are set to 1.
-// Scales go through registers (their rows, K / 32 bytes long, have any
-// alignment): thread t fetches the 8 of row t % 256 of A or B and stores the
-// even ones and the odd ones as a dword each, lane half h's scales of the four
-// k-steps.
+// Staged weight rows of 64 bytes (4 chunks, 8-bit rows): row r's chunk c sits at
+// c ^ (r / 4) % 4.  A 32 x 32 read's pass (16 lanes that agree in the chunk and
+// in the parity of row bits 2..4) then takes each of the 16 bank groups once.
+__device__ __forceinline__ int mx4_off64(int r, int c) { return r * 64 + ((c ^ ((r >> 2) & 3)) << 4); }
+
+// Grouped product of e2m1 (A4) or e4m3 rows and e2m1 weights on 256 x 256
+// tiles: 8 waves in a 4 x 2 grid of 64 x 128,
+// v_mfma_scale_f32_32x32x64_f8f6f4.  A K-tile is 128 bytes of each row of A, 256
+// e2m1 or 128 e4m3 values, and as many of B, staged by LDS-DMA in two stages
+// (the fragment reads are free of bank conflicts); the barrier that frees a
+// stage sits before the last of a K-tile's k-steps (of 64 values), whose
+// fragments are in registers, as in group_gemm_kernel.  A block of 32 values is
+// one 16-byte chunk of e2m1 codes or two of e4m3, so a K that ends inside a
+// K-tile masks whole chunks: their DMA is sent out of the descriptor's range
+// and reads zeros, their scales are set to 1.  Scales go through registers
+// (their rows, K / 32 bytes long, have any alignment): thread t fetches those
+// of row t % 256 of A or B and stores the even blocks' and the odd blocks' in a
+// run each: lane half h's scales of the k-steps.
+template <bool A4>
 __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
   // Four arrays (A and B of the two stages), so that the compiler can tell the
   // DMA of one stage from the reads of the other.
-  __shared__ __attribute__((aligned(16))) uint8_t a0[32768], a1[32768], b0[32768], b1[32768];
-  __shared__ __attribute__((aligned(16))) uint32_t sc0[1024], sc1[1024];
+  constexpr int KB = A4 ? 8 : 4;          // blocks of 32 values per K-tile
+  constexpr int KSN = KB / 2;             // k-steps per K-tile
+  constexpr int NJB = A4 ? 4 : 2;         // B DMA pieces (1 KB) per wave
+  __shared__ __attribute__((aligned(16))) uint8_t a0[32768], a1[32768], b0[8192 * NJB], b1[8192 * NJB];
+  __shared__ __attribute__((aligned(16))) uint8_t sc0[512 * KB], sc1[512 * KB];
   __shared__ RowScan gs;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -294,8 +304,8 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
   build_row_scan<512, MX4_BM>(gs, p.counts, p.E, p.M_cap, p.offsets_out, p.status_out, blockIdx.x == 0);
   const int NT = (p.N + MX4_BN - 1) / MX4_BN;
   const int nblk = p.K >> 5;              // blocks of 32 values
-  const int nk = (nblk + 7) >> 3;         // K-tiles
-  const uint32_t ld = (uint32_t)p.K >> 1; // bytes per row of A and of B
+  const int nk = (nblk + KB - 1) / KB;    // K-tiles
+  const uint32_t lda = A4 ? (uint32_t)p.K >> 1 : (uint32_t)p.K, ldb = (uint32_t)p.K >> 1;   // bytes per row
   const long long total = (long long)gs.tile_off[p.E] * NT;
   const int P = gridDim.x;
   // workgroups are dealt to the 8 XCDs in turn: each XCD gets a run of tiles
@@ -327,26 +337,30 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
       constexpr int MI = decltype(mic)::value;      // 32-row blocks per wave: 2, or 1 for up to 128 rows
       constexpr int NJA = 2 * MI;                   // A DMA pieces (8 rows each) per wave
       const int lane_t = lane + opaque_zero();
-      const rsrc_t rsA = make_rsrc(p.A + (long long)row0 * ld, (long long)rows * ld);
-      const rsrc_t rsB = make_rsrc(p.B + brow0 * ld, (long long)cols * ld);
-      // DMA piece: 8 LDS rows; lane (rl, pc) lands on row rl, physical chunk
-      // pc, and fetches logical chunk pc ^ key of its row.  Both parts of the
-      // address are linear in the piece's row and the lane's: mx4_col(8 x + y) =
-      // mx4_col(8 x) + mx4_col(y) for y < 8.
+      const rsrc_t rsA = make_rsrc(p.A + (long long)row0 * lda, (long long)rows * lda);
+      const rsrc_t rsB = make_rsrc(p.B + brow0 * ldb, (long long)cols * ldb);
+      // DMA piece: 1 KB of LDS, 8 rows of 128 bytes (or 16 of 64); lane (rl,
+      // pc) lands on row rl, physical chunk pc, and fetches logical chunk pc ^
+      // key of its row.  The address is linear in the piece's row and the
+      // lane's: mx4_col(8 x + y) = mx4_col(8 x) + mx4_col(y) for y < 8 (and so
+      // with 16).
       const int rl = lane_t >> 3, ck = (lane_t & 7) ^ rl;
-      const uint32_t la = (uint32_t)rl * ld, lb = (uint32_t)mx4_col(rl) * ld;
-      auto dma = [&](const rsrc_t& rs, uint8_t* base, int piece, uint32_t lrow, int urow, int kt) {
-        const int c = ck ^ swz_hi(piece & 3);
-        const uint32_t off = lrow + (uint32_t)(c * 16) + ((uint32_t)urow * ld + (uint32_t)(kt * 128));
-        lds_dma16(rs, base + piece * 1024, c < nblk - 8 * kt ? off : 0xFFFFFFF0u, 0);
-      };
+      const uint32_t la = (uint32_t)rl * lda;
+      const uint32_t lb = (uint32_t)mx4_col(A4 ? rl : lane_t >> 2) * ldb;
+      const int ckb = (lane_t & 3) ^ ((lane_t >> 4) & 3);   // 64-byte rows: key (row / 4) % 4
       auto dmaA = [&](int kt, uint8_t* st, int j) {
         const int piece = wave * NJA + j;
-        dma(rsA, st, piece, la, piece * 8, kt);
+        const int c = ck ^ swz_hi(piece & 3);
+        const uint32_t off = la + (uint32_t)(c * 16) + ((uint32_t)(piece * 8) * lda + (uint32_t)(kt * 128));
+        const int left = (nblk - KB * kt) * (A4 ? 1 : 2);     // chunks of the row that are left
+        lds_dma16(rsA, st + piece * 1024, c < left ? off : 0xFFFFFFF0u, 0);
       };
       auto dmaB = [&](int kt, uint8_t* st, int j) {
-        const int piece = wave * 4 + j;
-        dma(rsB, st, piece, lb, mx4_col(piece * 8), kt);
+        const int piece = wave * NJB + j;
+        const int c = A4 ? ck ^ swz_hi(piece & 3) : ckb;
+        const int urow = mx4_col(piece * (A4 ? 8 : 16));
+        const uint32_t off = lb + (uint32_t)(c * 16) + ((uint32_t)urow * ldb + (uint32_t)(kt * (A4 ? 128 : 64)));
+        lds_dma16(rsB, st + piece * 1024, c < nblk - KB * kt ? off : 0xFFFFFFF0u, 0);
       };
       // scales of K-tile kt: row tid % 256 of A (threads 0..255) or B.  Loads
       // stay inside the row: the last K-tile's 8 bytes end with the row and are
@@ -359,29 +373,47 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
       const bool s_in = isA ? srow < rows : mx4_col(srow) < cols;
       const uint8_t* sp = (isA ? p.a_scales : p.b_scales) +
                           ((isA ? row0 : brow0) + (!s_in ? 0 : isA ? srow : mx4_col(srow))) * (long long)nblk;
-      unsigned long long sv = 0;
-      auto scale_load = [&](int kt) { __builtin_memcpy(&sv, sp + min(8 * kt, nblk - 8), 8); };
-      auto scale_load_short = [&]() {   // a row of less than 8 blocks: its bytes at the end of the 8
+      using sv_t = std::conditional_t<A4, unsigned long long, uint32_t>;   // a row's KB scale bytes
+      sv_t sv = 0;
+      auto scale_load = [&](int kt) { __builtin_memcpy(&sv, sp + min(KB * kt, nblk - KB), KB); };
+      auto scale_load_short = [&]() {   // a row of less than KB blocks: its bytes at the end
         sv = 0;
-        for (int i = 0; i < nblk; ++i) sv |= (unsigned long long)sp[i] << (8 * (8 - nblk + i));
+        for (int i = 0; i < nblk; ++i) sv |= (sv_t)sp[i] << (8 * (KB - nblk + i));
       };
-      auto scale_store = [&](uint32_t* sc, int kt) {
-        const int past = max(0, min(8 * kt + 8 - nblk, 7));   // blocks past the end of K: 1 (byte 127)
-        const unsigned long long v = (sv >> (8 * past)) | ((0x7F7F7F7F7F7F7F7Full << 1) << (63 - 8 * past));
-        const uint32_t lo4 = s_in ? (uint32_t)v : 0x7F7F7F7Fu, hi4 = s_in ? (uint32_t)(v >> 32) : 0x7F7F7F7Fu;
-        *reinterpret_cast<uint2*>(sc + tid * 2) = make_uint2(__builtin_amdgcn_perm(hi4, lo4, 0x06040200u),
-                                                             __builtin_amdgcn_perm(hi4, lo4, 0x07050301u));
+      auto scale_store = [&](uint8_t* sc, int kt) {
+        const int past = max(0, min(KB * kt + KB - nblk, KB - 1));   // blocks past the end of K: 1 (byte 127)
+        const sv_t ones = (sv_t)0x7F7F7F7F7F7F7F7Full;
+        sv_t v = (sv_t)(sv >> (8 * past)) | (sv_t)((sv_t)(ones << 1) << (8 * KB - 1 - 8 * past));
+        v = s_in ? v : ones;
+        if constexpr (A4) {
+          const uint32_t lo4 = (uint32_t)v, hi4 = (uint32_t)(v >> 32);
+          *reinterpret_cast<uint2*>(sc + tid * 8) = make_uint2(__builtin_amdgcn_perm(hi4, lo4, 0x06040200u),
+                                                               __builtin_amdgcn_perm(hi4, lo4, 0x07050301u));
+        } else {
+          *reinterpret_cast<uint32_t*>(sc + tid * 4) = __builtin_amdgcn_perm((uint32_t)v, (uint32_t)v, 0x03010200u);
+        }
       };
       const int h = lane_t >> 5;
       const int ra = wm * 32 * MI + (lane_t & 31), rb = wn * 128 + (lane_t & 31);
-      auto rdA = [&](const uint8_t* st, int ks, int i) {
-        return *reinterpret_cast<const i32x4*>(st + swz_off(ra + 32 * i, 2 * ks + h));
+      using fragA = std::conditional_t<A4, i32x4, i32x8>;
+      auto rdA = [&](const uint8_t* st, int ks, int i) -> fragA {
+        if constexpr (A4) {
+          return *reinterpret_cast<const i32x4*>(st + swz_off(ra + 32 * i, 2 * ks + h));
+        } else {   // bytes 16 h .. + 15 of each of the k-step's two blocks
+          const i32x4 lo4 = *reinterpret_cast<const i32x4*>(st + swz_off(ra + 32 * i, 4 * ks + h));
+          const i32x4 hi4 = *reinterpret_cast<const i32x4*>(st + swz_off(ra + 32 * i, 4 * ks + 2 + h));
+          return __builtin_shufflevector(lo4, hi4, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
       };
       auto rdB = [&](const uint8_t* st, int ks, int j) {
-        return *reinterpret_cast<const i32x4*>(st + swz_off(rb + 32 * j, 2 * ks + h));
+        return *reinterpret_cast<const i32x4*>(
+            st + (A4 ? swz_off(rb + 32 * j, 2 * ks + h) : mx4_off64(rb + 32 * j, 2 * ks + h)));
       };
-      auto rdSA = [&](const uint32_t* sc, int i) { return (int)sc[(ra + 32 * i) * 2 + h]; };
-      auto rdSB = [&](const uint32_t* sc, int j) { return (int)sc[(256 + rb + 32 * j) * 2 + h]; };
+      using sw_t = std::conditional_t<A4, uint32_t, uint16_t>;   // a lane half's scales of a K-tile
+      auto rdSA = [&](const uint8_t* sc, int i) { return (int)reinterpret_cast<const sw_t*>(sc)[(ra + 32 * i) * 2 + h]; };
+      auto rdSB = [&](const uint8_t* sc, int j) {
+        return (int)reinterpret_cast<const sw_t*>(sc)[(256 + rb + 32 * j) * 2 + h];
+      };
       f32x16 acc[MI][4];
 #pragma unroll
       for (int i = 0; i < MI; ++i)
@@ -389,22 +421,27 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-      i32x4 aF[2][MI], bF[4];
+      fragA aF[2][MI];
+      i32x4 bF[4];
       int sA[2][MI], sB[2][4];
+      auto operandA = [](const fragA& f) {
+        if constexpr (A4) return mx4_frag(f);
+        else return f;
+      };
       // one k-step, B block j outer: fragment j is dead after its MI MFMAs and
       // is read again for the next k-step at once; the next A fragments go
       // into the other buffer.  KS: this k-step of its K-tile; SS: the K-tile's
       // scale set.  The last k-step reads the next K-tile's fragments and
       // scales, and issues the DMA of the K-tile after that, two per block.
-      auto kstep = [&](auto ksc, auto ssc, auto dmac, const uint8_t* na, const uint8_t* nbt, const uint32_t* nsc,
+      auto kstep = [&](auto ksc, auto ssc, auto dmac, const uint8_t* na, const uint8_t* nbt, const uint8_t* nsc,
                        int dkt, uint8_t* da, uint8_t* db) {
-        constexpr int KS = decltype(ksc)::value, SS = decltype(ssc)::value, NK = (KS + 1) & 3;
+        constexpr int KS = decltype(ksc)::value, SS = decltype(ssc)::value, NK = (KS + 1) % KSN;
         constexpr bool DMA = decltype(dmac)::value;
         static_for<4>([&](auto jc) {
           constexpr int j = decltype(jc)::value;
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (j < MI) aF[(KS + 1) & 1][j] = rdA(na, NK, j);
-          if constexpr (KS == 3) {
+          if constexpr (KS == KSN - 1) {
             if constexpr (j < MI) sA[SS ^ 1][j] = rdSA(nsc, j);
             sB[SS ^ 1][j] = rdSB(nsc, j);
           }
@@ -413,14 +450,14 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
               dmaA(dkt, da, 2 * j);
               dmaA(dkt, da, 2 * j + 1);
             } else if constexpr (j < MI + 2) {
-              dmaB(dkt, db, 2 * (j - MI));
-              dmaB(dkt, db, 2 * (j - MI) + 1);
+              dmaB(dkt, db, NJB / 2 * (j - MI));
+              if constexpr (A4) dmaB(dkt, db, 2 * (j - MI) + 1);
             }
           }
           static_for<MI>([&](auto ic) {
             constexpr int i = decltype(ic)::value;
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                mx4_frag(bF[j]), mx4_frag(aF[KS & 1][i]), acc[i][j], 4, 4, KS, sB[SS][j], KS, sA[SS][i]);
+                mx4_frag(bF[j]), operandA(aF[KS & 1][i]), acc[i][j], 4, A4 ? 4 : 0, KS, sB[SS][j], KS, sA[SS][i]);
           });
           bF[j] = rdB(nbt, NK, j);
         });
@@ -430,11 +467,11 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
 #pragma unroll
         for (int j = 0; j < NJA; ++j) dmaA(kt, da, j);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dmaB(kt, db, j);
+        for (int j = 0; j < NJB; ++j) dmaB(kt, db, j);
       };
       // K-tile kt (in the other stage) has landed, its scales are stored, and
       // every wave's reads of this stage are done
-      auto stage_barrier = [&](uint32_t* sc, int kt) {
+      auto stage_barrier = [&](uint8_t* sc, int kt) {
         __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
         scale_store(sc, kt);
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
@@ -442,19 +479,16 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
       };
       using I0 = std::integral_constant<int, 0>;
       using I1 = std::integral_constant<int, 1>;
-      using I2 = std::integral_constant<int, 2>;
-      using I3 = std::integral_constant<int, 3>;
+      using IL = std::integral_constant<int, KSN - 1>;
       using No = std::false_type;
       using Yes = std::true_type;
-      // k-steps 0 .. 2 of the K-tile in (a, b)
+      // all but the last k-step of the K-tile in (a, b)
       auto first_steps = [&](auto ssc, const uint8_t* a, const uint8_t* b) {
-        kstep(I0{}, ssc, No{}, a, b, nullptr, 0, nullptr, nullptr);
-        kstep(I1{}, ssc, No{}, a, b, nullptr, 0, nullptr, nullptr);
-        kstep(I2{}, ssc, No{}, a, b, nullptr, 0, nullptr, nullptr);
+        static_for<KSN - 1>([&](auto ks) { kstep(ks, ssc, No{}, a, b, nullptr, 0, nullptr, nullptr); });
       };
       __syncthreads();            // the previous tile's reads are done
       issue(0, a0, b0);
-      if (nblk >= 8) scale_load(0);
+      if (nblk >= KB) scale_load(0);
       else scale_load_short();
       stage_barrier(sc0, 0);
       issue(1, a1, b1);
@@ -469,15 +503,15 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
         first_steps(I0{}, a0, b0);
         stage_barrier(sc1, kt + 1);
         scale_load(kt + 2);
-        kstep(I3{}, I0{}, Yes{}, a1, b1, sc1, kt + 2, a0, b0);
+        kstep(IL{}, I0{}, Yes{}, a1, b1, sc1, kt + 2, a0, b0);
         first_steps(I1{}, a1, b1);
         stage_barrier(sc0, kt + 2);
         scale_load(kt + 3);
-        kstep(I3{}, I1{}, Yes{}, a0, b0, sc0, kt + 3, a1, b1);
+        kstep(IL{}, I1{}, Yes{}, a0, b0, sc0, kt + 3, a1, b1);
       }
       if (nk & 1) {
         first_steps(I0{}, a0, b0);
-        kstep(I3{}, I0{}, No{}, a0, b0, sc0, 0, nullptr, nullptr);
+        kstep(IL{}, I0{}, No{}, a0, b0, sc0, 0, nullptr, nullptr);
       }
       // (the DMA past the end, zeros, must land before the next tile's)
       __builtin_amdgcn_s_waitcnt(0x0F70);
