@@ -287,14 +287,18 @@ __device__ __forceinline__ int mx4_off64(int r, int c) { return r * 64 + ((c ^ (
 // and reads zeros, their scales are set to 1.  Scales go through registers
 // (their rows, K / 32 bytes long, have any alignment): thread t fetches those
 // of row t % 256 of A or B and stores the even blocks' and the odd blocks' in a
-// run each: lane half h's scales of the k-steps.
+// run each: lane half h's scales of the k-steps.  (K >= 32 KB: a row has at
+// least one K-tile's scales.)
+// The stream of K-tiles runs on over the tiles: the last pair of a tile fetches
+// the first pair of the workgroup's next one, and the epilogue works from
+// registers alone, so that its stores and the next tile's first loads overlap.
 template <bool A4>
 __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
   // Four arrays (A and B of the two stages), so that the compiler can tell the
   // DMA of one stage from the reads of the other.
   constexpr int KB = A4 ? 8 : 4;          // blocks of 32 values per K-tile
   constexpr int KSN = KB / 2;             // k-steps per K-tile
-  constexpr int NJB = A4 ? 4 : 2;         // B DMA pieces (1 KB) per wave
+  constexpr int NJB = A4 ? 4 : 2;         // B DMA pieces (1 KB) per wave; A: 4
   __shared__ __attribute__((aligned(16))) uint8_t a0[32768], a1[32768], b0[8192 * NJB], b1[8192 * NJB];
   __shared__ __attribute__((aligned(16))) uint8_t sc0[512 * KB], sc1[512 * KB];
   __shared__ RowScan gs;
@@ -303,22 +307,34 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
   const int wm = wave >> 1, wn = wave & 1;
   build_row_scan<512, MX4_BM>(gs, p.counts, p.E, p.M_cap, p.offsets_out, p.status_out, blockIdx.x == 0);
   const int NT = (p.N + MX4_BN - 1) / MX4_BN;
-  const int nblk = p.K >> 5;              // blocks of 32 values
-  const int nk = (nblk + KB - 1) / KB;    // K-tiles
+  const int nblk = p.K >> 5;                          // blocks of 32 values
+  const int nk = ((nblk + KB - 1) / KB + 1) & ~1;     // K-tiles, in pairs (an odd one out is a masked one)
   const uint32_t lda = A4 ? (uint32_t)p.K >> 1 : (uint32_t)p.K, ldb = (uint32_t)p.K >> 1;   // bytes per row
-  const long long total = (long long)gs.tile_off[p.E] * NT;
+  const int ntiles = __builtin_amdgcn_readfirstlane(gs.tile_off[p.E]);
+  const long long total = (long long)ntiles * NT;
   const int P = gridDim.x;
   // workgroups are dealt to the 8 XCDs in turn: each XCD gets a run of tiles
   const int slot = (P % 8 == 0) ? ((blockIdx.x & 7) * (P >> 3) + (blockIdx.x >> 3)) : blockIdx.x;
-  for (long long tile = slot; tile < total; tile += P) {
+
+  // (carried from tile to tile in vector registers, whatever the compiler may
+  // know: scalars again where they are used, see uniform)
+  struct Tile { int e, row0, rows, n0; };
+  auto uniform = [](const Tile& t) {
+    Tile u;
+    u.e = __builtin_amdgcn_readfirstlane(t.e);
+    u.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+    u.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    u.n0 = __builtin_amdgcn_readfirstlane(t.n0);
+    return u;
+  };
+  auto decode = [&](long long tile) {
     int lo = 0, hi = p.E;   // the last e with tile_off[e] * NT <= tile
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if ((long long)gs.tile_off[mid] * NT <= tile) lo = mid; else hi = mid;
     }
-    const int e = lo;
-    const int local = (int)(tile - (long long)gs.tile_off[e] * NT);
-    const int MT = gs.tile_off[e + 1] - gs.tile_off[e];
+    const int t_off = gs.tile_off[lo], MT = gs.tile_off[lo + 1] - t_off;
+    const int local = (int)(tile - (long long)t_off * NT);
     // blocks of 4 m-tiles x 8 n-tiles, m fastest: the run of tiles that an
     // XCD works on together shares few panels of either operand
     constexpr int BHT = 4, BWT = 8;
@@ -328,71 +344,123 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
     const int nb = l2 / (bh * BWT);
     const int l3 = l2 - nb * bh * BWT;
     const int mt = band * BHT + l3 % bh, nt = nb * BWT + l3 / bh;
-    const int row0 = gs.row_off[e] + mt * MX4_BM;
-    const int rows = min(MX4_BM, gs.row_off[e + 1] - row0);
-    const int n0 = nt * MX4_BN, cols = min(MX4_BN, p.N - n0);
-    const long long brow0 = (long long)e * p.N + n0;
+    Tile t;
+    t.e = lo;
+    t.row0 = gs.row_off[lo] + mt * MX4_BM;
+    t.rows = min(MX4_BM, gs.row_off[lo + 1] - t.row0);
+    t.n0 = nt * MX4_BN;
+    return t;
+  };
+
+  // ---- the fetching side: the operands of one tile
+  const int srow = tid & 255;
+  const bool isA = wave < 4;
+  struct Fetch { rsrc_t A, B; const uint8_t* sp; int s_off; };
+  auto fetch_of = [&](const Tile& t, bool any) {
+    const int cols = min(MX4_BN, p.N - t.n0);
+    const long long brow0 = (long long)t.e * p.N + t.n0;
+    Fetch f;
+    f.A = make_rsrc(p.A + (long long)t.row0 * lda, any ? (long long)t.rows * lda : 0);
+    f.B = make_rsrc(p.B + brow0 * ldb, any ? (long long)cols * ldb : 0);
+    // (rows and columns past the end take the last one's scales: what they
+    // scale is not stored)
+    f.sp = isA ? p.a_scales + (long long)t.row0 * nblk : p.b_scales + brow0 * nblk;
+    f.s_off = (isA ? min(srow, t.rows - 1) : min(mx4_col(srow), cols - 1)) * nblk;
+    return f;
+  };
+  // DMA piece: 1 KB of LDS, 8 rows of 128 bytes (or 16 of 64); lane (rl, pc)
+  // lands on row rl, physical chunk pc, and fetches logical chunk pc ^ key of
+  // its row.  The address is linear in the piece's row and the lane's: mx4_col(8
+  // x + y) = mx4_col(8 x) + mx4_col(y) for y < 8 (and so with 16).  The lane's
+  // part is derived anew for each K-tile (opaque zero): registers are what the
+  // main loop is short of.
+  struct LanePart { uint32_t la, lb; int ck, ckb; };
+  auto lane_part = [&]() {
+    const int l = lane + opaque_zero(), rl = l >> 3;
+    LanePart d;
+    d.la = (uint32_t)rl * lda;
+    d.lb = (uint32_t)mx4_col(A4 ? rl : l >> 2) * ldb;
+    d.ck = (l & 7) ^ rl;
+    d.ckb = (l & 3) ^ ((l >> 4) & 3);     // 64-byte rows: key (row / 4) % 4
+    return d;
+  };
+  auto dmaA = [&](const LanePart& d, const Fetch& f, int kt, uint8_t* st, int j) {
+    const int piece = wave * 4 + j;
+    const int c = d.ck ^ swz_hi(piece & 3);
+    const uint32_t off = d.la + (uint32_t)(c * 16) + ((uint32_t)(piece * 8) * lda + (uint32_t)(kt * 128));
+    const int left = (nblk - KB * kt) * (A4 ? 1 : 2);     // chunks of the row that are left
+    lds_dma16(f.A, st + piece * 1024, c < left ? off : 0xFFFFFFF0u, 0);
+  };
+  auto dmaB = [&](const LanePart& d, const Fetch& f, int kt, uint8_t* st, int j) {
+    const int piece = wave * NJB + j;
+    const int c = A4 ? d.ck ^ swz_hi(piece & 3) : d.ckb;
+    const int urow = mx4_col(piece * (A4 ? 8 : 16));
+    const uint32_t off = d.lb + (uint32_t)(c * 16) + ((uint32_t)urow * ldb + (uint32_t)(kt * (A4 ? 128 : 64)));
+    lds_dma16(f.B, st + piece * 1024, c < nblk - KB * kt ? off : 0xFFFFFFF0u, 0);
+  };
+  auto issue = [&](const Fetch& f, int kt, uint8_t* da, uint8_t* db) {
+    const LanePart d = lane_part();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dmaA(d, f, kt, da, j);
+#pragma unroll
+    for (int j = 0; j < NJB; ++j) dmaB(d, f, kt, db, j);
+  };
+  // scales of K-tile kt of row srow.  Loads stay inside the row: the last
+  // K-tile's bytes end with the row and are shifted down; a masked K-tile's
+  // load is dropped.  No branch: with one in the main loop the compiler sinks a
+  // k-step's MFMAs below it and spills the fragments.  The bytes are worked on
+  // when they are stored, a K-tile after their load.
+  using sv_t = std::conditional_t<A4, unsigned long long, uint32_t>;   // a row's KB scale bytes
+  sv_t sv = 0;
+  auto scale_load = [&](const Fetch& f, int kt) {
+    __builtin_memcpy(&sv, f.sp + (f.s_off + min(KB * kt, nblk - KB)), KB);
+  };
+  auto scale_store = [&](uint8_t* sc, int kt) {
+    const int past = max(0, min(KB * kt + KB - nblk, KB - 1));   // blocks past the end of K: 1 (byte 127)
+    const sv_t ones = (sv_t)0x7F7F7F7F7F7F7F7Full;
+    sv_t v = (sv_t)(sv >> (8 * past)) | (sv_t)((sv_t)(ones << 1) << (8 * KB - 1 - 8 * past));
+    v = KB * kt < nblk ? v : ones;
+    if constexpr (A4) {
+      const uint32_t lo4 = (uint32_t)v, hi4 = (uint32_t)(v >> 32);
+      *reinterpret_cast<uint2*>(sc + tid * 8) = make_uint2(__builtin_amdgcn_perm(hi4, lo4, 0x06040200u),
+                                                           __builtin_amdgcn_perm(hi4, lo4, 0x07050301u));
+    } else {
+      *reinterpret_cast<uint32_t*>(sc + tid * 4) = __builtin_amdgcn_perm((uint32_t)v, (uint32_t)v, 0x03010200u);
+    }
+  };
+  // the K-tile in the other stage has landed, its scales are stored, and every
+  // wave's reads of this stage are done
+  auto stage_barrier = [&](uint8_t* sc, int kt) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+    scale_store(sc, kt);
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+    __syncthreads();
+  };
+
+  long long tile = slot;
+  if (tile >= total) return;   // (the whole workgroup)
+  Tile cur_ = decode(tile);
+  {
+    const Fetch f = fetch_of(uniform(cur_), true);
+    issue(f, 0, a0, b0);
+    scale_load(f, 0);
+    stage_barrier(sc0, 0);
+    issue(f, 1, a1, b1);
+    scale_load(f, 1);
+  }
+
+  for (;;) {
+    // K-tile 0 of the tile is in (a0, b0, sc0); K-tile 1 is on its way to (a1,
+    // b1) and its scales to sv
+    const long long ntile = tile + P;
+    const bool more = ntile < total;
+    Tile nxt_ = cur_;
+    if (more) nxt_ = decode(ntile);
+    const Tile cur = uniform(cur_), nxt = uniform(nxt_);
 
     auto tile_body = [&](auto mic) {
       constexpr int MI = decltype(mic)::value;      // 32-row blocks per wave: 2, or 1 for up to 128 rows
-      constexpr int NJA = 2 * MI;                   // A DMA pieces (8 rows each) per wave
       const int lane_t = lane + opaque_zero();
-      const rsrc_t rsA = make_rsrc(p.A + (long long)row0 * lda, (long long)rows * lda);
-      const rsrc_t rsB = make_rsrc(p.B + brow0 * ldb, (long long)cols * ldb);
-      // DMA piece: 1 KB of LDS, 8 rows of 128 bytes (or 16 of 64); lane (rl,
-      // pc) lands on row rl, physical chunk pc, and fetches logical chunk pc ^
-      // key of its row.  The address is linear in the piece's row and the
-      // lane's: mx4_col(8 x + y) = mx4_col(8 x) + mx4_col(y) for y < 8 (and so
-      // with 16).
-      const int rl = lane_t >> 3, ck = (lane_t & 7) ^ rl;
-      const uint32_t la = (uint32_t)rl * lda;
-      const uint32_t lb = (uint32_t)mx4_col(A4 ? rl : lane_t >> 2) * ldb;
-      const int ckb = (lane_t & 3) ^ ((lane_t >> 4) & 3);   // 64-byte rows: key (row / 4) % 4
-      auto dmaA = [&](int kt, uint8_t* st, int j) {
-        const int piece = wave * NJA + j;
-        const int c = ck ^ swz_hi(piece & 3);
-        const uint32_t off = la + (uint32_t)(c * 16) + ((uint32_t)(piece * 8) * lda + (uint32_t)(kt * 128));
-        const int left = (nblk - KB * kt) * (A4 ? 1 : 2);     // chunks of the row that are left
-        lds_dma16(rsA, st + piece * 1024, c < left ? off : 0xFFFFFFF0u, 0);
-      };
-      auto dmaB = [&](int kt, uint8_t* st, int j) {
-        const int piece = wave * NJB + j;
-        const int c = A4 ? ck ^ swz_hi(piece & 3) : ckb;
-        const int urow = mx4_col(piece * (A4 ? 8 : 16));
-        const uint32_t off = lb + (uint32_t)(c * 16) + ((uint32_t)urow * ldb + (uint32_t)(kt * (A4 ? 128 : 64)));
-        lds_dma16(rsB, st + piece * 1024, c < nblk - KB * kt ? off : 0xFFFFFFF0u, 0);
-      };
-      // scales of K-tile kt: row tid % 256 of A (threads 0..255) or B.  Loads
-      // stay inside the row: the last K-tile's 8 bytes end with the row and are
-      // shifted down; rows and K-tiles past the end load what is there and
-      // drop it.  No branch: with one in the loop the compiler sinks a k-step's
-      // MFMAs below it and spills the fragments.  The bytes are worked on when
-      // they are stored, a K-tile after their load.
-      const int srow = tid & 255;
-      const bool isA = tid < 256;
-      const bool s_in = isA ? srow < rows : mx4_col(srow) < cols;
-      const uint8_t* sp = (isA ? p.a_scales : p.b_scales) +
-                          ((isA ? row0 : brow0) + (!s_in ? 0 : isA ? srow : mx4_col(srow))) * (long long)nblk;
-      using sv_t = std::conditional_t<A4, unsigned long long, uint32_t>;   // a row's KB scale bytes
-      sv_t sv = 0;
-      auto scale_load = [&](int kt) { __builtin_memcpy(&sv, sp + min(KB * kt, nblk - KB), KB); };
-      auto scale_load_short = [&]() {   // a row of less than KB blocks: its bytes at the end
-        sv = 0;
-        for (int i = 0; i < nblk; ++i) sv |= (sv_t)sp[i] << (8 * (KB - nblk + i));
-      };
-      auto scale_store = [&](uint8_t* sc, int kt) {
-        const int past = max(0, min(KB * kt + KB - nblk, KB - 1));   // blocks past the end of K: 1 (byte 127)
-        const sv_t ones = (sv_t)0x7F7F7F7F7F7F7F7Full;
-        sv_t v = (sv_t)(sv >> (8 * past)) | (sv_t)((sv_t)(ones << 1) << (8 * KB - 1 - 8 * past));
-        v = s_in ? v : ones;
-        if constexpr (A4) {
-          const uint32_t lo4 = (uint32_t)v, hi4 = (uint32_t)(v >> 32);
-          *reinterpret_cast<uint2*>(sc + tid * 8) = make_uint2(__builtin_amdgcn_perm(hi4, lo4, 0x06040200u),
-                                                               __builtin_amdgcn_perm(hi4, lo4, 0x07050301u));
-        } else {
-          *reinterpret_cast<uint32_t*>(sc + tid * 4) = __builtin_amdgcn_perm((uint32_t)v, (uint32_t)v, 0x03010200u);
-        }
-      };
       const int h = lane_t >> 5;
       const int ra = wm * 32 * MI + (lane_t & 31), rb = wn * 128 + (lane_t & 31);
       using fragA = std::conditional_t<A4, i32x4, i32x8>;
@@ -424,34 +492,34 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
       fragA aF[2][MI];
       i32x4 bF[4];
       int sA[2][MI], sB[2][4];
-      auto operandA = [](const fragA& f) {
-        if constexpr (A4) return mx4_frag(f);
-        else return f;
+      auto operandA = [](const fragA& v) {
+        if constexpr (A4) return mx4_frag(v);
+        else return v;
       };
       // one k-step, B block j outer: fragment j is dead after its MI MFMAs and
       // is read again for the next k-step at once; the next A fragments go
       // into the other buffer.  KS: this k-step of its K-tile; SS: the K-tile's
       // scale set.  The last k-step reads the next K-tile's fragments and
-      // scales, and issues the DMA of the K-tile after that, two per block.
-      auto kstep = [&](auto ksc, auto ssc, auto dmac, const uint8_t* na, const uint8_t* nbt, const uint8_t* nsc,
+      // scales, and issues the DMA of the K-tile after that.
+      auto kstep = [&](auto ksc, auto ssc, const uint8_t* na, const uint8_t* nbt, const uint8_t* nsc, const Fetch& ff,
                        int dkt, uint8_t* da, uint8_t* db) {
         constexpr int KS = decltype(ksc)::value, SS = decltype(ssc)::value, NK = (KS + 1) % KSN;
-        constexpr bool DMA = decltype(dmac)::value;
+        constexpr bool LAST = KS == KSN - 1;
+        LanePart d;
+        if constexpr (LAST) d = lane_part();
         static_for<4>([&](auto jc) {
           constexpr int j = decltype(jc)::value;
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (j < MI) aF[(KS + 1) & 1][j] = rdA(na, NK, j);
-          if constexpr (KS == KSN - 1) {
+          if constexpr (LAST) {
             if constexpr (j < MI) sA[SS ^ 1][j] = rdSA(nsc, j);
             sB[SS ^ 1][j] = rdSB(nsc, j);
-          }
-          if constexpr (DMA) {
-            if constexpr (j < MI) {
-              dmaA(dkt, da, 2 * j);
-              dmaA(dkt, da, 2 * j + 1);
-            } else if constexpr (j < MI + 2) {
-              dmaB(dkt, db, NJB / 2 * (j - MI));
-              if constexpr (A4) dmaB(dkt, db, 2 * (j - MI) + 1);
+            if constexpr (j < 2) {
+              dmaA(d, ff, dkt, da, 2 * j);
+              dmaA(d, ff, dkt, da, 2 * j + 1);
+            } else {
+              dmaB(d, ff, dkt, db, NJB / 2 * (j - 2));
+              if constexpr (A4) dmaB(d, ff, dkt, db, 2 * (j - 2) + 1);
             }
           }
           static_for<MI>([&](auto ic) {
@@ -463,58 +531,38 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
         });
         __builtin_amdgcn_sched_barrier(0);
       };
-      auto issue = [&](int kt, uint8_t* da, uint8_t* db) {
-#pragma unroll
-        for (int j = 0; j < NJA; ++j) dmaA(kt, da, j);
-#pragma unroll
-        for (int j = 0; j < NJB; ++j) dmaB(kt, db, j);
-      };
-      // K-tile kt (in the other stage) has landed, its scales are stored, and
-      // every wave's reads of this stage are done
-      auto stage_barrier = [&](uint8_t* sc, int kt) {
-        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
-        scale_store(sc, kt);
-        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-        __syncthreads();
-      };
       using I0 = std::integral_constant<int, 0>;
       using I1 = std::integral_constant<int, 1>;
       using IL = std::integral_constant<int, KSN - 1>;
-      using No = std::false_type;
-      using Yes = std::true_type;
       // all but the last k-step of the K-tile in (a, b)
       auto first_steps = [&](auto ssc, const uint8_t* a, const uint8_t* b) {
-        static_for<KSN - 1>([&](auto ks) { kstep(ks, ssc, No{}, a, b, nullptr, 0, nullptr, nullptr); });
+        static_for<KSN - 1>([&](auto ks) { kstep(ks, ssc, a, b, nullptr, Fetch{}, 0, nullptr, nullptr); });
       };
-      __syncthreads();            // the previous tile's reads are done
-      issue(0, a0, b0);
-      if (nblk >= KB) scale_load(0);
-      else scale_load_short();
-      stage_barrier(sc0, 0);
-      issue(1, a1, b1);
-      if (nk > 1) scale_load(1);
+      // K-tiles kt and kt + 1; fetches K-tiles fkt and fkt + 1 of ff
+      auto pair = [&](int kt, const Fetch& ff, int fkt) {
+        first_steps(I0{}, a0, b0);
+        stage_barrier(sc1, kt + 1);
+        scale_load(ff, fkt);
+        kstep(IL{}, I0{}, a1, b1, sc1, ff, fkt, a0, b0);
+        first_steps(I1{}, a1, b1);
+        stage_barrier(sc0, fkt);
+        scale_load(ff, fkt + 1);
+        kstep(IL{}, I1{}, a0, b0, sc0, ff, fkt + 1, a1, b1);
+      };
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < MI; ++i) { aF[0][i] = rdA(a0, 0, i); sA[0][i] = rdSA(sc0, i); }
 #pragma unroll
       for (int j = 0; j < 4; ++j) { bF[j] = rdB(b0, 0, j); sB[0][j] = rdSB(sc0, j); }
-      const int nk2 = nk & ~1;
-      for (int kt = 0; kt < nk2; kt += 2) {
-        first_steps(I0{}, a0, b0);
-        stage_barrier(sc1, kt + 1);
-        scale_load(kt + 2);
-        kstep(IL{}, I0{}, Yes{}, a1, b1, sc1, kt + 2, a0, b0);
-        first_steps(I1{}, a1, b1);
-        stage_barrier(sc0, kt + 2);
-        scale_load(kt + 3);
-        kstep(IL{}, I1{}, Yes{}, a0, b0, sc0, kt + 3, a1, b1);
-      }
-      if (nk & 1) {
-        first_steps(I0{}, a0, b0);
-        kstep(IL{}, I0{}, No{}, a0, b0, sc0, 0, nullptr, nullptr);
-      }
-      // (the DMA past the end, zeros, must land before the next tile's)
-      __builtin_amdgcn_s_waitcnt(0x0F70);
+      const Fetch f = fetch_of(cur, true);
+      for (int kt = 0; kt < nk - 2; kt += 2) pair(kt, f, kt + 2);
+      pair(nk - 2, fetch_of(nxt, more), 0);   // (after the last tile the loads read nothing)
+      // the sums are needed here: without this the compiler sinks the last
+      // MFMAs into the epilogue's branches, with their fragments in scratch
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[i][j]));
       // lane (r, h) holds, of row r, columns 8 h .. + 7 of the first and of the
       // second 16 of each 32; the swap gives lanes r and r + 16 the two halves
       // of one row, so that a store covers 64 bytes of each of 16 rows
@@ -523,7 +571,7 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         const int m = wm * 32 * MI + 32 * i + er;
-        uint16_t* crow = p.C + (long long)(row0 + m) * p.N + n0 + eo;
+        uint16_t* crow = p.C + (long long)(cur.row0 + m) * p.N + cur.n0 + eo;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int n = wn * 128 + 32 * j;
@@ -532,16 +580,19 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
           for (int d = 0; d < 8; ++d) w[d] = pack_bf16x2(acc[i][j][2 * d], acc[i][j][2 * d + 1]);
 #pragma unroll
           for (int d = 0; d < 4; ++d) swap16(w[d], w[4 + d]);
-          if (n < cols) {
-            if (m < rows) *reinterpret_cast<uint4*>(crow + n) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (m + 16 < rows)
+          if (n < p.N - cur.n0) {
+            if (m < cur.rows) *reinterpret_cast<uint4*>(crow + n) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (m + 16 < cur.rows)
               *reinterpret_cast<uint4*>(crow + 16LL * p.N + n) = make_uint4(w[4], w[5], w[6], w[7]);
           }
         }
       }
     };
-    if (rows > 128) tile_body(std::integral_constant<int, 2>{});
+    if (cur.rows > 128) tile_body(std::integral_constant<int, 2>{});
     else tile_body(std::integral_constant<int, 1>{});
+    if (!more) break;
+    cur_ = nxt_;
+    tile = ntile;
   }
 }
 
