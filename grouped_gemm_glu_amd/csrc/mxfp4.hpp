@@ -278,40 +278,63 @@ __device__ __forceinline__ int mx4_off64(int r, int c) { return r * 64 + ((c ^ (
 // Grouped product of e2m1 (A4) or e4m3 rows and e2m1 weights on 256 x 256
 // tiles: 8 waves in a 4 x 2 grid of 64 x 128,
 // v_mfma_scale_f32_32x32x64_f8f6f4.  A K-tile is 128 bytes of each row of A, 256
-// e2m1 or 128 e4m3 values, and as many of B, staged by LDS-DMA in two stages
-// (the fragment reads are free of bank conflicts); the barrier that frees a
-// stage sits before the last of a K-tile's k-steps (of 64 values), whose
-// fragments are in registers, as in group_gemm_kernel.  A block of 32 values is
-// one 16-byte chunk of e2m1 codes or two of e4m3, so a K that ends inside a
-// K-tile masks whole chunks: their DMA is sent out of the descriptor's range
-// and reads zeros, their scales are set to 1.  Scales go through registers
-// (their rows, K / 32 bytes long, have any alignment): thread t fetches those
-// of row t % 256 of A or B and stores the even blocks' and the odd blocks' in a
-// run each: lane half h's scales of the k-steps.  (K >= 32 KB: a row has at
-// least one K-tile's scales.)
-// The stream of K-tiles runs on over the tiles: the last pair of a tile fetches
-// the first pair of the workgroup's next one, and the epilogue works from
-// registers alone, so that its stores and the next tile's first loads overlap.
+// e2m1 or 128 e4m3 values, and as many of B, staged by LDS-DMA in NST stages (2
+// of 64 KB, or 3 of 48 KB).  The fragment reads are free of bank conflicts; the
+// barrier that frees a stage sits before the last of a K-tile's k-steps (of 64
+// values), whose fragments are in registers.  A block of 32 values is one
+// 16-byte chunk of e2m1 codes or two of e4m3, so a K that ends inside a K-tile
+// masks whole chunks: their DMA is sent out of the descriptor's range and reads
+// zeros, their scales are set to 1.  Scales go through registers (their rows, K
+// / 32 bytes long, have any alignment): thread t fetches those of row t % 256
+// of A or B and stores the even blocks' and the odd blocks' in a run each: lane
+// half h's scales of the k-steps.  (A row has at least one K-tile's scales: K >=
+// 256, or 128 for e4m3.)
+// The stream of K-tiles runs on over the tiles: the last NST K-tiles of a tile
+// fetch the first ones of the workgroup's next tile, and the epilogue works
+// from registers alone, so that its stores and the next tile's first loads
+// overlap.
+// What bounds it (16384 rows in 32 groups x 4096 x 7168, e2m1, per 256-value
+// K-tile of a CU): 1.35 us with the loads left out (the MFMAs, which run at
+// 6.1 PFLOP/s at most on random codes, the chip being power-limited), 2.17 us
+// with the MFMAs left out (the operands' round trip), 2.1 us together.  64 KB
+// of aligned 128-byte row pieces take 0.64 us from L2, of 64-byte pieces or of
+// pieces that straddle lines (K % 256 != 0) 1.1 us: four stages of 128 values
+// were 20% slower for e2m1 rows for that reason, three of them 5% faster than
+// two for e4m3 rows, of which only the weights take 64-byte pieces.
 template <bool A4>
 __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
-  // Four arrays (A and B of the two stages), so that the compiler can tell the
-  // DMA of one stage from the reads of the other.
+  constexpr int NST = A4 ? 2 : 3;         // stages
   constexpr int KB = A4 ? 8 : 4;          // blocks of 32 values per K-tile
   constexpr int KSN = KB / 2;             // k-steps per K-tile
-  constexpr int NJB = A4 ? 4 : 2;         // B DMA pieces (1 KB) per wave; A: 4
-  __shared__ __attribute__((aligned(16))) uint8_t a0[32768], a1[32768], b0[8192 * NJB], b1[8192 * NJB];
-  __shared__ __attribute__((aligned(16))) uint8_t sc0[512 * KB], sc1[512 * KB];
+  constexpr int NJB = A4 ? 4 : 2;         // DMA pieces (1 KB) of B per wave and K-tile; of A: 4
+  constexpr int ABYTES = 32768;           // A's part of a stage, B's after it
+  constexpr int SBYTES = ABYTES + 8192 * NJB;
+  // One array per stage, so that the compiler can tell the DMA of one from the
+  // reads of another.
+  __shared__ __attribute__((aligned(16))) uint8_t st0[SBYTES], st1[SBYTES], st2[NST > 2 ? SBYTES : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t sc0[512 * KB], sc1[512 * KB], sc2[NST > 2 ? 512 * KB : 16];
   __shared__ RowScan gs;
+  auto stage = [&](auto ic) -> uint8_t* {
+    constexpr int i = decltype(ic)::value % NST;
+    if constexpr (i == 0) return st0;
+    else if constexpr (i == 1) return st1;
+    else return st2;
+  };
+  auto scales = [&](auto ic) -> uint8_t* {
+    constexpr int i = decltype(ic)::value % NST;
+    if constexpr (i == 0) return sc0;
+    else if constexpr (i == 1) return sc1;
+    else return sc2;
+  };
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   build_row_scan<512, MX4_BM>(gs, p.counts, p.E, p.M_cap, p.offsets_out, p.status_out, blockIdx.x == 0);
   const int NT = (p.N + MX4_BN - 1) / MX4_BN;
-  const int nblk = p.K >> 5;                          // blocks of 32 values
-  const int nk = ((nblk + KB - 1) / KB + 1) & ~1;     // K-tiles, in pairs (an odd one out is a masked one)
+  const int nblk = p.K >> 5;                                        // blocks of 32 values
+  const int nk = ((nblk + KB - 1) / KB + NST - 1) / NST * NST;      // K-tiles, rounded up by masked ones
   const uint32_t lda = A4 ? (uint32_t)p.K >> 1 : (uint32_t)p.K, ldb = (uint32_t)p.K >> 1;   // bytes per row
-  const int ntiles = __builtin_amdgcn_readfirstlane(gs.tile_off[p.E]);
-  const long long total = (long long)ntiles * NT;
+  const long long total = (long long)__builtin_amdgcn_readfirstlane(gs.tile_off[p.E]) * NT;
   const int P = gridDim.x;
   // workgroups are dealt to the 8 XCDs in turn: each XCD gets a run of tiles
   const int slot = (P % 8 == 0) ? ((blockIdx.x & 7) * (P >> 3) + (blockIdx.x >> 3)) : blockIdx.x;
@@ -368,57 +391,52 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
     f.s_off = (isA ? min(srow, t.rows - 1) : min(mx4_col(srow), cols - 1)) * nblk;
     return f;
   };
-  // DMA piece: 1 KB of LDS, 8 rows of 128 bytes (or 16 of 64); lane (rl, pc)
-  // lands on row rl, physical chunk pc, and fetches logical chunk pc ^ key of
-  // its row.  The address is linear in the piece's row and the lane's: mx4_col(8
+  // DMA piece: 1 KB of LDS, 8 rows of 128 bytes or 16 of 64; a lane lands on
+  // row l / 8 (l / 4) of it and fetches the logical chunk that its physical one
+  // holds.  The address is linear in the piece's row and the lane's: mx4_col(8
   // x + y) = mx4_col(8 x) + mx4_col(y) for y < 8 (and so with 16).  The lane's
   // part is derived anew for each K-tile (opaque zero): registers are what the
   // main loop is short of.
-  struct LanePart { uint32_t la, lb; int ck, ckb; };
+  struct LanePart { uint32_t la, lb; int ca, cb; };
   auto lane_part = [&]() {
     const int l = lane + opaque_zero(), rl = l >> 3;
     LanePart d;
+    d.ca = (l & 7) ^ rl;                                  // swz_off, but for the piece's part
+    d.cb = A4 ? d.ca : (l & 3) ^ ((l >> 4) & 3);          // mx4_off64
     d.la = (uint32_t)rl * lda;
     d.lb = (uint32_t)mx4_col(A4 ? rl : l >> 2) * ldb;
-    d.ck = (l & 7) ^ rl;
-    d.ckb = (l & 3) ^ ((l >> 4) & 3);     // 64-byte rows: key (row / 4) % 4
     return d;
   };
   auto dmaA = [&](const LanePart& d, const Fetch& f, int kt, uint8_t* st, int j) {
     const int piece = wave * 4 + j;
-    const int c = d.ck ^ swz_hi(piece & 3);
+    const int c = d.ca ^ swz_hi(piece & 3);
     const uint32_t off = d.la + (uint32_t)(c * 16) + ((uint32_t)(piece * 8) * lda + (uint32_t)(kt * 128));
     const int left = (nblk - KB * kt) * (A4 ? 1 : 2);     // chunks of the row that are left
     lds_dma16(f.A, st + piece * 1024, c < left ? off : 0xFFFFFFF0u, 0);
   };
   auto dmaB = [&](const LanePart& d, const Fetch& f, int kt, uint8_t* st, int j) {
     const int piece = wave * NJB + j;
-    const int c = A4 ? d.ck ^ swz_hi(piece & 3) : d.ckb;
+    const int c = A4 ? d.cb ^ swz_hi(piece & 3) : d.cb;
     const int urow = mx4_col(piece * (A4 ? 8 : 16));
     const uint32_t off = d.lb + (uint32_t)(c * 16) + ((uint32_t)urow * ldb + (uint32_t)(kt * (A4 ? 128 : 64)));
-    lds_dma16(f.B, st + piece * 1024, c < nblk - KB * kt ? off : 0xFFFFFFF0u, 0);
+    lds_dma16(f.B, st + ABYTES + piece * 1024, c < nblk - KB * kt ? off : 0xFFFFFFF0u, 0);
   };
-  auto issue = [&](const Fetch& f, int kt, uint8_t* da, uint8_t* db) {
-    const LanePart d = lane_part();
-#pragma unroll
-    for (int j = 0; j < 4; ++j) dmaA(d, f, kt, da, j);
-#pragma unroll
-    for (int j = 0; j < NJB; ++j) dmaB(d, f, kt, db, j);
-  };
-  // scales of K-tile kt of row srow.  Loads stay inside the row: the last
-  // K-tile's bytes end with the row and are shifted down; a masked K-tile's
-  // load is dropped.  No branch: with one in the main loop the compiler sinks a
-  // k-step's MFMAs below it and spills the fragments.  The bytes are worked on
-  // when they are stored, a K-tile after their load.
+  // scales of K-tile kt of row srow, one register per stage.  Loads stay inside
+  // the row: the last K-tile's bytes end with the row and are shifted down; a
+  // masked K-tile's load is dropped.  No branch: with one in the main loop the
+  // compiler sinks a k-step's MFMAs below it and spills the fragments.  The
+  // bytes are worked on when they are stored, K-tiles after their load.
   using sv_t = std::conditional_t<A4, unsigned long long, uint32_t>;   // a row's KB scale bytes
-  sv_t sv = 0;
+  sv_t sv[NST];
   auto scale_load = [&](const Fetch& f, int kt) {
-    __builtin_memcpy(&sv, f.sp + (f.s_off + min(KB * kt, nblk - KB)), KB);
+    sv_t v;
+    __builtin_memcpy(&v, f.sp + (f.s_off + min(KB * kt, nblk - KB)), KB);
+    return v;
   };
-  auto scale_store = [&](uint8_t* sc, int kt) {
+  auto scale_store = [&](uint8_t* sc, sv_t v, int kt) {
     const int past = max(0, min(KB * kt + KB - nblk, KB - 1));   // blocks past the end of K: 1 (byte 127)
     const sv_t ones = (sv_t)0x7F7F7F7F7F7F7F7Full;
-    sv_t v = (sv_t)(sv >> (8 * past)) | (sv_t)((sv_t)(ones << 1) << (8 * KB - 1 - 8 * past));
+    v = (sv_t)(v >> (8 * past)) | (sv_t)((sv_t)(ones << 1) << (8 * KB - 1 - 8 * past));
     v = KB * kt < nblk ? v : ones;
     if constexpr (A4) {
       const uint32_t lo4 = (uint32_t)v, hi4 = (uint32_t)(v >> 32);
@@ -428,30 +446,29 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
       *reinterpret_cast<uint32_t*>(sc + tid * 4) = __builtin_amdgcn_perm((uint32_t)v, (uint32_t)v, 0x03010200u);
     }
   };
-  // the K-tile in the other stage has landed, its scales are stored, and every
-  // wave's reads of this stage are done
-  auto stage_barrier = [&](uint8_t* sc, int kt) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
-    scale_store(sc, kt);
-    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-    __syncthreads();
-  };
 
   long long tile = slot;
   if (tile >= total) return;   // (the whole workgroup)
   Tile cur_ = decode(tile);
   {
     const Fetch f = fetch_of(uniform(cur_), true);
-    issue(f, 0, a0, b0);
-    scale_load(f, 0);
-    stage_barrier(sc0, 0);
-    issue(f, 1, a1, b1);
-    scale_load(f, 1);
+    const LanePart d = lane_part();
+    static_for<NST>([&](auto i) {
+      sv[i] = scale_load(f, i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dmaA(d, f, i, stage(i), j);
+#pragma unroll
+      for (int j = 0; j < NJB; ++j) dmaB(d, f, i, stage(i), j);
+    });
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+    scale_store(sc0, sv[0], 0);
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+    __syncthreads();
   }
 
   for (;;) {
-    // K-tile 0 of the tile is in (a0, b0, sc0); K-tile 1 is on its way to (a1,
-    // b1) and its scales to sv
+    // K-tile 0 of the tile is in stage 0, its scales too; K-tiles 1 .. NST - 1
+    // are on their way to the other stages and their scales to sv
     const long long ntile = tile + P;
     const bool more = ntile < total;
     Tile nxt_ = cur_;
@@ -474,8 +491,8 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
         }
       };
       auto rdB = [&](const uint8_t* st, int ks, int j) {
-        return *reinterpret_cast<const i32x4*>(
-            st + (A4 ? swz_off(rb + 32 * j, 2 * ks + h) : mx4_off64(rb + 32 * j, 2 * ks + h)));
+        const int r = rb + 32 * j, c = 2 * ks + h;
+        return *reinterpret_cast<const i32x4*>(st + ABYTES + (A4 ? swz_off(r, c) : mx4_off64(r, c)));
       };
       using sw_t = std::conditional_t<A4, uint32_t, uint16_t>;   // a lane half's scales of a K-tile
       auto rdSA = [&](const uint8_t* sc, int i) { return (int)reinterpret_cast<const sw_t*>(sc)[(ra + 32 * i) * 2 + h]; };
@@ -491,72 +508,88 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
           for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
       fragA aF[2][MI];
       i32x4 bF[4];
-      int sA[2][MI], sB[2][4];
+      int sA[MI], sB[4], nA[MI], nB[4];
       auto operandA = [](const fragA& v) {
         if constexpr (A4) return mx4_frag(v);
         else return v;
       };
-      // one k-step, B block j outer: fragment j is dead after its MI MFMAs and
-      // is read again for the next k-step at once; the next A fragments go
-      // into the other buffer.  KS: this k-step of its K-tile; SS: the K-tile's
-      // scale set.  The last k-step reads the next K-tile's fragments and
-      // scales, and issues the DMA of the K-tile after that.
-      auto kstep = [&](auto ksc, auto ssc, const uint8_t* na, const uint8_t* nbt, const uint8_t* nsc, const Fetch& ff,
-                       int dkt, uint8_t* da, uint8_t* db) {
-        constexpr int KS = decltype(ksc)::value, SS = decltype(ssc)::value, NK = (KS + 1) % KSN;
+      // one k-step (KS) of the K-tile in stage S, B block j outer: fragment j is
+      // dead after its MI MFMAs and is read again for the next k-step at once;
+      // the next A fragments go into the other buffer.  The last k-step reads the
+      // next stage's fragments and scales, and issues the DMA of K-tile dkt of
+      // ff into its own stage.
+      auto kstep = [&](auto ksc, auto sc_, const Fetch& ff, int dkt) {
+        constexpr int KS = decltype(ksc)::value, S = decltype(sc_)::value;
         constexpr bool LAST = KS == KSN - 1;
+        constexpr int NK = (KS + 1) % KSN;
+        using NS = std::integral_constant<int, (S + (LAST ? 1 : 0)) % NST>;
         LanePart d;
         if constexpr (LAST) d = lane_part();
         static_for<4>([&](auto jc) {
           constexpr int j = decltype(jc)::value;
           __builtin_amdgcn_sched_barrier(0);
-          if constexpr (j < MI) aF[(KS + 1) & 1][j] = rdA(na, NK, j);
+          if constexpr (j < MI) aF[(KS + 1) & 1][j] = rdA(stage(NS{}), NK, j);
           if constexpr (LAST) {
-            if constexpr (j < MI) sA[SS ^ 1][j] = rdSA(nsc, j);
-            sB[SS ^ 1][j] = rdSB(nsc, j);
-            if constexpr (j < 2) {
-              dmaA(d, ff, dkt, da, 2 * j);
-              dmaA(d, ff, dkt, da, 2 * j + 1);
+            if constexpr (j < MI) nA[j] = rdSA(scales(NS{}), j);
+            nB[j] = rdSB(scales(NS{}), j);
+            if constexpr (A4) {
+              if constexpr (j < 2) {
+                dmaA(d, ff, dkt, stage(sc_), 2 * j);
+                dmaA(d, ff, dkt, stage(sc_), 2 * j + 1);
+              } else {
+                dmaB(d, ff, dkt, stage(sc_), 2 * j - 4);
+                dmaB(d, ff, dkt, stage(sc_), 2 * j - 3);
+              }
             } else {
-              dmaB(d, ff, dkt, db, NJB / 2 * (j - 2));
-              if constexpr (A4) dmaB(d, ff, dkt, db, 2 * (j - 2) + 1);
+              dmaA(d, ff, dkt, stage(sc_), j);
+              if constexpr (j >= 2) dmaB(d, ff, dkt, stage(sc_), j - 2);
             }
           }
           static_for<MI>([&](auto ic) {
             constexpr int i = decltype(ic)::value;
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                mx4_frag(bF[j]), operandA(aF[KS & 1][i]), acc[i][j], 4, A4 ? 4 : 0, KS, sB[SS][j], KS, sA[SS][i]);
+                mx4_frag(bF[j]), operandA(aF[KS & 1][i]), acc[i][j], 4, A4 ? 4 : 0, KS, sB[j], KS, sA[i]);
           });
-          bF[j] = rdB(nbt, NK, j);
+          bF[j] = rdB(stage(NS{}), NK, j);
         });
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (LAST) {
+#pragma unroll
+          for (int i = 0; i < MI; ++i) sA[i] = nA[i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sB[j] = nB[j];
+        }
       };
-      using I0 = std::integral_constant<int, 0>;
-      using I1 = std::integral_constant<int, 1>;
-      using IL = std::integral_constant<int, KSN - 1>;
-      // all but the last k-step of the K-tile in (a, b)
-      auto first_steps = [&](auto ssc, const uint8_t* a, const uint8_t* b) {
-        static_for<KSN - 1>([&](auto ks) { kstep(ks, ssc, a, b, nullptr, Fetch{}, 0, nullptr, nullptr); });
-      };
-      // K-tiles kt and kt + 1; fetches K-tiles fkt and fkt + 1 of ff
-      auto pair = [&](int kt, const Fetch& ff, int fkt) {
-        first_steps(I0{}, a0, b0);
-        stage_barrier(sc1, kt + 1);
-        scale_load(ff, fkt);
-        kstep(IL{}, I0{}, a1, b1, sc1, ff, fkt, a0, b0);
-        first_steps(I1{}, a1, b1);
-        stage_barrier(sc0, fkt);
-        scale_load(ff, fkt + 1);
-        kstep(IL{}, I1{}, a0, b0, sc0, ff, fkt + 1, a1, b1);
+      // K-tiles kt .. kt + NST - 1; fetches K-tiles fkt .. of ff.  Before the
+      // last k-step of each: K-tile kt + s + 1 has landed (the DMA of the NST -
+      // 2 after it may be on its way; with their scales' loads that is less than
+      // what is, and waits for the oldest of them too), its scales are stored,
+      // and every wave's reads of stage s are done.
+      auto round = [&](int kt, const Fetch& ff, int fkt) {
+        static_for<NST>([&](auto sc_) {
+          constexpr int S = decltype(sc_)::value, NX = (S + 1) % NST;
+          static_for<KSN - 1>([&](auto ks) { kstep(ks, sc_, ff, 0); });
+          constexpr int VM = (NST - 2) * (4 + NJB);
+          __builtin_amdgcn_s_waitcnt(0x0F70 | (VM & 15) | ((VM >> 4) << 14));   // vmcnt(VM)
+          scale_store(scales(std::integral_constant<int, NX>{}), sv[NX], S == NST - 1 ? fkt : kt + S + 1);
+          // (the bare barrier: __syncthreads would wait for all loads)
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_sched_barrier(0);
+          sv[S] = scale_load(ff, fkt + S);
+          kstep(std::integral_constant<int, KSN - 1>{}, sc_, ff, fkt + S);
+        });
       };
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < MI; ++i) { aF[0][i] = rdA(a0, 0, i); sA[0][i] = rdSA(sc0, i); }
+      for (int i = 0; i < MI; ++i) { aF[0][i] = rdA(st0, 0, i); sA[i] = rdSA(sc0, i); }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) { bF[j] = rdB(b0, 0, j); sB[0][j] = rdSB(sc0, j); }
+      for (int j = 0; j < 4; ++j) { bF[j] = rdB(st0, 0, j); sB[j] = rdSB(sc0, j); }
       const Fetch f = fetch_of(cur, true);
-      for (int kt = 0; kt < nk - 2; kt += 2) pair(kt, f, kt + 2);
-      pair(nk - 2, fetch_of(nxt, more), 0);   // (after the last tile the loads read nothing)
+      for (int kt = 0; kt < nk - NST; kt += NST) round(kt, f, kt + NST);
+      round(nk - NST, fetch_of(nxt, more), 0);   // (after the last tile the loads read nothing)
       // the sums are needed here: without this the compiler sinks the last
       // MFMAs into the epilogue's branches, with their fragments in scratch
 #pragma unroll
