@@ -36,43 +36,55 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], float scale) {
   return w;
 }
 
+// Routed rows: the sum of the clamped counts, at most M_cap, by one wave alone.
+__device__ __forceinline__ int routed_rows(const int* __restrict__ counts, int E, int M_cap) {
+  long long n = 0;
+  for (int e = threadIdx.x & 63; e < E; e += 64) n += max(counts[e], 0);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d, 64);
+  return (int)(n < M_cap ? n : M_cap);
+}
+
 // Row-wise quantisation of a bf16 [R][C] matrix: 4 lanes per 32-value block,
-// 16 bytes read and 4 bytes of codes written per lane.  A block holding a NaN
-// or an infinity gets the NaN scale 0xFF and zero codes (e2m1 has no NaN).
+// 16 bytes read and 4 bytes of codes written per lane, U of them in flight.  A
+// block holding a NaN or an infinity gets the NaN scale 0xFF and zero codes
+// (e2m1 has no NaN).
+template <int U>
 __global__ __launch_bounds__(256) void mx4_rows_kernel(const uint16_t* __restrict__ v, int R, int C,
                                                        const int* __restrict__ counts, int E,
                                                        uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
-  __shared__ GroupScan gs;
-  int rows = R;
-  if (counts) {
-    build_group_scan<256>(gs, counts, E, R, 1, 0, nullptr, nullptr, false);
-    rows = gs.row_off[E];
-  }
-  const long long total = (long long)rows * (C >> 3);   // a multiple of 4
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long long)gridDim.x * 256) {
-    const uint4 u = reinterpret_cast<const uint4*>(v)[i];
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float x[8];
-    float amax = 0.0f;
-    int nan = 0;
+  const long long rows = counts ? routed_rows(counts, E, R) : R;
+  const long long total = rows * (C >> 3);   // 16-byte chunks: a multiple of 4
+  for (long long i0 = (long long)blockIdx.x * 256 * U + threadIdx.x; i0 < total;
+       i0 += (long long)gridDim.x * 256 * U) {
+    uint4 u[U];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = __uint_as_float(w[j] << 16);
-      x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    for (int k = 0; k < U; ++k) {
+      u[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (i0 + 256 * k < total) u[k] = reinterpret_cast<const uint4*>(v)[i0 + 256 * k];
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      amax = fmaxf(amax, fabsf(x[j]));
-      nan |= x[j] != x[j];
-    }
+    for (int k = 0; k < U; ++k) {
+      const long long i = i0 + 256 * k;
+      const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+      // the block's largest magnitude as bits: bf16 bits order like the values,
+      // and a NaN's are above infinity's
+      uint32_t mag = 0;
+      float x[8];
 #pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-      amax = fmaxf(amax, __shfl_xor(amax, d, 64));
-      nan |= __shfl_xor(nan, d, 64);
+      for (int j = 0; j < 4; ++j) {
+        x[2 * j] = __uint_as_float(w[j] << 16);
+        x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        mag = max(mag, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
+      }
+      mag = max(mag, (uint32_t)__shfl_xor((int)mag, 1, 64));
+      mag = max(mag, (uint32_t)__shfl_xor((int)mag, 2, 64));
+      const int X = mx4_scale_exponent(__uint_as_float(mag));   // (128 from infinity up)
+      if (i < total) {
+        reinterpret_cast<uint32_t*>(q)[i] = X == 128 ? 0u : e2m1x8(x, pow2f(X));
+        if ((i & 3) == 0) s[i >> 2] = e8m0_byte(X);
+      }
     }
-    const int X = nan ? 128 : mx4_scale_exponent(amax);
-    reinterpret_cast<uint32_t*>(q)[i] = X == 128 ? 0u : e2m1x8(x, pow2f(X));
-    if ((i & 3) == 0) s[i >> 2] = e8m0_byte(X);
   }
 }
 
@@ -103,91 +115,7 @@ __global__ __launch_bounds__(256) void mx4_weight_kn_kernel(const uint16_t* __re
   s[row * (K / 32) + kb] = e8m0_byte(X);
 }
 
-// Grouped product straight from memory: one workgroup per (16 MB rows of a
-// group, 16 columns), its 4 waves sharing K in steps of 128 values; the
-// partial sums are added through LDS in wave order.  Lane (r, q) = (l % 16,
-// l / 16) of v_mfma_scale_f32_16x16x128_f8f6f4 holds, of an e2m1 operand, row
-// r's block q (16 bytes) with its scale; of an e4m3 operand, bytes 16 q .. + 15
-// of the step's first 64 values and of its second 64, and the scale of block q.
-// The result's lane holds columns 4 q .. + 3 of row r.
-template <bool A4, int MB>
-__global__ __launch_bounds__(256) void mx4_gemm_small_kernel(Mx4Args p) {
-  __shared__ GroupScan gs;
-  __shared__ f32x4 red[3][MB][64];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, q = lane >> 4;
-  build_group_scan<256>(gs, p.counts, p.E, p.M_cap, 16 * MB, 0, p.offsets_out, p.status_out, blockIdx.x == 0);
-  const int ncb = p.N >> 4, nblk = p.K >> 5;
-  const long long items = (long long)gs.tile_off[p.E] * ncb;
-  const long long ldb = p.K >> 1, lda = A4 ? p.K >> 1 : p.K;
-  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-    const int tile = (int)(it / ncb), n0 = (int)(it - (long long)tile * ncb) * 16;
-    int lo = 0, hi = p.E;   // the last e with tile_off[e] <= tile
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (gs.tile_off[mid] <= tile) lo = mid; else hi = mid;
-    }
-    const int row0 = gs.row_off[lo] + (tile - gs.tile_off[lo]) * 16 * MB;
-    const int rows = min(16 * MB, gs.row_off[lo + 1] - row0);
-    const long long brow = (long long)lo * p.N + n0 + r;
-    f32x4 acc[MB];
-#pragma unroll
-    for (int m = 0; m < MB; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int ks = wave * 4; ks < nblk; ks += 16) {   // first block of the step
-      const int b = ks + q;
-      i32x8 bv = {0, 0, 0, 0, 0, 0, 0, 0};
-      int sb = 127;
-      if (b < nblk) {
-        const int4 u = *reinterpret_cast<const int4*>(p.B + brow * ldb + b * 16);
-        bv[0] = u.x; bv[1] = u.y; bv[2] = u.z; bv[3] = u.w;
-        sb = p.b_scales[brow * nblk + b];
-      }
-#pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        const long long arow = row0 + m * 16 + r;
-        const bool in = m * 16 + r < rows;
-        i32x8 av = {0, 0, 0, 0, 0, 0, 0, 0};
-        int sa = 127;
-        if (in && b < nblk) sa = p.a_scales[arow * nblk + b];
-        if constexpr (A4) {
-          if (in && b < nblk) {
-            const int4 u = *reinterpret_cast<const int4*>(p.A + arow * lda + b * 16);
-            av[0] = u.x; av[1] = u.y; av[2] = u.z; av[3] = u.w;
-          }
-        } else {
-          const int b0 = ks + (q >> 1), b1 = b0 + 2;   // the blocks of this lane's two 16-byte pieces
-          const uint8_t* ap = p.A + arow * lda + (long long)b0 * 32 + (q & 1) * 16;
-          if (in && b0 < nblk) {
-            const int4 u = *reinterpret_cast<const int4*>(ap);
-            av[0] = u.x; av[1] = u.y; av[2] = u.z; av[3] = u.w;
-          }
-          if (in && b1 < nblk) {
-            const int4 u = *reinterpret_cast<const int4*>(ap + 64);
-            av[4] = u.x; av[5] = u.y; av[6] = u.z; av[7] = u.w;
-          }
-        }
-        acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, av, acc[m], 4, A4 ? 4 : 0, 0, sb, 0, sa);
-      }
-    }
-    __syncthreads();   // the previous item's sums are read
-    if (wave > 0)
-#pragma unroll
-      for (int m = 0; m < MB; ++m) red[wave - 1][m][lane] = acc[m];
-    __syncthreads();
-    if (wave == 0) {
-#pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        if (m * 16 + r >= rows) continue;
-        const f32x4 v = acc[m] + red[0][m][lane] + red[1][m][lane] + red[2][m][lane];
-        *reinterpret_cast<uint2*>(p.C + (long long)(row0 + m * 16 + r) * p.N + n0 + 4 * q) =
-            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-      }
-    }
-  }
-}
-
-// ---------------------------------------------------------------- tiles
+// ---------------------------------------------------------------- groups
 // Row and m-tile prefixes of the device counts for tiles of BM rows: the part
 // of GroupScan that these kernels need, at half its LDS.
 struct RowScan {
@@ -252,6 +180,200 @@ __device__ __forceinline__ i32x8 mx4_frag(i32x4 v) {
   return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
 }
 
+// ---------------------------------------------------------------- few rows
+// The tiles of BM rows of up to 64 experts, lane e holding expert e's: built
+// and searched by each wave alone, without LDS or barriers.
+struct WaveScan {
+  int row0, rows, tile0, tiles;   // of this lane's expert
+  int total;                      // tiles of all
+};
+template <int BM>
+__device__ __forceinline__ WaveScan wave_scan(const int* __restrict__ counts, int E, int M_cap, int* offsets_out,
+                                              int* status_out, bool writer) {
+  const int lane = threadIdx.x & 63;
+  const int c = lane < E ? counts[lane] : 0;
+  const bool neg = __any(c < 0);
+  long long run = max(c, 0);
+  const long long own = run;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const long long o = __shfl_up(run, d, 64);
+    if (lane >= d) run += o;
+  }
+  const bool over = __shfl(run, 63, 64) > M_cap;
+  WaveScan w;
+  w.row0 = (int)(run - own < M_cap ? run - own : M_cap);
+  const int end = (int)(run < M_cap ? run : M_cap);
+  w.rows = end - w.row0;
+  w.tiles = (w.rows + BM - 1) / BM;
+  int t = w.tiles;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(t, d, 64);
+    if (lane >= d) t += o;
+  }
+  w.tile0 = t - w.tiles;
+  w.total = __shfl(t, 63, 64);
+  if (writer) {
+    if (offsets_out) {
+      if (lane < E) offsets_out[lane] = w.row0;
+      if (lane == E - 1) offsets_out[E] = end;
+    }
+    const int st = (neg ? 1 : 0) | (over ? 2 : 0);
+    if (status_out && lane == 0 && st) atomicOr(status_out, st);
+  }
+  return w;
+}
+
+// Grouped product straight from memory, for groups of few rows, where what
+// counts is to stream the active experts' weights at the memory's rate: a wave
+// takes 16 columns of a tile of up to 16 rows of one group and all of K, or a
+// quarter of it (SPLIT: the workgroup's 4 waves take the same 16 columns and
+// add their sums through LDS in wave order; for launches of few waves).  Lane
+// (r, q) = (l % 16, l / 16) of v_mfma_scale_f32_16x16x128_f8f6f4 holds, of an
+// e2m1 operand, row r's block q (16 bytes) with its scale; of an e4m3 operand,
+// bytes 16 q .. + 15 of the step's first 64 values and of its second 64, and the
+// scale of block q.  The result's lane holds columns 4 q .. + 3 of row r.  Groups
+// of four steps (512 values) of both operands are loaded two ahead of the one
+// that is multiplied: loads return in order, so rows fetched later than the
+// weights would wait for the weights behind them.
+template <bool A4, bool SMALL_E, bool SPLIT>
+__global__ __launch_bounds__(256) void mx4_gemm_rows_kernel(Mx4Args p) {
+  __shared__ std::conditional_t<SMALL_E, int, RowScan> gs;
+  __shared__ f32x4 red[SPLIT ? 3 : 1][SPLIT ? 64 : 1];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  WaveScan ws;
+  int ntiles;
+  if constexpr (SMALL_E) {
+    ws = wave_scan<16>(p.counts, p.E, p.M_cap, p.offsets_out, p.status_out, blockIdx.x == 0 && wave == 0);
+    ntiles = ws.total;
+  } else {
+    build_row_scan<256, 16>(gs, p.counts, p.E, p.M_cap, p.offsets_out, p.status_out, blockIdx.x == 0);
+    ntiles = gs.tile_off[p.E];
+  }
+  ntiles = __builtin_amdgcn_readfirstlane(ntiles);
+  const int nblk = p.K >> 5;
+  const int ncb = SPLIT ? p.N >> 4 : p.N >> 6;   // column blocks: of 16 (all waves) or of 64
+  const long long items = (long long)ntiles * ncb;
+  const long long ldb = p.K >> 1, lda = A4 ? p.K >> 1 : p.K;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const int tile = __builtin_amdgcn_readfirstlane((int)(it % ntiles));   // (a group's tiles side by side)
+    const int cb = __builtin_amdgcn_readfirstlane((int)(it / ntiles));
+    const int n0 = SPLIT ? cb * 16 : cb * 64 + wave * 16;
+    int e, row0, rows;
+    if constexpr (SMALL_E) {
+      e = __builtin_ctzll(__ballot(tile >= ws.tile0 && tile < ws.tile0 + ws.tiles));
+      const int local = tile - __builtin_amdgcn_readlane(ws.tile0, e);
+      row0 = __builtin_amdgcn_readlane(ws.row0, e) + local * 16;
+      rows = min(16, __builtin_amdgcn_readlane(ws.rows, e) - local * 16);
+    } else {
+      int lo = 0, hi = p.E;   // the last e with tile_off[e] <= tile
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (gs.tile_off[mid] <= tile) lo = mid; else hi = mid;
+      }
+      e = __builtin_amdgcn_readfirstlane(lo);
+      row0 = __builtin_amdgcn_readfirstlane(gs.row_off[e] + (tile - gs.tile_off[e]) * 16);
+      rows = min(16, __builtin_amdgcn_readfirstlane(gs.row_off[e + 1]) - row0);
+    }
+    const long long brow = (long long)e * p.N + n0 + r;
+    const uint8_t* bq = p.B + brow * ldb + q * 16;
+    const uint8_t* bs = p.b_scales + brow * nblk;
+    // (the last row again behind the tile's end: its results there are not
+    // stored)
+    const long long arow = row0 + min(r, rows - 1);
+    const uint8_t* aq = p.A + arow * lda + (A4 ? q * 16 : (q >> 1) * 32 + (q & 1) * 16);
+    const uint8_t* as = p.a_scales + arow * nblk;
+    constexpr int AST = A4 ? 16 : 32;   // bytes per block of a row
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto mfma = [&](i32x4 bv, int sb, i32x4 a0, i32x4 a1, int sa) {
+      if constexpr (A4)
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx4_frag(bv), mx4_frag(a0), acc, 4, 4, 0, sb, 0, sa);
+      else
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            mx4_frag(bv), __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7), acc, 4, 0, 0, sb, 0, sa);
+    };
+    // a group of 16 blocks (4 steps): the codes, and the 16 scales of each row,
+    // byte 4 s + q of them this lane's
+    struct Group { i32x4 b[4], a0[4], a1[A4 ? 1 : 4], sb, sa; };
+    auto load = [&](int g) {
+      Group v;
+      const uint8_t* bp = bq + (long long)g * 256;
+      const uint8_t* ap = aq + (long long)g * 16 * AST;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        v.b[s] = *reinterpret_cast<const i32x4*>(bp + 64 * s);
+        v.a0[s] = *reinterpret_cast<const i32x4*>(ap + 4 * s * AST);
+        if constexpr (!A4) v.a1[s] = *reinterpret_cast<const i32x4*>(ap + 4 * s * AST + 64);
+      }
+      __builtin_memcpy(&v.sb, bs + 16 * g, 16);
+      __builtin_memcpy(&v.sa, as + 16 * g, 16);
+      return v;
+    };
+    auto use = [&](const Group& v) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        mfma(v.b[s], (int)((uint32_t)v.sb[s] >> (8 * q)), v.a0[s], v.a1[A4 ? 0 : s], (int)((uint32_t)v.sa[s] >> (8 * q)));
+    };
+    const int ngrp = nblk >> 4;
+    constexpr int ST = SPLIT ? 4 : 1;
+    const int g0 = SPLIT ? wave : 0;
+    // the blocks behind the last whole group first, so that their loads do not
+    // stand alone at the end (SPLIT: the wave whose turn that group would be):
+    // zero codes and scale 1 past the end of K, and the scales byte by byte,
+    // since 16 bytes would leave the row
+    Group t;
+    const bool tail = nblk > 16 * ngrp && (!SPLIT || ngrp % 4 == wave);
+    if (tail) {
+      const i32x4 z = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int k0 = 16 * ngrp + 4 * s;
+        const uint8_t* ap = aq + (long long)k0 * AST;
+        const bool in = k0 + q < nblk;
+        t.b[s] = in ? *reinterpret_cast<const i32x4*>(bq + (long long)k0 * 16) : z;
+        t.a0[s] = (A4 ? in : k0 + (q >> 1) < nblk) ? *reinterpret_cast<const i32x4*>(ap) : z;
+        if constexpr (!A4) t.a1[s] = k0 + 2 + (q >> 1) < nblk ? *reinterpret_cast<const i32x4*>(ap + 64) : z;
+        t.sb[s] = in ? bs[k0 + q] : 127;
+        t.sa[s] = in ? as[k0 + q] : 127;
+      }
+    }
+    Group x, y;
+    if (g0 < ngrp) {
+      x = load(g0);
+      y = load(min(g0 + ST, ngrp - 1));
+    }
+    if (tail) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) mfma(t.b[s], t.sb[s], t.a0[s], t.a1[A4 ? 0 : s], t.sa[s]);
+    }
+    if (g0 < ngrp) {
+      int g = g0;
+      for (; g + 2 * ST < ngrp; g += 2 * ST) {
+        use(x);
+        x = load(g + 2 * ST);
+        use(y);
+        y = load(min(g + 3 * ST, ngrp - 1));
+      }
+      use(x);
+      if (g + ST < ngrp) use(y);
+    }
+    if constexpr (SPLIT) {
+      __syncthreads();   // the previous item's sums are read
+      if (wave > 0) red[wave - 1][lane] = acc;
+      __syncthreads();
+      if (wave > 0) continue;
+      acc = acc + red[0][lane] + red[1][lane] + red[2][lane];
+    }
+    if (r < rows)
+      *reinterpret_cast<uint2*>(p.C + (long long)(row0 + r) * p.N + n0 + 4 * q) =
+          make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+  }
+}
+
+// ---------------------------------------------------------------- many rows
 constexpr int MX4_BM = 256, MX4_BN = 256;
 
 // Tile column (weight row) that row rho of a staged 32-row block holds.  The 32

@@ -243,11 +243,63 @@ def test_product_many_experts_and_margin(G, a):
 
 @pytest.mark.parametrize("a", ["fp4", "fp8"])
 def test_product_rows_do_not_depend_on_their_company(G, a):
-    """A row's result is the same in bits alone in its group and among others."""
+    """A row's result is the same in bits whatever its neighbours hold and wherever it sits in a group (the same
+    capacity, so the same kernel)."""
     rng = np.random.default_rng(8)
     N, K = 128, 736
-    ops = _operands(rng, 40, K, 1, N, a)
-    many = _product(G, [40], 40, K, N, a, ops)
-    for r in (0, 17, 39):
-        sub = (ops[0][r:r + 1], ops[1][r:r + 1], ops[2], ops[3])
-        assert np.array_equal(_product(G, [1], 1, K, N, a, sub)[0], many[r])
+    for M in (40, 3000):
+        ops = _operands(rng, M, K, 1, N, a)
+        many = _product(G, [M], M, K, N, a, ops)
+        turned = _product(G, [M], M, K, N, a, (np.roll(ops[0], 7, 0), np.roll(ops[1], 7, 0), ops[2], ops[3]))
+        assert np.array_equal(np.roll(turned[:M], -7, 0), many[:M])
+
+
+# groups large enough for the 256 x 256 tiles: whole and short last m-tiles (more and less than 128 rows), N that
+# ends inside a tile, K that ends inside a K-tile and in odd numbers of them, empty groups, one row, rows behind
+TILE_CASES = [([2000], 576, 1056, 0), ([700, 0, 1, 900, 129], 640, 2880, 7), ([256, 512, 128, 384], 1024, 768, 0),
+              ([1300, 1301], 320, 1312, 3), ([255, 257, 511, 1000], 704, 256, 0), ([3000, 5], 256, 7168, 1)]
+
+
+@pytest.mark.parametrize("a", ["fp4", "fp8"])
+@pytest.mark.parametrize("counts,N,K,pad", TILE_CASES)
+def test_product_tiles(G, counts, N, K, pad, a):
+    rng = np.random.default_rng(N + K + sum(counts))
+    M = sum(counts)
+    ops = _operands(rng, M + pad, K, len(counts), N, a)
+    one = _product(G, counts, M + pad, K, N, a, ops, scale_shift=K % 3)
+    _check(one, counts, M, ops[4], ops[5], a)
+    # six compute units: several tiles for each workgroup, one stream of K-tiles over them
+    few = _product(G, counts, M + pad, K, N, a, ops, cu_margin=250)
+    _check(few, counts, M, ops[4], ops[5], a, "six units")
+
+
+@pytest.mark.parametrize("a", ["fp4", "fp8"])
+def test_product_tiles_nan_rows_and_columns_stay_their_own(G, a):
+    """A NaN scale reaches its row, or its column in its group, and nothing else, across the tiles' edges and
+    in rows and columns that share a staged tile."""
+    rng = np.random.default_rng(9)
+    counts, N, K = [1500, 700], 576, 1056
+    M = sum(counts)
+    ops = list(_operands(rng, M, K, 2, N, a))
+    ops[1][[0, 255, 256, 1499, 1500, M - 1], [0, 5, 32, 7, 31, 32]] = 255
+    ops[3][0, [0, 575], [32, 3]] = 255
+    got = F.bf16_bits_to_f64(_product(G, counts, M, K, N, a, ops)[:M])
+    want = np.zeros((M, N), bool)
+    want[[0, 255, 256, 1499, 1500, M - 1]] = True
+    want[:1500, [0, 575]] = True
+    assert np.array_equal(np.isnan(got), want)
+
+
+@pytest.mark.parametrize("a", ["fp4", "fp8"])
+@pytest.mark.parametrize("E,counts,N,K", [(100, {3: 1, 99: 1}, 64, 32), (65, {0: 17, 64: 3}, 64, 32),
+                                          (64, {63: 40}, 64, 32), (1024, {500: 33}, 64, 32),
+                                          (100, {3: 1, 99: 1}, 192, 544), (65, {0: 17, 64: 3}, 192, 544),
+                                          (64, {63: 40}, 192, 544), (2, {1: 9}, 320, 2080)])
+def test_product_few_rows_of_many_experts(G, E, counts, N, K, a):
+    rng = np.random.default_rng(E + N)
+    c = np.zeros(E, np.int64)
+    for e, n in counts.items():
+        c[e] = n
+    M = int(c.sum())
+    ops = _operands(rng, M + 2, K, E, N, a)
+    _check(_product(G, c, M + 2, K, N, a, ops, scale_shift=1), c, M, ops[4], ops[5], a)
