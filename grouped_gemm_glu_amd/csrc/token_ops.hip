@@ -30,12 +30,37 @@ void for_chunks(int H, F&& f) {
 }
 }  // namespace
 
+// f(lanes per token, quads of experts per lane) as integral constants
+template <typename F>
+void for_router_shape(int E, F&& f) {
+  using std::integral_constant;
+  if (E <= 64) f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  else if (E <= 128) f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+  else if (E <= 256) f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+  else if (E <= 512) f(integral_constant<int, 32>{}, integral_constant<int, 4>{});
+  else f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+}
+
 moe_status_t launch_router(const RouterArgs& a, bool bf16, int* ids, float* weights, hipStream_t s) {
   if (a.T == 0) return MOE_OK;
+  const int lanes = a.E <= 256 ? 16 : a.E <= 512 ? 32 : 64;
+  const int gsz = a.E / a.n_groups;
+  const bool fast = a.E % 4 == 0 && (a.n_groups == 1 || (gsz % 4 == 0 && (gsz & (gsz - 1)) == 0 && gsz <= 4 * lanes));
+  if (fast) {
+    const int per_block = 4 * (64 / lanes);
+    const dim3 grid((unsigned)(((long long)a.T + per_block - 1) / per_block));
+    for_router_shape(a.E, [&](auto l, auto n) {
+      constexpr int L = decltype(l)::value, NI = decltype(n)::value;
+      if (bf16) hipLaunchKernelGGL((router_kernel<L, NI, true>), grid, dim3(256), 0, s, a, ids, weights);
+      else hipLaunchKernelGGL((router_kernel<L, NI, false>), grid, dim3(256), 0, s, a, ids, weights);
+    });
+    return launched();
+  }
   const dim3 grid((unsigned)(((long long)a.T + 3) / 4));
   for_experts_per_lane(a.E, [&](auto v) {
-    if (bf16) hipLaunchKernelGGL((router_kernel<decltype(v)::value, true>), grid, dim3(256), 0, s, a, ids, weights);
-    else hipLaunchKernelGGL((router_kernel<decltype(v)::value, false>), grid, dim3(256), 0, s, a, ids, weights);
+    constexpr int V = decltype(v)::value;
+    if (bf16) hipLaunchKernelGGL((router_exact_kernel<V, true>), grid, dim3(256), 0, s, a, ids, weights);
+    else hipLaunchKernelGGL((router_exact_kernel<V, false>), grid, dim3(256), 0, s, a, ids, weights);
   });
   return launched();
 }
@@ -70,9 +95,17 @@ moe_status_t launch_combine_bwd(const uint16_t* dout, const uint16_t* y, int M_c
 
 moe_status_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s) {
   if (a.T == 0) return MOE_OK;
-  for_chunks(a.H, [&](auto nc) {
-    hipLaunchKernelGGL((add_rmsnorm_kernel<decltype(nc)::value>), dim3(token_grid(a.T)), dim3(256), 0, s, a);
-  });
+  const dim3 grid(token_grid(a.T));
+  // few rows: 1024 threads, so that a row is in flight at once (1 row of 7168:
+  // 5.6 -> NORM1 us)
+  if (a.T <= 512 && a.H > 2048) {
+    if (a.H <= 8192) hipLaunchKernelGGL((add_rmsnorm_kernel<1024, 1>), grid, dim3(1024), 0, s, a);
+    else hipLaunchKernelGGL((add_rmsnorm_kernel<1024, 2>), grid, dim3(1024), 0, s, a);
+  } else {
+    for_chunks(a.H, [&](auto nc) {
+      hipLaunchKernelGGL((add_rmsnorm_kernel<256, decltype(nc)::value>), grid, dim3(256), 0, s, a);
+    });
+  }
   return launched();
 }
 
@@ -85,7 +118,7 @@ moe_status_t launch_add_rmsnorm_bwd(const NormBwdArgs& a, float* dweight, int ac
       hipLaunchKernelGGL((add_rmsnorm_bwd_kernel<decltype(nc)::value>), dim3((unsigned)parts), dim3(256), 0, s, a);
     });
   if (dweight)
-    hipLaunchKernelGGL(norm_dweight_kernel, dim3((unsigned)((a.H + 255) / 256)), dim3(256), 0, s, a.part,
+    hipLaunchKernelGGL(norm_dweight_kernel, dim3((unsigned)((a.H + 31) / 32)), dim3(256), 0, s, a.part,
                        parts, a.H, dweight, accumulate);
   return launched();
 }

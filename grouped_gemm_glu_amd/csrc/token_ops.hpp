@@ -43,24 +43,22 @@ __device__ __forceinline__ float load_logit(const void* p, long long i) {
   else return static_cast<const float*>(p)[i];
 }
 
-// One token per wave, experts lane, lane + 64, ...: k rounds of a wave-wide
-// maximum.  Scores and choice values are kept in 64 bits, so that the choice
-// is the one that the formulas make: in 32 bits the scores of neighbouring
-// logits round to one value and the order is lost.
+// One token by a whole wave, experts lane, lane + 64, ...: k rounds of a
+// wave-wide maximum.  Scores and choice values are kept in 64 bits, so that
+// the choice is the one that the formulas make: in 32 bits the scores of
+// neighbouring logits round to one value and the order is lost.  tmp: 64 VPL
+// doubles of LDS that are this wave's alone.
 template <int VPL, bool BF16>
-__global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restrict__ ids,
-                                                     float* __restrict__ weights) {
-  __shared__ double choice_lds[4][64 * VPL];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const long long tok = (long long)blockIdx.x * 4 + wave;
-  const bool tv = tok < p.T;
+__device__ void router_token_exact(const RouterArgs& p, long long tok, double* tmp, int* __restrict__ ids,
+                                   float* __restrict__ weights) {
+  const int lane = threadIdx.x & 63;
   float x[VPL];
   float m = -INFINITY;
   bool nan = false;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = lane + 64 * i;
-    x[i] = tv && e < p.E ? load_logit<BF16>(p.logits, tok * p.E + e) : -INFINITY;
+    x[i] = e < p.E ? load_logit<BF16>(p.logits, tok * p.E + e) : -INFINITY;
     m = fmaxf(m, x[i]);
     nan = nan || x[i] != x[i];
   }
@@ -94,14 +92,14 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
   if (p.n_groups > 1) {
     const int gsz = p.E / p.n_groups;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) choice_lds[wave][lane + 64 * i] = c[i];
-    __syncthreads();
+    for (int i = 0; i < VPL; ++i) tmp[lane + 64 * i] = c[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     unsigned long long key = 0;
     if (lane < p.n_groups) {
       double b0 = -INFINITY, b1 = -INFINITY;
       bool num = false, num2 = false;   // a first and a second number in the group
       for (int i = 0; i < gsz; ++i) {
-        const double v = choice_lds[wave][lane * gsz + i];
+        const double v = tmp[lane * gsz + i];
         if (v != v) continue;
         num2 = num2 || num;
         num = true;
@@ -110,6 +108,7 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
       if (p.top2) key = num2 ? rank_key(b0 + b1) : 1ull;
       else key = num ? rank_key(b0) : 1ull;
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // (tmp may be the next token's)
     int before = 0;
     for (int g = 0; g < p.n_groups; ++g) {
       const unsigned long long o = __shfl(key, g, 64);
@@ -149,11 +148,255 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
       if (lane + 64 * i == be) key[i] = 0;
     if (lane == j) { my_id = be; my_x = bx; }
   }
-  double s = lane < p.k ? score(my_x) : 0.0;
+  const double s = lane < p.k ? score(my_x) : 0.0;
   const double total = p.renorm ? wave_sum(s) : 1.0;
-  if (tv && lane < p.k) {
+  if (lane < p.k) {
     ids[tok * p.k + lane] = my_id;
     weights[tok * p.k + lane] = total == 0.0 ? 0.0f : (float)((double)p.scale * s / total);
+  }
+}
+
+// Every token by the exact routine: for what the fast kernel does not take
+// (E % 4 != 0, groups of other sizes than 4, 8, 16, ... experts).
+template <int VPL, bool BF16>
+__global__ __launch_bounds__(256) void router_exact_kernel(RouterArgs p, int* __restrict__ ids,
+                                                           float* __restrict__ weights) {
+  __shared__ double tmp[4][64 * VPL];
+  const int wave = threadIdx.x >> 6;
+  const long long tok = (long long)blockIdx.x * 4 + wave;
+  if (tok < p.T) router_token_exact<VPL, BF16>(p, tok, tmp[wave], ids, weights);
+}
+
+// Maximum (minimum) over the L lanes of a token, which all get it: rotations
+// within each row of 16 lanes, then across the rows.
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false));   // row_ror:8
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xF, 0xF, false));
+  if constexpr (L >= 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
+  if constexpr (L >= 64) v = max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ int lanes_min(int v) { return (int)~lanes_max<L>(~(uint32_t)v); }
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < L; d <<= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+// As rank_key, of 32-bit values.
+__device__ __forceinline__ uint32_t rank_key32(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return v != v ? 1u : ((b >> 31) ? ~b : (b | 0x80000000u));
+}
+__device__ __forceinline__ float of_rank_key32(uint32_t k) {
+  return k <= 1u ? __builtin_nanf("") : __uint_as_float((k >> 31) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+// 64 / L tokens per wave, L lanes each; lane l holds experts 4 (l + L i) .. + 3, i
+// < NI.  The choice is made on 32-bit values: without a bias (and without sums
+// of scores for groups) these are the logits, and exact.  Where scores decide,
+// their 32-bit forms are off by at most 2^-21.4 max(1, |c|) for a sigmoid (its
+// exponential by (|x| + 2) 2^-24 of itself, s (1 - s) |x| <= 0.23, a quotient and
+// two sums), 2^-19 for a softmax (a sum of E terms, in 20 roundings); a token
+// with two neighbours among its k + 1 best closer than four times that, or
+// groups that close at the border, is done again in 64 bits by the whole wave.
+// Bound by instructions: a round of the choice is about 80 for 64 / L tokens.
+template <int L, int NI, bool BF16>
+__global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restrict__ ids,
+                                                     float* __restrict__ weights) {
+  constexpr int VPL = (L * NI * 4 + 63) / 64;   // experts per lane of the exact routine
+  __shared__ double tmp[4][64 * VPL];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & (L - 1);
+  const long long tok0 = ((long long)blockIdx.x * 4 + wave) * (64 / L);
+  const long long tok = tok0 + lane / L;
+  const bool tv = tok < p.T;
+  float x[NI][4], c[NI][4];
+  float m = -INFINITY;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int e = 4 * (l + L * i);
+    if (tv && e < p.E) {   // (E % 4 == 0: whole quads)
+      if constexpr (BF16) {
+        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.logits) + tok * p.E + e);
+        x[i][0] = __uint_as_float(u.x << 16);
+        x[i][1] = __uint_as_float(u.x & 0xFFFF0000u);
+        x[i][2] = __uint_as_float(u.y << 16);
+        x[i][3] = __uint_as_float(u.y & 0xFFFF0000u);
+      } else {
+        const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(p.logits) + tok * p.E + e);
+        x[i][0] = u.x;
+        x[i][1] = u.y;
+        x[i][2] = u.z;
+        x[i][3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[i][q] = -INFINITY;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      m = fmaxf(m, x[i][q]);
+      nan = nan || x[i][q] != x[i][q];
+    }
+  }
+  const bool by_score = p.bias != nullptr || (p.n_groups > 1 && p.top2);
+  // softmax: maximum and, where the scores themselves count, the row's sum
+  float inv = 1.0f;
+  bool empty = false;
+  if (!p.sigmoid) {
+    m = of_rank_key32(lanes_max<L>(rank_key32(m)));
+    const bool any_nan = lanes_max<L>(nan ? 1u : 0u) != 0u;
+    empty = m == -INFINITY && !any_nan;
+    float sum = any_nan ? __builtin_nanf("") : 1.0f;
+    if (by_score || !p.renorm) {
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (4 * (l + L * i) < p.E) sum += __expf(x[i][q] - m);
+      sum = lanes_sum<L>(sum);
+    }
+    inv = 1.0f / sum;
+  }
+  auto score = [&](float v) -> float {
+    if (p.sigmoid) return __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+    return empty ? 0.0f : __expf(v - m) * inv;
+  };
+  bool redo = false;
+  // the relative width within which 32-bit choice values say nothing
+  const float tol = p.sigmoid ? 0x1p-19f : 0x1p-17f;
+  auto close = [&](float hi, float lo) {   // (true for NaN)
+    return !(hi - lo > tol * fmaxf(1.0f, fmaxf(fabsf(hi), fabsf(lo))));
+  };
+  if (by_score) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int e = 4 * (l + L * i);
+      float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (p.bias && e < p.E) __builtin_memcpy(b, p.bias + e, 16);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) c[i][q] = score(x[i][q]) + b[q];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) c[i][q] = x[i][q];
+  }
+  uint32_t open = (1u << NI) - 1;   // bit i: this lane's quad i takes part
+  if (p.n_groups > 1) {
+    // a group is W = size / 4 neighbouring lanes' quads i (W a power of two up to
+    // L): the two best values of the quad, then of the W lanes
+    const int W = p.E / p.n_groups / 4, sh = __builtin_ctz(W);
+    float value[NI];
+    uint32_t key[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      float b0 = fmaxf(c[i][0], c[i][1]), b1 = fminf(c[i][0], c[i][1]);
+      const float d0 = fmaxf(c[i][2], c[i][3]), d1 = fminf(c[i][2], c[i][3]);
+      b1 = fmaxf(fminf(b0, d0), fmaxf(b1, d1));
+      b0 = fmaxf(b0, d0);
+      for (int d = 1; d < W; d <<= 1) {
+        const float o0 = __shfl_xor(b0, d, 64), o1 = __shfl_xor(b1, d, 64);
+        b1 = fmaxf(fminf(b0, o0), fmaxf(b1, o1));
+        b0 = fmaxf(b0, o0);
+      }
+      // (fmax and fmin drop a NaN: such rows are done again below)
+      value[i] = p.top2 ? b0 + b1 : b0;
+      key[i] = 4 * (l + L * i) < p.E ? rank_key32(value[i]) : 0u;
+    }
+    redo = lanes_max<L>(nan ? 1u : 0u) != 0u;
+    // the kept groups, best first, ties to the lower id; the last kept and the
+    // first left out tell whether 32 bits decide
+    open = 0;
+    float last = 0.0f;
+    for (int g = 0; g <= p.topk_groups; ++g) {
+      uint32_t b = 0;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) b = max(b, key[i]);
+      b = lanes_max<L>(b);
+      if (g == p.topk_groups) {
+        if (by_score && b != 0u && close(last, of_rank_key32(b))) redo = true;
+        break;
+      }
+      int at = 0x7FFFFFFF;   // group id
+#pragma unroll
+      for (int i = NI - 1; i >= 0; --i)
+        if (key[i] == b) at = (l + L * i) >> sh;
+      at = lanes_min<L>(at);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if ((l + L * i) >> sh == at) {
+          key[i] = 0;
+          open |= 1u << i;
+        }
+      last = of_rank_key32(b);
+    }
+    if (!p.bias && p.top2) {   // without a bias the experts' order is the logits'
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c[i][q] = x[i][q];
+    }
+  }
+  const bool check = p.bias != nullptr;   // the choice among experts is by scores
+  uint32_t key[NI][4];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      key[i][q] = ((open >> i) & 1u) && 4 * (l + L * i) < p.E ? rank_key32(c[i][q]) : 0u;
+  int my_id = 0;
+  float last = 0.0f;
+  for (int j = 0; j < p.k + (check ? 1 : 0); ++j) {
+    uint32_t b = 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) b = max(max(b, max(key[i][0], key[i][1])), max(key[i][2], key[i][3]));
+    b = lanes_max<L>(b);
+    if (check) {
+      const float v = of_rank_key32(b);
+      if (j > 0 && b != 0u && close(last, v)) redo = true;
+      last = v;
+      if (j == p.k) break;
+    }
+    int at = 0x7FFFFFFF;
+#pragma unroll
+    for (int i = NI - 1; i >= 0; --i)
+#pragma unroll
+      for (int q = 3; q >= 0; --q) at = key[i][q] == b ? 4 * (l + L * i) + q : at;
+    at = lanes_min<L>(at);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) key[i][q] = 4 * (l + L * i) + q == at ? 0u : key[i][q];
+    if (l == j) my_id = at;
+  }
+  const bool sel = tv && l < p.k;
+  float s = 0.0f;
+  bool tiny = false;   // a score near or below what fp32 holds: its ratio to the others may still count
+  if (sel) {
+    const float v = load_logit<BF16>(p.logits, tok * p.E + my_id);
+    s = p.sigmoid ? 1.0f / (1.0f + expf(-v)) : (empty ? 0.0f : expf(v - m) * inv);
+    tiny = s < 1e-30f && v != -INFINITY && !empty;
+  }
+  redo = redo || lanes_max<L>(tiny ? 1u : 0u) != 0u;
+  const float total = p.renorm ? lanes_sum<L>(s) : 1.0f;
+  if (sel && !redo) {
+    ids[tok * p.k + l] = my_id;
+    weights[tok * p.k + l] = total == 0.0f ? 0.0f : p.scale * s / total;
+  }
+  unsigned long long again = __ballot(tv && redo && l == 0);
+  while (again) {
+    const int at = __builtin_ctzll(again);
+    again &= again - 1;
+    router_token_exact<VPL, BF16>(p, tok0 + at / L, tmp[wave], ids, weights);
   }
 }
 
@@ -355,22 +598,27 @@ __device__ __forceinline__ float block_sum(float v, float* tmp) {
   return s;
 }
 
-// One workgroup of 256 threads per row, NC chunks of 8 columns per thread.
+// One workgroup of NT threads per row, NC chunks of 8 columns per thread.
 // h = bf16(x + residual) is what the residual stream keeps and what the norm
 // is taken of, so that the backward pass sees the same values; y is rounded
 // once, and the MXFP8 copy is the rounded y's (as the GEMM epilogues do).
-template <int NC>
-__global__ __launch_bounds__(256) void add_rmsnorm_kernel(NormArgs p) {
-  __shared__ float tmp[4];
+// Bound by memory: 16384 x 7168 with residual and MXFP8 copy 0.20 ms, 5.3 TB/s,
+// the rate of a large copy; one row is one round trip to memory (the weights
+// are fetched with the row) and a workgroup-wide sum.
+template <int NT, int NC>
+__global__ __launch_bounds__(NT) void add_rmsnorm_kernel(NormArgs p) {
+  __shared__ float tmp[NT / 64];
   const int nch = p.H >> 3;
   for (long long r = blockIdx.x; r < p.T; r += gridDim.x) {
+    uint4 wt[NC];
     float v[NC][8];
     float sq = 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int ch = c * 256 + threadIdx.x;
+      const int ch = c * NT + threadIdx.x;
       if (ch >= nch) continue;
       const long long at = r * p.H + ch * 8;
+      wt[c] = *reinterpret_cast<const uint4*>(p.weight + ch * 8);
       unpack8(*reinterpret_cast<const uint4*>(p.x + at), v[c]);
       if (p.residual) {
         float w[8];
@@ -386,15 +634,15 @@ __global__ __launch_bounds__(256) void add_rmsnorm_kernel(NormArgs p) {
 #pragma unroll
       for (int q = 0; q < 8; ++q) sq = fmaf(v[c][q], v[c][q], sq);
     }
-    const float rstd = 1.0f / sqrtf(block_sum<4>(sq, tmp) / (float)p.H + p.eps);
+    const float rstd = 1.0f / sqrtf(block_sum<NT / 64>(sq, tmp) / (float)p.H + p.eps);
     if (p.rstd && threadIdx.x == 0) p.rstd[r] = rstd;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int ch = c * 256 + threadIdx.x;
+      const int ch = c * NT + threadIdx.x;
       if (ch >= nch) continue;   // (with p.q a row is whole blocks of 4 lanes)
       const long long at = r * p.H + ch * 8;
       float w[8];
-      unpack8(*reinterpret_cast<const uint4*>(p.weight + ch * 8), w);
+      unpack8(wt[c], w);
 #pragma unroll
       for (int q = 0; q < 8; ++q) w[q] = v[c][q] * rstd * w[q];
       const uint4 yv = pack8(w);
@@ -439,50 +687,65 @@ __global__ __launch_bounds__(256) void add_rmsnorm_kernel(NormArgs p) {
 
 // With n = h rstd and g = dy weight: dx = rstd (g - n mean(g n)) + dh, and
 // dweight = sum over rows of dy n.  Each workgroup takes rows blockIdx.x +
-// i gridDim.x and keeps its columns' share of dweight in registers; the
-// shares are added in a fixed order by the kernel below.
+// i gridDim.x, the next one's loads going out before the current one's sum, and
+// keeps its columns' share of dweight in registers; the shares are added in a
+// fixed order by the kernel below.  Bound by memory.
 template <int NC>
 __global__ __launch_bounds__(256) void add_rmsnorm_bwd_kernel(NormBwdArgs p) {
   __shared__ float tmp[4];
   const int nch = p.H >> 3;
-  float dwt[NC][8];
-#pragma unroll
-  for (int c = 0; c < NC; ++c)
-#pragma unroll
-    for (int q = 0; q < 8; ++q) dwt[c][q] = 0.0f;
-  for (long long r = blockIdx.x; r < p.T; r += gridDim.x) {
-    const float rstd = p.rstd[r];
-    float n[NC][8], g[NC][8];
-    float dot = 0.0f;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  float dwt[NC][8], w[NC][8];
+  uint4 dy[NC], h[NC], dh[NC];
+  float rstd = 0.0f;
+  auto fetch = [&](long long r) {
+    rstd = p.rstd[r];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int ch = c * 256 + threadIdx.x;
+      dy[c] = h[c] = dh[c] = zero;
       if (ch >= nch) continue;
       const long long at = r * p.H + ch * 8;
-      float w[8];
-      unpack8(*reinterpret_cast<const uint4*>(p.dy + at), g[c]);
-      unpack8(*reinterpret_cast<const uint4*>(p.h + at), n[c]);
-      unpack8(*reinterpret_cast<const uint4*>(p.weight + ch * 8), w);
+      dy[c] = *reinterpret_cast<const uint4*>(p.dy + at);
+      h[c] = *reinterpret_cast<const uint4*>(p.h + at);
+      if (p.dx && p.dh) dh[c] = *reinterpret_cast<const uint4*>(p.dh + at);
+    }
+  };
+  if (blockIdx.x < p.T) fetch(blockIdx.x);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int ch = c * 256 + threadIdx.x;
+    unpack8(ch < nch ? *reinterpret_cast<const uint4*>(p.weight + ch * 8) : zero, w[c]);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) dwt[c][q] = 0.0f;
+  }
+  for (long long r = blockIdx.x; r < p.T; r += gridDim.x) {
+    float n[NC][8], g[NC][8], d[NC][8];
+    const float rs = rstd;
+    float dot = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      unpack8(dy[c], g[c]);
+      unpack8(h[c], n[c]);
+      unpack8(dh[c], d[c]);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        n[c][q] *= rstd;
+        n[c][q] *= rs;
         dwt[c][q] = fmaf(g[c][q], n[c][q], dwt[c][q]);
-        g[c][q] *= w[q];
+        g[c][q] *= w[c][q];
         dot = fmaf(g[c][q], n[c][q], dot);
       }
     }
+    if (r + gridDim.x < p.T) fetch(r + gridDim.x);
     if (!p.dx) continue;
     const float mean = block_sum<4>(dot, tmp) / (float)p.H;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int ch = c * 256 + threadIdx.x;
       if (ch >= nch) continue;
-      const long long at = r * p.H + ch * 8;
-      float d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (p.dh) unpack8(*reinterpret_cast<const uint4*>(p.dh + at), d);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) d[q] += rstd * (g[c][q] - n[c][q] * mean);
-      *reinterpret_cast<uint4*>(p.dx + at) = pack8(d);
+      for (int q = 0; q < 8; ++q) d[c][q] += rs * (g[c][q] - n[c][q] * mean);
+      *reinterpret_cast<uint4*>(p.dx + r * p.H + ch * 8) = pack8(d[c]);
     }
   }
   if (p.part) {
@@ -497,15 +760,35 @@ __global__ __launch_bounds__(256) void add_rmsnorm_bwd_kernel(NormBwdArgs p) {
   }
 }
 
-// dweight[col] (+)= the sum of nparts partial rows, in a fixed order.
+// dweight (+)= the sum of nparts partial rows, in a fixed order: a workgroup
+// takes 32 columns (8 threads of 4), thread group g of 32 the rows g, g + 32,
+// ..., whose sums are then added in order of g.
 __global__ __launch_bounds__(256) void norm_dweight_kernel(const float* __restrict__ part, int nparts,
                                                            int H, float* __restrict__ dweight,
                                                            int accumulate) {
-  const int col = blockIdx.x * 256 + threadIdx.x;
-  if (col >= H) return;
-  float s = accumulate ? dweight[col] : 0.0f;
-  for (int i = 0; i < nparts; ++i) s += part[(long long)i * H + col];
-  dweight[col] = s;
+  __shared__ float4 sums[32][8];
+  const int cl = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const int col = blockIdx.x * 32 + cl * 4;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (col < H) {   // (H is a multiple of 8)
+#pragma unroll 8
+    for (int i = g; i < nparts; i += 32) {
+      const float4 v = *reinterpret_cast<const float4*>(part + (long long)i * H + col);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+  }
+  sums[g][cl] = s;
+  __syncthreads();
+  if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < H) {
+    const int c = threadIdx.x;
+    float* o = dweight + blockIdx.x * 32 + c;
+    float t = accumulate ? *o : 0.0f;
+    for (int i = 0; i < 32; ++i) t += reinterpret_cast<const float*>(&sums[i][c >> 2])[c & 3];
+    *o = t;
+  }
 }
 
 }  // namespace moe

@@ -104,7 +104,8 @@ def _check_grad(got, v, ids, dw, R, bf16, score="softmax", renorm=True, scale=1.
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("T,E,k", [(0, 8, 2), (1, 1, 1), (3, 5, 5), (257, 64, 6), (70, 65, 8), (33, 200, 16),
-                                   (19, 256, 8), (9, 513, 3), (6, 1024, 16)])
+                                   (19, 256, 8), (9, 513, 3), (6, 1024, 16), (1030, 128, 4), (75, 512, 8),
+                                   (21, 36, 16)])
 def test_router_sizes(G, T, E, k, score, bf16):
     rng = np.random.default_rng(T + E + k)
     x = rng.standard_normal((T, E)) * 2
@@ -115,7 +116,7 @@ def test_router_sizes(G, T, E, k, score, bf16):
 @pytest.mark.parametrize("score,group_score", [("softmax", "max"), ("softmax", "top2"), ("sigmoid", "max"),
                                                ("sigmoid", "top2")])
 @pytest.mark.parametrize("with_bias", [False, True])
-@pytest.mark.parametrize("T,E,k,groups,keep", [(61, 256, 8, 8, 4), (40, 160, 6, 8, 3), (30, 12, 3, 4, 1),
+@pytest.mark.parametrize("T,E,k,groups,keep", [(61, 256, 8, 8, 4), (40, 160, 6, 8, 3), (33, 512, 10, 4, 2), (30, 12, 3, 4, 1),
                                                (20, 128, 2, 64, 1), (15, 1024, 16, 16, 16), (25, 21, 7, 3, 2)])
 def test_router_groups_and_bias(G, T, E, k, groups, keep, with_bias, score, group_score):
     if group_score == "top2" and E // groups < 2:
@@ -225,3 +226,16 @@ def test_router_gradient_against_differences(G):
         G.moe_router_topk_bwd(lg, 1, E, k, r, torch.from_numpy(ids0).cuda(), torch.from_numpy(dw[None]).cuda(), d)
         torch.cuda.synchronize()
         assert np.max(np.abs(d.cpu().numpy()[0] - num)) <= h * h / 6 * 10 * np.abs(dw).sum() + 1e-5
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_router_small_scores_beside_a_bias(G, score):
+    """A bias that decides for experts whose scores fp32 does not hold, or only just: their weights are still the
+    ratios of the scores."""
+    E = 64
+    rng = np.random.default_rng(14)
+    x = (rng.standard_normal((24, E)) * 2).astype(np.float32)
+    x[:, :8] -= np.linspace(0, 230, 24, dtype=np.float32)[:, None]
+    bias = np.where(np.arange(E) < 8, 2.0, 0.0).astype(np.float32)
+    _run(G, x, 4, False, bias, None, score=score)
+    _run(G, x, 4, False, bias, None, score=score, renorm=False)
