@@ -21,20 +21,61 @@ __device__ __forceinline__ unsigned long long rank_key(double v) {
   return v != v ? 1ull : s;
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+// Another lane's value by data-parallel primitives (a few cycles each, where a
+// shuffle through LDS takes over a hundred); rows not in ROWS get `other`.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ uint32_t dpp(uint32_t v, uint32_t other = 0) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)other, (int)v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float dpp(float v, float other = 0.0f) {
+  return __uint_as_float(dpp<CTRL, ROWS>(__float_as_uint(v), __float_as_uint(other)));
+}
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ double dpp(double v) {
+  const unsigned long long b = __builtin_bit_cast(unsigned long long, v);
+  const unsigned long long o = (unsigned long long)dpp<CTRL, ROWS>((uint32_t)(b >> 32)) << 32 |
+                               dpp<CTRL, ROWS>((uint32_t)b);
+  return __builtin_bit_cast(double, o);
+}
+__device__ __forceinline__ uint32_t lane63(uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 63); }
+
+// Over a whole wave (all lanes active): rotations within the rows of 16 lanes,
+// then lane 15 of rows 0 and 2 to rows 1 and 3, lane 31 to rows 2 and 3.
+template <class V>
+__device__ __forceinline__ V wave_sum_to_lane63(V v) {
+  v += dpp<0x128>(v);
+  v += dpp<0x124>(v);
+  v += dpp<0x122>(v);
+  v += dpp<0x121>(v);
+  v += dpp<0x142, 0xA>(v);
+  v += dpp<0x143, 0xC>(v);
   return v;
 }
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
+  return __uint_as_float(lane63(__float_as_uint(wave_sum_to_lane63(v))));
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  const unsigned long long b = __builtin_bit_cast(unsigned long long, wave_sum_to_lane63(v));
+  return __builtin_bit_cast(double, (unsigned long long)lane63((uint32_t)(b >> 32)) << 32 | lane63((uint32_t)b));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, dpp<0x128>(v));
+  v = max(v, dpp<0x124>(v));
+  v = max(v, dpp<0x122>(v));
+  v = max(v, dpp<0x121>(v));
+  v = max(v, dpp<0x142, 0xA>(v));
+  v = max(v, dpp<0x143, 0xC>(v));
+  return lane63(v);
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-  return v;
+  v = fmaxf(v, dpp<0x128>(v));
+  v = fmaxf(v, dpp<0x124>(v));
+  v = fmaxf(v, dpp<0x122>(v));
+  v = fmaxf(v, dpp<0x121>(v));
+  v = fmaxf(v, dpp<0x142, 0xA>(v, -INFINITY));
+  v = fmaxf(v, dpp<0x143, 0xC>(v, -INFINITY));
+  return __uint_as_float(lane63(__float_as_uint(v)));
 }
 
 template <bool BF16>
@@ -98,12 +139,15 @@ __device__ void router_token_exact(const RouterArgs& p, long long tok, double* t
     if (lane < p.n_groups) {
       double b0 = -INFINITY, b1 = -INFINITY;
       bool num = false, num2 = false;   // a first and a second number in the group
+#pragma unroll 8
       for (int i = 0; i < gsz; ++i) {
-        const double v = tmp[lane * gsz + i];
-        if (v != v) continue;
-        num2 = num2 || num;
-        num = true;
-        if (v > b0) { b1 = b0; b0 = v; } else if (v > b1) b1 = v;
+        double v = tmp[lane * gsz + i];
+        const bool is = v == v;
+        v = is ? v : -INFINITY;
+        num2 = num2 || (num && is);
+        num = num || is;
+        b1 = fmax(b1, fmin(b0, v));
+        b0 = fmax(b0, v);
       }
       if (p.top2) key = num2 ? rank_key(b0 + b1) : 1ull;
       else key = num ? rank_key(b0) : 1ull;
@@ -128,26 +172,23 @@ __device__ void router_token_exact(const RouterArgs& p, long long tok, double* t
     key[i] = in ? rank_key(c[i]) : 0ull;
   }
   int my_id = 0;
-  float my_x = 0.0f;
   for (int j = 0; j < p.k; ++j) {
-    unsigned long long bk = 0;
-    int be = 0x7FFFFFFF;
-    float bx = 0.0f;
+    unsigned long long b = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) b = key[i] > b ? key[i] : b;
+    const uint32_t hi = wave_max((uint32_t)(b >> 32));
+    const uint32_t lo = wave_max((uint32_t)(b >> 32) == hi ? (uint32_t)b : 0u);
+    b = (unsigned long long)hi << 32 | lo;
+    uint32_t at = 0;   // ~expert: the lowest of equals
+#pragma unroll
+    for (int i = VPL - 1; i >= 0; --i) at = key[i] == b ? ~(uint32_t)(lane + 64 * i) : at;
+    const int e = (int)~wave_max(at);
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (key[i] > bk) { bk = key[i]; be = lane + 64 * i; bx = x[i]; }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-      const unsigned long long ok = __shfl_xor(bk, d, 64);
-      const int oe = __shfl_xor(be, d, 64);
-      const float ox = __shfl_xor(bx, d, 64);
-      if (ok > bk || (ok == bk && oe < be)) { bk = ok; be = oe; bx = ox; }
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane + 64 * i == be) key[i] = 0;
-    if (lane == j) { my_id = be; my_x = bx; }
+      if (lane + 64 * i == e) key[i] = 0;
+    if (lane == j) my_id = e;
   }
+  const float my_x = lane < p.k ? load_logit<BF16>(p.logits, tok * p.E + my_id) : 0.0f;
   const double s = lane < p.k ? score(my_x) : 0.0;
   const double total = p.renorm ? wave_sum(s) : 1.0;
   if (lane < p.k) {
@@ -171,10 +212,10 @@ __global__ __launch_bounds__(256) void router_exact_kernel(RouterArgs p, int* __
 // within each row of 16 lanes, then across the rows.
 template <int L>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false));   // row_ror:8
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, false));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xF, 0xF, false));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xF, 0xF, false));
+  v = max(v, dpp<0x128>(v));
+  v = max(v, dpp<0x124>(v));
+  v = max(v, dpp<0x122>(v));
+  v = max(v, dpp<0x121>(v));
   if constexpr (L >= 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
   if constexpr (L >= 64) v = max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
   return v;
@@ -183,8 +224,13 @@ template <int L>
 __device__ __forceinline__ int lanes_min(int v) { return (int)~lanes_max<L>(~(uint32_t)v); }
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < L; d <<= 1) v += __shfl_xor(v, d, 64);
+  static_assert(L >= 16, "rows of 16 lanes");
+  v += dpp<0x128>(v);
+  v += dpp<0x124>(v);
+  v += dpp<0x122>(v);
+  v += dpp<0x121>(v);
+  if constexpr (L >= 32) v += __shfl_xor(v, 16, 64);
+  if constexpr (L >= 64) v += __shfl_xor(v, 32, 64);
   return v;
 }
 
@@ -202,9 +248,10 @@ __device__ __forceinline__ float of_rank_key32(uint32_t k) {
 // of scores for groups) these are the logits, and exact.  Where scores decide,
 // their 32-bit forms are off by at most 2^-21.4 max(1, |c|) for a sigmoid (its
 // exponential by (|x| + 2) 2^-24 of itself, s (1 - s) |x| <= 0.23, a quotient and
-// two sums), 2^-19 for a softmax (a sum of E terms, in 20 roundings); a token
-// with two neighbours among its k + 1 best closer than four times that, or
-// groups that close at the border, is done again in 64 bits by the whole wave.
+// two sums), 2^-19.5 for a softmax (a sum of E terms, in 20 roundings); a token
+// with two neighbours among its k + 1 best closer than twice that (and a
+// little), or groups closer than four times that at the border, is done again
+// in 64 bits by the whole wave.
 // Bound by instructions: a round of the choice is about 80 for 64 / L tokens.
 template <int L, int NI, bool BF16>
 __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restrict__ ids,
@@ -215,12 +262,15 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
   const long long tok0 = ((long long)blockIdx.x * 4 + wave) * (64 / L);
   const long long tok = tok0 + lane / L;
   const bool tv = tok < p.T;
-  float x[NI][4], c[NI][4];
+  const bool by_score = p.bias != nullptr || (p.n_groups > 1 && p.top2);
+  float x[NI][4], c[NI][4];   // (c: the bias first)
   float m = -INFINITY;
   bool nan = false;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int e = 4 * (l + L * i);
+    c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.0f;
+    if (p.bias && e < p.E) __builtin_memcpy(c[i], p.bias + e, 16);
     if (tv && e < p.E) {   // (E % 4 == 0: whole quads)
       if constexpr (BF16) {
         const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.logits) + tok * p.E + e);
@@ -239,13 +289,14 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
 #pragma unroll
       for (int q = 0; q < 4; ++q) x[i][q] = -INFINITY;
     }
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       m = fmaxf(m, x[i][q]);
       nan = nan || x[i][q] != x[i][q];
     }
-  }
-  const bool by_score = p.bias != nullptr || (p.n_groups > 1 && p.top2);
   // softmax: maximum and, where the scores themselves count, the row's sum
   float inv = 1.0f;
   bool empty = false;
@@ -265,37 +316,28 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
     }
     inv = 1.0f / sum;
   }
-  auto score = [&](float v) -> float {
-    if (p.sigmoid) return __builtin_amdgcn_rcpf(1.0f + __expf(-v));
-    return empty ? 0.0f : __expf(v - m) * inv;
-  };
   bool redo = false;
   // the relative width within which 32-bit choice values say nothing
-  const float tol = p.sigmoid ? 0x1p-19f : 0x1p-17f;
-  auto close = [&](float hi, float lo) {   // (true for NaN)
+  // (for a group's sum of two scores, and for one score)
+  const float tol2 = p.sigmoid ? 0x1p-19f : 0x1p-17f, tol1 = p.sigmoid ? 0x1p-20f : 0x1p-18f;
+  auto close = [](float hi, float lo, float tol) {   // (true for NaN)
     return !(hi - lo > tol * fmaxf(1.0f, fmaxf(fabsf(hi), fabsf(lo))));
   };
-  if (by_score) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int e = 4 * (l + L * i);
-      float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (p.bias && e < p.E) __builtin_memcpy(b, p.bias + e, 16);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) c[i][q] = score(x[i][q]) + b[q];
-    }
-  } else {
+  auto each = [&](auto f) {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) c[i][q] = x[i][q];
-  }
+      for (int q = 0; q < 4; ++q) c[i][q] = f(x[i][q], c[i][q]);
+  };
+  if (!by_score) each([](float v, float) { return v; });
+  else if (p.sigmoid) each([](float v, float b) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)) + b; });
+  else if (!empty) each([=](float v, float b) { return fmaf(__expf(v - m), inv, b); });
   uint32_t open = (1u << NI) - 1;   // bit i: this lane's quad i takes part
   if (p.n_groups > 1) {
     // a group is W = size / 4 neighbouring lanes' quads i (W a power of two up to
     // L): the two best values of the quad, then of the W lanes
     const int W = p.E / p.n_groups / 4, sh = __builtin_ctz(W);
-    float value[NI];
+    float v0[NI], v1[NI];
     uint32_t key[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -303,15 +345,29 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
       const float d0 = fmaxf(c[i][2], c[i][3]), d1 = fminf(c[i][2], c[i][3]);
       b1 = fmaxf(fminf(b0, d0), fmaxf(b1, d1));
       b0 = fmaxf(b0, d0);
-      for (int d = 1; d < W; d <<= 1) {
-        const float o0 = __shfl_xor(b0, d, 64), o1 = __shfl_xor(b1, d, 64);
-        b1 = fmaxf(fminf(b0, o0), fmaxf(b1, o1));
-        b0 = fmaxf(b0, o0);
-      }
-      // (fmax and fmin drop a NaN: such rows are done again below)
-      value[i] = p.top2 ? b0 + b1 : b0;
-      key[i] = 4 * (l + L * i) < p.E ? rank_key32(value[i]) : 0u;
+      v0[i] = b0;
+      v1[i] = b1;
     }
+    auto merge = [&](auto other) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const float o0 = other(v0[i]), o1 = other(v1[i]);
+        v1[i] = fmaxf(fminf(v0[i], o0), fmaxf(v1[i], o1));
+        v0[i] = fmaxf(v0[i], o0);
+      }
+    };
+    // lane ^ 1, ^ 2 by quad permutes; then, the quads being alike, the mirrors
+    // of 8 and of 16 lanes reach the other quad, the other half row
+    if (W > 1) merge([](float v) { return dpp<0xB1>(v); });
+    if (W > 2) merge([](float v) { return dpp<0x4E>(v); });
+    if (W > 4) merge([](float v) { return dpp<0x141>(v); });
+    if (W > 8) merge([](float v) { return dpp<0x140>(v); });
+    if (W > 16) merge([](float v) { return __shfl_xor(v, 16, 64); });
+    if (W > 32) merge([](float v) { return __shfl_xor(v, 32, 64); });
+    // (fmax and fmin drop a NaN: such rows are done again below)
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      key[i] = 4 * (l + L * i) < p.E ? rank_key32(p.top2 ? v0[i] + v1[i] : v0[i]) : 0u;
     redo = lanes_max<L>(nan ? 1u : 0u) != 0u;
     // the kept groups, best first, ties to the lower id; the last kept and the
     // first left out tell whether 32 bits decide
@@ -323,7 +379,7 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
       for (int i = 0; i < NI; ++i) b = max(b, key[i]);
       b = lanes_max<L>(b);
       if (g == p.topk_groups) {
-        if (by_score && b != 0u && close(last, of_rank_key32(b))) redo = true;
+        if (by_score && b != 0u && close(last, of_rank_key32(b), tol2)) redo = true;
         break;
       }
       int at = 0x7FFFFFFF;   // group id
@@ -362,7 +418,7 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
     b = lanes_max<L>(b);
     if (check) {
       const float v = of_rank_key32(b);
-      if (j > 0 && b != 0u && close(last, v)) redo = true;
+      if (j > 0 && b != 0u && close(last, v, tol1)) redo = true;
       last = v;
       if (j == p.k) break;
     }
@@ -461,8 +517,8 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs p, const int
     const int e = lane + 64 * i;
     float v = full && !empty && e < p.E ? -(expf(x[i] - m) / sum) * dot : 0.0f;
     for (int j = 0; j < p.k; ++j) {
-      const int ej = __shfl(id, j, 64);
-      const float dj = __shfl(d, j, 64);
+      const int ej = __builtin_amdgcn_readlane(id, j);
+      const float dj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(d), j));
       v += ej == e ? dj : 0.0f;
     }
     if (e < p.E) {
@@ -488,6 +544,7 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 
 // out[t] = residual[t] + sum_j w[t][j] y[dst[t][j]], the terms added in slot
 // order in fp32 and rounded once.  One thread per 8 columns of a token.
+constexpr int kCombineRows = 4;
 __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict__ y, int M_cap, int H,
                                                       const int* __restrict__ dst,
                                                       const float* __restrict__ weights, int T, int k,
@@ -498,14 +555,26 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
   for (long long t = blockIdx.x; t < T; t += gridDim.x) {
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (residual) unpack8(*reinterpret_cast<const uint4*>(residual + t * H + ch * 8), acc);
-    for (int j = 0; j < k; ++j) {
-      const int r = dst[t * k + j];
-      if (r < 0 || r >= M_cap) continue;
-      const float w = weights ? weights[t * k + j] : 1.0f;
-      float v[8];
-      unpack8(*reinterpret_cast<const uint4*>(y + (long long)r * H + ch * 8), v);
+    for (int j0 = 0; j0 < k; j0 += kCombineRows) {
+      uint4 v[kCombineRows];
+      float w[kCombineRows];
+      bool there[kCombineRows];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) acc[q] = fmaf(w, v[q], acc[q]);
+      for (int j = 0; j < kCombineRows; ++j) {
+        const int r = j0 + j < k ? dst[t * k + j0 + j] : -1;
+        there[j] = r >= 0 && r < M_cap;
+        if (!there[j]) continue;
+        w[j] = weights ? weights[t * k + j0 + j] : 1.0f;
+        v[j] = *reinterpret_cast<const uint4*>(y + (long long)r * H + ch * 8);
+      }
+#pragma unroll
+      for (int j = 0; j < kCombineRows; ++j) {
+        if (!there[j]) continue;
+        float f[8];
+        unpack8(v[j], f);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[q] = fmaf(w[j], f[q], acc[q]);
+      }
     }
     *reinterpret_cast<uint4*>(out + t * H + ch * 8) = pack8(acc);
   }
@@ -608,6 +677,7 @@ __device__ __forceinline__ float block_sum(float v, float* tmp) {
 template <int NT, int NC>
 __global__ __launch_bounds__(NT) void add_rmsnorm_kernel(NormArgs p) {
   __shared__ float tmp[NT / 64];
+  constexpr bool kEarly = NT == 1024;
   const int nch = p.H >> 3;
   for (long long r = blockIdx.x; r < p.T; r += gridDim.x) {
     uint4 wt[NC];
@@ -618,7 +688,7 @@ __global__ __launch_bounds__(NT) void add_rmsnorm_kernel(NormArgs p) {
       const int ch = c * NT + threadIdx.x;
       if (ch >= nch) continue;
       const long long at = r * p.H + ch * 8;
-      wt[c] = *reinterpret_cast<const uint4*>(p.weight + ch * 8);
+      if (kEarly) wt[c] = *reinterpret_cast<const uint4*>(p.weight + ch * 8);
       unpack8(*reinterpret_cast<const uint4*>(p.x + at), v[c]);
       if (p.residual) {
         float w[8];
@@ -642,7 +712,7 @@ __global__ __launch_bounds__(NT) void add_rmsnorm_kernel(NormArgs p) {
       if (ch >= nch) continue;   // (with p.q a row is whole blocks of 4 lanes)
       const long long at = r * p.H + ch * 8;
       float w[8];
-      unpack8(wt[c], w);
+      unpack8(kEarly ? wt[c] : *reinterpret_cast<const uint4*>(p.weight + ch * 8), w);
 #pragma unroll
       for (int q = 0; q < 8; ++q) w[q] = v[c][q] * rstd * w[q];
       const uint4 yv = pack8(w);
