@@ -414,7 +414,7 @@ static moe_status_t group_gemm_mxfp4(const moe_operand_t* a_op, const moe_operan
   if ((!a4 && a_op->dtype != MOE_DT_MXFP8) || b_op->layout != MOE_B_NK) return MOE_ERR_UNSUPPORTED;
   if (mx && (mx->row_q || mx->col_q)) return MOE_ERR_UNSUPPORTED;
   if (!a_op->scales || !b_op->scales || !c_bf16) return MOE_ERR_NULL;
-  if (K % 32 != 0 || K >= kMaxMx4K) return MOE_ERR_SHAPE;
+  if (K % 32 != 0 || K >= kMaxMx4K || N >= kMaxMx4N) return MOE_ERR_SHAPE;
   if (!aligned16(a_op->data) || !aligned16(b_op->data) || !aligned16(c_bf16)) return MOE_ERR_ALIGN;
   int cus;
   moe_status_t st = ensure_init(&cus);

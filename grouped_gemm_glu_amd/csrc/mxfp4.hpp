@@ -429,6 +429,8 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
   constexpr int KB = A4 ? 8 : 4;          // blocks of 32 values per K-tile
   constexpr int KSN = KB / 2;             // k-steps per K-tile
   constexpr int NJB = A4 ? 4 : 2;         // DMA pieces (1 KB) of B per wave and K-tile; of A: 4
+  constexpr int kStores = 16;             // of a tile, per wave
+  constexpr uint32_t kDrop = 0xFFFFFFF0u; // an offset behind every range
   constexpr int ABYTES = 32768;           // A's part of a stage, B's after it
   constexpr int SBYTES = ABYTES + 8192 * NJB;
   // One array per stage, so that the compiler can tell the DMA of one from the
@@ -500,7 +502,7 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
   // ---- the fetching side: the operands of one tile
   const int srow = tid & 255;
   const bool isA = wave < 4;
-  struct Fetch { rsrc_t A, B; const uint8_t* sp; int s_off; };
+  struct Fetch { rsrc_t A, B; const uint8_t* sp; int s_off, s_end; };
   auto fetch_of = [&](const Tile& t, bool any) {
     const int cols = min(MX4_BN, p.N - t.n0);
     const long long brow0 = (long long)t.e * p.N + t.n0;
@@ -511,6 +513,8 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
     // scale is not stored)
     f.sp = isA ? p.a_scales + (long long)t.row0 * nblk : p.b_scales + brow0 * nblk;
     f.s_off = (isA ? min(srow, t.rows - 1) : min(mx4_col(srow), cols - 1)) * nblk;
+    const long long left = (isA ? (long long)p.M_cap - t.row0 : (long long)p.E * p.N - brow0) * nblk;
+    f.s_end = (int)min(left, 1LL << 30) - KB * NST;   // the last offset a load may start at
     return f;
   };
   // DMA piece: 1 KB of LDS, 8 rows of 128 bytes or 16 of 64; a lane lands on
@@ -534,38 +538,56 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
     const int c = d.ca ^ swz_hi(piece & 3);
     const uint32_t off = d.la + (uint32_t)(c * 16) + ((uint32_t)(piece * 8) * lda + (uint32_t)(kt * 128));
     const int left = (nblk - KB * kt) * (A4 ? 1 : 2);     // chunks of the row that are left
-    lds_dma16(f.A, st + piece * 1024, c < left ? off : 0xFFFFFFF0u, 0);
+    lds_dma16(f.A, st + piece * 1024, c < left ? off : kDrop, 0);
   };
   auto dmaB = [&](const LanePart& d, const Fetch& f, int kt, uint8_t* st, int j) {
     const int piece = wave * NJB + j;
     const int c = A4 ? d.cb ^ swz_hi(piece & 3) : d.cb;
     const int urow = mx4_col(piece * (A4 ? 8 : 16));
     const uint32_t off = d.lb + (uint32_t)(c * 16) + ((uint32_t)urow * ldb + (uint32_t)(kt * (A4 ? 128 : 64)));
-    lds_dma16(f.B, st + ABYTES + piece * 1024, c < nblk - KB * kt ? off : 0xFFFFFFF0u, 0);
+    lds_dma16(f.B, st + ABYTES + piece * 1024, c < nblk - KB * kt ? off : kDrop, 0);
   };
-  // scales of K-tile kt of row srow, one register per stage.  Loads stay inside
-  // the row: the last K-tile's bytes end with the row and are shifted down; a
-  // masked K-tile's load is dropped.  No branch: with one in the main loop the
+  // scales of row srow, those of a round's NST K-tiles with one load: a wave's 64
+  // rows are 64 lines of memory however few bytes of each are taken.  The bytes
+  // may run over into the next rows, whose are masked; behind the array's last
+  // row the load is shifted down.  No branch: with one in the main loop the
   // compiler sinks a k-step's MFMAs below it and spills the fragments.  The
   // bytes are worked on when they are stored, K-tiles after their load.
-  using sv_t = std::conditional_t<A4, unsigned long long, uint32_t>;   // a row's KB scale bytes
-  sv_t sv[NST];
+  constexpr int SW = KB * NST / 4;
+  struct Scales { uint32_t w[SW]; int sh; };
+  Scales sv;
   auto scale_load = [&](const Fetch& f, int kt) {
-    sv_t v;
-    __builtin_memcpy(&v, f.sp + (f.s_off + min(KB * kt, nblk - KB)), KB);
+    const int want = f.s_off + KB * kt, at = min(want, f.s_end);
+    Scales v;
+    __builtin_memcpy(v.w, f.sp + at, 4 * SW);
+    v.sh = want - at;
     return v;
   };
-  auto scale_store = [&](uint8_t* sc, sv_t v, int kt) {
-    const int past = max(0, min(KB * kt + KB - nblk, KB - 1));   // blocks past the end of K: 1 (byte 127)
-    const sv_t ones = (sv_t)0x7F7F7F7F7F7F7F7Full;
-    v = (sv_t)(v >> (8 * past)) | (sv_t)((sv_t)(ones << 1) << (8 * KB - 1 - 8 * past));
-    v = KB * kt < nblk ? v : ones;
+  // the scales of the load's K-tile j, which is K-tile kt of its row
+  auto scale_store = [&](uint8_t* sc, const Scales& v, auto jc, int kt) {
+    constexpr int j = decltype(jc)::value;
+    // 4 bytes from byte 4 i + sh on (what is behind the load is behind the row)
+    auto word = [&](int i) {
+      uint32_t lo = v.w[i], hi = i + 1 < SW ? v.w[i + 1] : 0;
+#pragma unroll
+      for (int o = 1; i + o < SW; ++o) {
+        lo = v.sh >> 2 >= o ? v.w[i + o] : lo;
+        hi = v.sh >> 2 >= o ? (i + o + 1 < SW ? v.w[i + o + 1] : 0) : hi;
+      }
+      return __builtin_amdgcn_alignbyte(hi, lo, v.sh & 3);
+    };
+    const int here = min(max(nblk - KB * kt, 0), KB);   // blocks that the row has; the others: 1 (byte 127)
+    auto mask = [&](uint32_t w, int n) {
+      const uint32_t m = n >= 4 ? ~0u : (1u << (8 * max(n, 0))) - 1;
+      return (w & m) | (0x7F7F7F7Fu & ~m);
+    };
     if constexpr (A4) {
-      const uint32_t lo4 = (uint32_t)v, hi4 = (uint32_t)(v >> 32);
+      const uint32_t lo4 = mask(word(2 * j), here), hi4 = mask(word(2 * j + 1), here - 4);
       *reinterpret_cast<uint2*>(sc + tid * 8) = make_uint2(__builtin_amdgcn_perm(hi4, lo4, 0x06040200u),
                                                            __builtin_amdgcn_perm(hi4, lo4, 0x07050301u));
     } else {
-      *reinterpret_cast<uint32_t*>(sc + tid * 4) = __builtin_amdgcn_perm((uint32_t)v, (uint32_t)v, 0x03010200u);
+      const uint32_t w = mask(word(j), here);
+      *reinterpret_cast<uint32_t*>(sc + tid * 4) = __builtin_amdgcn_perm(w, w, 0x03010200u);
     }
   };
 
@@ -575,22 +597,23 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
   {
     const Fetch f = fetch_of(uniform(cur_), true);
     const LanePart d = lane_part();
+    sv = scale_load(f, 0);
     static_for<NST>([&](auto i) {
-      sv[i] = scale_load(f, i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) dmaA(d, f, i, stage(i), j);
 #pragma unroll
       for (int j = 0; j < NJB; ++j) dmaB(d, f, i, stage(i), j);
     });
     __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
-    scale_store(sc0, sv[0], 0);
+    static_for<NST>([&](auto i) { scale_store(scales(i), sv, i, i); });
     __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
     __syncthreads();
   }
 
   for (;;) {
-    // K-tile 0 of the tile is in stage 0, its scales too; K-tiles 1 .. NST - 1
-    // are on their way to the other stages and their scales to sv
+    // K-tile 0 of the tile is in stage 0, K-tiles 1 .. NST - 1 are on their way
+    // to the other stages; the scales of all of them are stored.  Behind them the
+    // last tile's stores may be on their way (always kStores of a wave)
     const long long ntile = tile + P;
     const bool more = ntile < total;
     Tile nxt_ = cur_;
@@ -686,21 +709,28 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
       // last k-step of each: K-tile kt + s + 1 has landed (the DMA of the NST -
       // 2 after it may be on its way; with their scales' loads that is less than
       // what is, and waits for the oldest of them too), its scales are stored,
-      // and every wave's reads of stage s are done.
-      auto round = [&](int kt, const Fetch& ff, int fkt) {
+      // and every wave's reads of stage s are done.  FIRST: the tile's first
+      // round, whose K-tiles but the last were asked for before the last tile's
+      // stores, and their scales stored: the counter is in issue order, so the
+      // stores may still be on their way.
+      auto round = [&](auto first, int kt, const Fetch& ff, int fkt) {
+        constexpr bool FIRST = decltype(first)::value;
         static_for<NST>([&](auto sc_) {
           constexpr int S = decltype(sc_)::value, NX = (S + 1) % NST;
           static_for<KSN - 1>([&](auto ks) { kstep(ks, sc_, ff, 0); });
-          constexpr int VM = (NST - 2) * (4 + NJB);
+          constexpr bool BEFORE = FIRST && S < NST - 1;
+          constexpr int VM = (NST - 2) * (4 + NJB) + (BEFORE ? kStores : 0);
           __builtin_amdgcn_s_waitcnt(0x0F70 | (VM & 15) | ((VM >> 4) << 14));   // vmcnt(VM)
-          scale_store(scales(std::integral_constant<int, NX>{}), sv[NX], S == NST - 1 ? fkt : kt + S + 1);
+          if constexpr (!BEFORE)
+            scale_store(scales(std::integral_constant<int, NX>{}), sv, std::integral_constant<int, NX>{},
+                        S == NST - 1 ? fkt : kt + S + 1);
           // (the bare barrier: __syncthreads would wait for all loads)
           asm volatile("" ::: "memory");
           __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
           __builtin_amdgcn_s_barrier();
           asm volatile("" ::: "memory");
           __builtin_amdgcn_sched_barrier(0);
-          sv[S] = scale_load(ff, fkt + S);
+          if constexpr (S == NST - 2) sv = scale_load(ff, fkt);   // (the last of the round before is stored)
           kstep(std::integral_constant<int, KSN - 1>{}, sc_, ff, fkt + S);
         });
       };
@@ -709,9 +739,19 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
       for (int i = 0; i < MI; ++i) { aF[0][i] = rdA(st0, 0, i); sA[i] = rdSA(sc0, i); }
 #pragma unroll
       for (int j = 0; j < 4; ++j) { bF[j] = rdB(st0, 0, j); sB[j] = rdSB(sc0, j); }
-      const Fetch f = fetch_of(cur, true);
-      for (int kt = 0; kt < nk - NST; kt += NST) round(kt, f, kt + NST);
-      round(nk - NST, fetch_of(nxt, more), 0);   // (after the last tile the loads read nothing)
+      // the operands that the round from K-tile kt on fetches: those behind it,
+      // or at the end the next tile's (after the last tile its loads read nothing)
+      auto fetch_at = [&](int kt) {
+        const bool end = kt + NST >= nk;
+        Tile t;
+        t.e = end ? nxt.e : cur.e;
+        t.row0 = end ? nxt.row0 : cur.row0;
+        t.rows = end ? nxt.rows : cur.rows;
+        t.n0 = end ? nxt.n0 : cur.n0;
+        return fetch_of(t, !end || more);
+      };
+      round(std::true_type{}, 0, fetch_at(0), NST < nk ? NST : 0);
+      for (int kt = NST; kt < nk; kt += NST) round(std::false_type{}, kt, fetch_at(kt), kt + NST < nk ? kt + NST : 0);
       // the sums are needed here: without this the compiler sinks the last
       // MFMAs into the epilogue's branches, with their fragments in scratch
 #pragma unroll
@@ -723,10 +763,10 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
       // of one row, so that a store covers 64 bytes of each of 16 rows
       const int z = opaque_zero(), le = lane + z;
       const int er = le & 15, eo = 16 * ((le >> 4) & 1) + 8 * (le >> 5);
+      const rsrc_t C = make_rsrc(p.C + (long long)cur.row0 * p.N + cur.n0, (long long)cur.rows * p.N * 2 - cur.n0 * 2LL);
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
-        const int m = wm * 32 * MI + 32 * i + er;
-        uint16_t* crow = p.C + (long long)(cur.row0 + m) * p.N + cur.n0 + eo;
+        const uint32_t row = (uint32_t)(wm * 32 * MI + 32 * i + er) * ((uint32_t)p.N * 2) + 2 * eo;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int n = wn * 128 + 32 * j;
@@ -735,13 +775,21 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
           for (int d = 0; d < 8; ++d) w[d] = pack_bf16x2(acc[i][j][2 * d], acc[i][j][2 * d + 1]);
 #pragma unroll
           for (int d = 0; d < 4; ++d) swap16(w[d], w[4 + d]);
-          if (n < p.N - cur.n0) {
-            if (m < cur.rows) *reinterpret_cast<uint4*>(crow + n) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (m + 16 < cur.rows)
-              *reinterpret_cast<uint4*>(crow + 16LL * p.N + n) = make_uint4(w[4], w[5], w[6], w[7]);
-          }
+          const uint32_t off = n < p.N - cur.n0 ? row + 2 * n : kDrop - 16 * (8 * i + 2 * j);
+          const uint32_t off16 = n < p.N - cur.n0 ? off + 16 * ((uint32_t)p.N * 2) : kDrop - 16 * (8 * i + 2 * j + 1);
+          __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[0], w[1], w[2], w[3]}, C, off, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[4], w[5], w[6], w[7]}, C, off16, 0, 0);
         }
       }
+      // (as many stores from either kind of tile, which round counts on: each of
+      // those that store nothing has an offset of its own, since the compiler
+      // drops a store that a later one covers)
+#pragma unroll
+      for (int i = 8 * MI; i < kStores; ++i) __builtin_amdgcn_raw_buffer_store_b128(u32x4{0, 0, 0, 0}, C, kDrop - 16 * i, 0, 0);
+      static_for<NST - 1>([&](auto i) {
+        constexpr std::integral_constant<int, decltype(i)::value + 1> s{};
+        scale_store(scales(s), sv, s, s);
+      });
     };
     if (cur.rows > 128) tile_body(std::integral_constant<int, 2>{});
     else tile_body(std::integral_constant<int, 1>{});

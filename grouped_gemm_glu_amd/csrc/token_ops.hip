@@ -97,7 +97,7 @@ moe_status_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s) {
   if (a.T == 0) return MOE_OK;
   const dim3 grid(token_grid(a.T));
   // few rows: 1024 threads, so that a row is in flight at once (1 row of 7168:
-  // 5.6 -> NORM1 us)
+  // 5.6 -> 3.6 us)
   if (a.T <= 512 && a.H > 2048) {
     if (a.H <= 8192) hipLaunchKernelGGL((add_rmsnorm_kernel<1024, 1>), grid, dim3(1024), 0, s, a);
     else hipLaunchKernelGGL((add_rmsnorm_kernel<1024, 2>), grid, dim3(1024), 0, s, a);

@@ -353,8 +353,8 @@ moe_status_t moe_group_gemm_dglu_bwd(const void* dy2, const moe_operand_t* w2, i
  * moe_mxfp4_quantize) or e4m3fn codes [M_cap][K] (MOE_DT_MXFP8), with scales
  * [M_cap][K/32]: the same sum over the codes' values.  A scale byte 0xFF (NaN)
  * makes every product with its block NaN.  c_bf16 is required, MXFP8 outputs
- * are MOE_ERR_UNSUPPORTED.  Requires K % 32 == 0, K < 2^24, N % 64 == 0;
- * codes and c 16-byte aligned, scales any.  The call takes any group sizes, from one row
+ * are MOE_ERR_UNSUPPORTED.  Requires K % 32 == 0, K < 2^24, N % 64 == 0,
+ * N < 2^23; codes and c 16-byte aligned, scales any.  The call takes any group sizes, from one row
  * per expert (decoding, where it streams the active experts' weights once) up. */
 moe_status_t moe_group_gemm_quant(const moe_operand_t* a, const moe_operand_t* b, int N, int K,
                                   const moe_groups_t* groups, void* c_bf16,

@@ -141,8 +141,9 @@ def test_mxfp4_refusals():
     assert gemm(b=G.operand(f, dtype=G.DT_MXFP8, layout=G.B_PACKED, scales=f), K=128) == UNSUP
     assert gemm(mx=B(G.mx_out(row_q=f, row_s=f))) == UNSUP
     assert gemm(a=G.operand(f + 8, dtype=G.DT_MXFP4, scales=f)) == ALIGN and gemm(c=f + 2) == ALIGN
-    # 256 rows of e4m3 codes are addressed with 32 bits
+    # 256 rows of e4m3 codes and of outputs are addressed with 32 bits
     assert gemm(K=1 << 24) == SHAPE and gemm(K=(1 << 31) - 32) == SHAPE
+    assert gemm(N=1 << 23) == SHAPE and gemm(N=(1 << 31) - 64) == SHAPE
     # the other operands keep their own rule for K
     assert gemm(a=G.operand(f), b=G.operand(f, layout=G.B_KN), K=32) == SHAPE
 
