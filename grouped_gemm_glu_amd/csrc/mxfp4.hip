@@ -54,8 +54,8 @@ moe_status_t launch_mx4_weight_kn(const uint16_t* src, int E, int N, int K, uint
 
 moe_status_t launch_mx4_gemm(const Mx4Args& a, bool a4, int cus, hipStream_t st) {
   if (a.M_cap == 0 && !a.offsets_out && !a.status_out) return MOE_OK;
-  // (two rows: a load of 16 scales then stays inside their array)
-  if (a.K >= 256 && a.M_cap > 1 && !few_rows(a, a4, cus)) {
+  // (the tiles load 16 scales at once, which their arrays have to hold)
+  if ((long long)a.M_cap * (a.K / 32) >= 16 && !few_rows(a, a4, cus)) {
     const long long tiles = ((long long)(a.M_cap + MX4_BM - 1) / MX4_BM + a.E) * ((a.N + MX4_BN - 1) / MX4_BN);
     const int g = (int)std::min<long long>(tiles, cus);
     if (a4) hipLaunchKernelGGL(mx4_gemm_tile_kernel<true>, dim3(g), dim3(512), 0, st, a);

@@ -409,20 +409,25 @@ __device__ __forceinline__ int mx4_off64(int r, int c) { return r * 64 + ((c ^ (
 // zeros, their scales are set to 1.  Scales go through registers (their rows, K
 // / 32 bytes long, have any alignment): thread t fetches those of row t % 256
 // of A or B and stores the even blocks' and the odd blocks' in a run each: lane
-// half h's scales of the k-steps.  (A row has at least one K-tile's scales: K >=
-// 256, or 128 for e4m3.)
+// half h's scales of the k-steps.
 // The stream of K-tiles runs on over the tiles: the last NST K-tiles of a tile
 // fetch the first ones of the workgroup's next tile, and the epilogue works
 // from registers alone, so that its stores and the next tile's first loads
 // overlap.
-// What bounds it (16384 rows in 32 groups x 4096 x 7168, e2m1, per 256-value
-// K-tile of a CU): 1.35 us with the loads left out (the MFMAs, which run at
-// 6.1 PFLOP/s at most on random codes, the chip being power-limited), 2.17 us
-// with the MFMAs left out (the operands' round trip), 2.1 us together.  64 KB
-// of aligned 128-byte row pieces take 0.64 us from L2, of 64-byte pieces or of
-// pieces that straddle lines (K % 256 != 0) 1.1 us: four stages of 128 values
-// were 20% slower for e2m1 rows for that reason, three of them 5% faster than
-// two for e4m3 rows, of which only the weights take 64-byte pieces.
+// What bounds it, by leaving parts out (16384 rows in 32 groups x 4096 x 7168,
+// 256 CUs): e2m1 rows 275 us (3.5 PFLOP/s), with every operand read from L2
+// again and again 247, without the MFMAs 251, without both 152; the MFMAs alone
+// 151, at the 6.1 PFLOP/s that random codes reach at most, the chip being
+// power-limited.  e4m3 rows 402 us, 364, 330, 212 and 243.  So the operands'
+// way through L2 and LDS and the MFMAs, each near the half of it, overlap in part,
+// and misses in L2 cost the rest.  An L2 prefetch two K-tiles ahead made it 5%
+// (weights alone, shared out) to 15% slower: the requests of a CU are scarce.
+// For the same reason a round's scales are one load (e4m3 446 -> 421 us against
+// a load per K-tile).  64 KB of aligned 128-byte row pieces take 0.53 us from
+// L2, of 64-byte pieces or of pieces that straddle lines (K % 256 != 0) 1.0 us:
+// four stages of 128 values were 20% slower for e2m1 rows for that reason, three
+// of them 5% faster than two for e4m3 rows, of which only the weights take
+// 64-byte pieces.
 template <bool A4>
 __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
   constexpr int NST = A4 ? 2 : 3;         // stages

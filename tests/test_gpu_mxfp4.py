@@ -274,6 +274,21 @@ def test_product_tiles(G, counts, N, K, pad, a):
 
 
 @pytest.mark.parametrize("a", ["fp4", "fp8"])
+@pytest.mark.parametrize("counts,N,K", [([1500, 1001], 2048, 32), ([1500, 0, 1001], 2048, 64), ([1301, 3], 2048, 96),
+                                        ([2049], 1024, 160), ([2500], 4096, 128), ([700, 1000], 2048, 224),
+                                        ([1025, 512], 1024, 352), ([1100], 1024, 480)])
+def test_product_short_rows(G, counts, N, K, a):
+    """Many rows of fewer blocks than a round of K-tiles: the scales' loads run
+    over the rows' ends, and at the arrays' ends are shifted."""
+    rng = np.random.default_rng(N + K)
+    M = sum(counts)
+    ops = _operands(rng, M, K, len(counts), N, a)
+    for margin in (0, 250):                     # with few units the tiles are taken from fewer rows on
+        got = _product(G, counts, M, K, N, a, ops, cu_margin=margin, scale_shift=K % 3)
+        _check(got, counts, M, ops[4], ops[5], a, f"margin {margin}")
+
+
+@pytest.mark.parametrize("a", ["fp4", "fp8"])
 def test_product_tiles_nan_rows_and_columns_stay_their_own(G, a):
     """A NaN scale reaches its row, or its column in its group, and nothing else, across the tiles' edges and
     in rows and columns that share a staged tile."""
