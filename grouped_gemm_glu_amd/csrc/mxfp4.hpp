@@ -164,7 +164,9 @@ __device__ void build_row_scan(RowScan& rs, const int* __restrict__ counts, int 
     trun += c[i];
   }
   if (t == NT - 1) rs.tile_off[E] = trun;
-  const int st = __syncthreads_or((neg ? 1 : 0) | (over ? 2 : 0));
+  // (__syncthreads_or tells whether any is set, not which bits)
+  const bool any_neg = __syncthreads_or(neg), any_over = __syncthreads_or(over);
+  const int st = (any_neg ? 1 : 0) | (any_over ? 2 : 0);
   if (writer) {
     if (offsets_out)
       for (int e = t; e <= E; e += NT) offsets_out[e] = rs.row_off[e];

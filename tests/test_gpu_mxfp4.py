@@ -227,6 +227,24 @@ def test_product_bad_counts_are_clamped(G, a):
         _check(got, eff, sum(eff), ops[4], ops[5], a)
 
 
+@pytest.mark.parametrize("E,M_cap,N,K", [(70, 30, 64, 96), (3, 2000, 576, 1056)])   # many groups; the 256 x 256 tiles
+@pytest.mark.parametrize("a", ["fp4", "fp8"])
+def test_product_status_of_every_kernel(G, a, E, M_cap, N, K):
+    import torch
+    rng = np.random.default_rng(16)
+    ops = _operands(rng, M_cap, K, E, N, a)
+    half, rest = M_cap // 2, [0] * (E - 3)
+    for counts, eff, st in (([half, 5, 0], [half, 5, 0], 0), ([half, -5, 4], [half, 0, 4], 1),
+                            ([half, M_cap, 7], [half, M_cap - half, 0], 2),
+                            ([-1, M_cap + 1, 7], [0, M_cap, 0], 3), ([1 << 30, 1 << 30, 1 << 30], [M_cap, 0, 0], 2)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        offs = torch.full((E + 1,), -7, dtype=torch.int32, device="cuda")
+        got = _product(G, rest + counts, M_cap, K, N, a, ops, status, offs)
+        assert int(status) == st
+        assert offs.tolist() == [0] + np.cumsum(rest + eff).tolist()
+        _check(got, rest + eff, sum(eff), ops[4], ops[5], a)
+
+
 @pytest.mark.parametrize("a", ["fp4", "fp8"])
 def test_product_many_experts_and_margin(G, a):
     """1024 experts, most of them empty; fewer compute units; the same bits."""
