@@ -690,6 +690,7 @@ moe_status_t moe_router_topk_bwd(const void* logits, int logits_dtype, int T, in
   if (st != MOE_OK) return st;
   if (!ids || !dweights || !dlogits) return MOE_ERR_NULL;
   if (!aligned4(ids) || !aligned4(dweights) || !aligned16(dlogits)) return MOE_ERR_ALIGN;
+  if (dlogits == logits) return MOE_ERR_UNSUPPORTED;
   int cus;
   if ((st = ensure_init(&cus)) != MOE_OK) return st;
   return launch_router_bwd(a, logits_dtype == MOE_DT_BF16, ids, dweights, dlogits, (hipStream_t)stream);
@@ -697,7 +698,8 @@ moe_status_t moe_router_topk_bwd(const void* logits, int logits_dtype, int T, in
 
 static moe_status_t check_combine(int M_cap, int H, const int32_t* dst, int T, int k, const float* weights) {
   if (!dst) return MOE_ERR_NULL;
-  if (M_cap < 0 || T < 0 || k < 1 || k > kMaxTopk || H < 8 || H % 8 != 0) return MOE_ERR_SHAPE;
+  if (M_cap < 0 || T < 0 || k < 1 || k > kMaxTopk || H < 8 || H % 8 != 0 || H > kMaxCombineH)
+    return MOE_ERR_SHAPE;
   if (!aligned4(dst) || (weights && !aligned4(weights))) return MOE_ERR_ALIGN;
   return MOE_OK;
 }
@@ -708,6 +710,7 @@ moe_status_t moe_combine(const void* y, int M_cap, int H, const int32_t* dst, co
   if (st != MOE_OK) return st;
   if (!y || !out) return MOE_ERR_NULL;
   if (!aligned16(y) || !aligned16(out) || (residual && !aligned16(residual))) return MOE_ERR_ALIGN;
+  if (out == y) return MOE_ERR_UNSUPPORTED;
   int cus;
   if ((st = ensure_init(&cus)) != MOE_OK) return st;
   return launch_combine(static_cast<const uint16_t*>(y), M_cap, H, dst, weights, T, k,
@@ -743,6 +746,7 @@ moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* we
   if (!aligned16(x) || !aligned16(weight) || (residual && !aligned16(residual)) || (h && !aligned16(h)) ||
       (y && !aligned16(y)) || (rstd && !aligned4(rstd)))
     return MOE_ERR_ALIGN;
+  if (y && (y == h || y == x || y == residual)) return MOE_ERR_UNSUPPORTED;
   int cus;
   if ((st = ensure_init(&cus)) != MOE_OK) return st;
   NormArgs a;
@@ -780,6 +784,7 @@ moe_status_t moe_add_rmsnorm_bwd(const void* dy, const void* h, const void* weig
   if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned4(rstd) || (dh && !aligned16(dh)) ||
       (dx && !aligned16(dx)) || (dweight && !aligned4(dweight)) || (workspace && !aligned16(workspace)))
     return MOE_ERR_ALIGN;
+  if (dx && (dx == dy || dx == h)) return MOE_ERR_UNSUPPORTED;
   int cus;
   moe_status_t st = ensure_init(&cus);
   if (st != MOE_OK) return st;

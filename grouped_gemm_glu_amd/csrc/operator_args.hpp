@@ -10,6 +10,7 @@ constexpr int kMaxTopk = 16;
 constexpr int kMaxRouterTokens = 1 << 25;   // a launch of 64 lanes per token stays below 2^32
 constexpr int kMaxRouterGroups = 64;        // one lane per group
 constexpr int kNormMaxH = 16384;
+constexpr int kMaxCombineH = 1 << 26;       // 2048 columns per row of the grid
 constexpr int kMaxMx4K = 1 << 24;           // a tile's 256 rows of codes, and of outputs, within a
 constexpr int kMaxMx4N = 1 << 23;           // descriptor's 2^32 bytes
 

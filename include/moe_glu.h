@@ -353,9 +353,10 @@ moe_status_t moe_group_gemm_dglu_bwd(const void* dy2, const moe_operand_t* w2, i
  * moe_mxfp4_quantize) or e4m3fn codes [M_cap][K] (MOE_DT_MXFP8), with scales
  * [M_cap][K/32]: the same sum over the codes' values.  A scale byte 0xFF (NaN)
  * makes every product with its block NaN.  c_bf16 is required, MXFP8 outputs
- * are MOE_ERR_UNSUPPORTED.  Requires K % 32 == 0, K < 2^24, N % 64 == 0,
- * N < 2^23; codes and c 16-byte aligned, scales any.  The call takes any group sizes, from one row
- * per expert (decoding, where it streams the active experts' weights once) up. */
+ * are MOE_ERR_UNSUPPORTED.  Requires K % 32 == 0, K < 2^24, N % 64 == 0, N <
+ * 2^23; codes and c 16-byte aligned, scales any.  The call takes any group
+ * sizes, from one row per expert (decoding, where it streams the active
+ * experts' weights once) up. */
 moe_status_t moe_group_gemm_quant(const moe_operand_t* a, const moe_operand_t* b, int N, int K,
                                   const moe_groups_t* groups, void* c_bf16,
                                   const moe_mx_out_t* mx, int cu_margin, void* stream);
@@ -490,8 +491,8 @@ moe_status_t moe_router_topk_bwd(const void* logits, int logits_dtype, int T, in
  * dropped), weights fp32 [T][k] (NULL: all 1, which makes this call the
  * gradient of the row gather), residual bf16 [T][H] (NULL: none; the shared
  * expert's output or the residual stream), out bf16 [T][H], which may be the
- * residual itself but not overlap y.  Requires H % 8 == 0, 1 <= k <= 16; y,
- * residual and out 16-byte, dst and weights 4-byte aligned. */
+ * residual itself but not overlap y.  Requires H % 8 == 0, H <= 2^26, 1 <= k
+ * <= 16; y, residual and out 16-byte, dst and weights 4-byte aligned. */
 moe_status_t moe_combine(const void* y, int M_cap, int H, const int32_t* dst, const float* weights, int T,
                          int k, const void* residual, void* out, void* stream);
 
@@ -513,8 +514,9 @@ moe_status_t moe_combine_bwd(const void* dout, const void* y, int M_cap, int H, 
  *   mx: row-wise MXFP8 copy of y (mx->row_q, row_s; byte-identical to
  *       moe_mxfp8_quantize of y; the transposed copy is MOE_ERR_UNSUPPORTED)
  * x, residual, h, y: bf16 [T][H]; weight bf16 [H]; rstd fp32 [T].  Each output
- * may be NULL, one is required.  h may be x or residual itself.  Requires
- * H % 8 == 0, 8 <= H <= 16384 (H % 32 == 0 with mx), eps >= 0. */
+ * may be NULL, one is required.  h may be x or residual itself, y none of
+ * them.  Requires H % 8 == 0, 8 <= H <= 16384 (H % 32 == 0 with mx), eps >= 0;
+ * x, residual, weight, h and y 16-byte, rstd 4-byte aligned. */
 moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* weight, int T, int H,
                              float eps, void* h, void* y, float* rstd, const moe_mx_out_t* mx, void* stream);
 

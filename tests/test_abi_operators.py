@@ -49,6 +49,7 @@ def test_router_refusals():
             assert call(r=bad) == UNSUP, field
     assert fwd(w=NULL) == NULL_ and fwd(w=f + 1) == ALIGN
     assert bwd(dw=NULL) == NULL_ and bwd(dl=NULL) == NULL_ and bwd(dl=f + 4) == ALIGN
+    assert bwd() == UNSUP                                                 # dlogits over the logits
     with pytest.raises(TypeError):
         import torch
         G.moe_router_topk(torch.zeros(2, 4, dtype=torch.float16), 2, 4, 1, G.router(), f, f, stream=1)
@@ -72,6 +73,8 @@ def test_combine_refusals():
     assert fwd(out=NULL) == NULL_ and fwd(out=f + 8) == ALIGN and fwd(res=f + 8) == ALIGN
     assert bwd(dout=NULL) == NULL_ and bwd(dy=NULL, dw=NULL) == NULL_ and bwd(dout=f + 8) == ALIGN
     assert bwd(dy=f) == UNSUP and bwd(dy=2 * f) == UNSUP      # over dout, over y
+    assert fwd(out=f) == UNSUP                                # over y
+    assert fwd(H=(1 << 26) + 8) == SHAPE and bwd(H=(1 << 31) - 8) == SHAPE
     assert bwd(dw=f + 1) == ALIGN and bwd(dy=f + 8) == ALIGN
 
 
@@ -99,6 +102,8 @@ def test_norm_refusals():
     need = G.moe_add_rmsnorm_bwd_workspace_bytes(4, 64)
     assert need > 0 and bwd(n=need - 1) == SHAPE and bwd(ws=f + 4) == ALIGN
     assert bwd(acc=2) == UNSUP and bwd(dh=f + 2) == ALIGN and bwd(dx=f + 2) == ALIGN
+    assert bwd(h=2 * f) == UNSUP and bwd(dy=2 * f) == UNSUP              # dx over dy, over h
+    assert fwd(y=f) == UNSUP and fwd(x=2 * f, res=f) == UNSUP and fwd(x=2 * f, h=f) == UNSUP
     assert G.moe_add_rmsnorm_bwd_workspace_bytes(0, 64) == 0
     # the workspace stops growing with the token count
     assert (G.moe_add_rmsnorm_bwd_workspace_bytes(1 << 20, 7168)
