@@ -212,12 +212,12 @@ __global__ __launch_bounds__(256) void router_exact_kernel(RouterArgs p, int* __
 // within each row of 16 lanes, then across the rows.
 template <int L>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  if constexpr (L == 64) return wave_max(v);
   v = max(v, dpp<0x128>(v));
   v = max(v, dpp<0x124>(v));
   v = max(v, dpp<0x122>(v));
   v = max(v, dpp<0x121>(v));
-  if constexpr (L >= 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
-  if constexpr (L >= 64) v = max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+  if constexpr (L == 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
   return v;
 }
 template <int L>
@@ -225,12 +225,12 @@ __device__ __forceinline__ int lanes_min(int v) { return (int)~lanes_max<L>(~(ui
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
   static_assert(L >= 16, "rows of 16 lanes");
+  if constexpr (L == 64) return wave_sum(v);
   v += dpp<0x128>(v);
   v += dpp<0x124>(v);
   v += dpp<0x122>(v);
   v += dpp<0x121>(v);
-  if constexpr (L >= 32) v += __shfl_xor(v, 16, 64);
-  if constexpr (L >= 64) v += __shfl_xor(v, 32, 64);
+  if constexpr (L == 32) v += __shfl_xor(v, 16, 64);
   return v;
 }
 
@@ -253,8 +253,8 @@ __device__ __forceinline__ float of_rank_key32(uint32_t k) {
 // little), or groups closer than four times that at the border, is done again
 // in 64 bits by the whole wave.
 // Bound by instructions and their latency: a round of the choice is about 80 for
-// 64 / L tokens.  256 experts in 8 groups, k = 8, sigmoid and bias: one token 7.4
-// us (a launch that does nothing takes 3.6), 16384 tokens 20 us, of which the
+// 64 / L tokens.  256 experts in 8 groups, k = 8, sigmoid and bias: one token 5.0
+// us (a launch that does nothing takes 3.6), 16384 tokens 19 us, of which the
 // few tokens of 64 bits, whose waves end last, are about 5 (without a bias, where
 // none needs them, 10); 65536 tokens 50 us.  A token per wave in 64 bits
 // throughout took 55 us for 16384, and one token 11.

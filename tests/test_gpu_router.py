@@ -113,6 +113,23 @@ def test_router_sizes(G, T, E, k, score, bf16):
         _run(G, x, k, bf16, None, rng.standard_normal((T, k)), score=score, renorm=renorm, scale=scale)
 
 
+# more tokens than take a wave each
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("score,with_bias,group_score", [("softmax", False, "top2"), ("sigmoid", True, "top2"),
+                                                         ("softmax", True, "max"), ("sigmoid", False, "max")])
+@pytest.mark.parametrize("T,E,k,groups,keep", [(2049, 68, 5, 1, 1), (2053, 128, 6, 8, 4), (2050, 200, 16, 1, 1),
+                                               (2051, 256, 8, 8, 4), (2052, 264, 7, 1, 1), (2049, 512, 10, 4, 2),
+                                               (2050, 256, 8, 2, 1)])
+def test_router_many_tokens(G, T, E, k, groups, keep, score, with_bias, group_score, bf16):
+    rng = np.random.default_rng(T + E)
+    bias = (rng.standard_normal(E) * 0.2).astype(np.float32) if with_bias else None
+    x = rng.standard_normal((T, E))
+    x[7] = -np.inf
+    x[8, ::2] = -np.inf
+    x[9, 3] = np.nan
+    _run(G, x, k, bf16, bias, None, score=score, n_groups=groups, topk_groups=keep, group_score=group_score, scale=1.5)
+
+
 @pytest.mark.parametrize("score,group_score", [("softmax", "max"), ("softmax", "top2"), ("sigmoid", "max"),
                                                ("sigmoid", "top2")])
 @pytest.mark.parametrize("with_bias", [False, True])
