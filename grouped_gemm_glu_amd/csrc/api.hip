@@ -757,6 +757,7 @@ moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* we
   a.T = T;
   a.H = H;
   a.eps = eps;
+  a.inv_h = 1.0 / H;
   a.h = static_cast<uint16_t*>(h);
   a.y = static_cast<uint16_t*>(y);
   a.rstd = rstd;

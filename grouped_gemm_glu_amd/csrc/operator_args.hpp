@@ -31,6 +31,7 @@ struct NormArgs {
   const uint16_t* weight;     // [H]
   int T, H;
   float eps;
+  double inv_h;               // 1 / H
   uint16_t* h;                // or null
   uint16_t* y;                // or null
   float* rstd;                // or null

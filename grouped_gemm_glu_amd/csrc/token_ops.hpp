@@ -661,35 +661,51 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const uint16_t* __rest
 // ---------------------------------------------------------------- add + RMS norm
 // Sum over the workgroup's NW waves; every thread gets it.  The partial sums
 // are added in wave order.
-template <int NW>
-__device__ __forceinline__ float block_sum(float v, float* tmp) {
+template <int NW, class V>
+__device__ __forceinline__ V block_sum(V v, V* tmp) {
   v = wave_sum(v);
   if constexpr (NW == 1) return v;
   __syncthreads();
   if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
   __syncthreads();
-  float s = 0.0f;
+  V s = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) s += tmp[w];
   return s;
+}
+
+// v (rh + rl) w rounded to a float once: v rh in two floats, and what they and rl
+// leave added to their product with w.  Three roundings, of 1 / sqrt and of two
+// products, would put one value in 10^5 on the other side of its rounding to
+// bf16, and with it the scale of a block whose largest it is.  A zero keeps its
+// sign, and where a part is not finite the plain product stays.
+__device__ __forceinline__ float norm_value(float v, float rh, float rl, float w) {
+#pragma clang fp contract(off)
+  const float p = v * rh;
+  const float e = fmaf(v, rl, fmaf(v, rh, -p));
+  const float t = fmaf(p, w, e * w);
+  return fabsf(t) > 0.0f ? t : p * w;
 }
 
 // One workgroup of NT threads per row, NC chunks of 8 columns per thread.
 // h = bf16(x + residual) is what the residual stream keeps and what the norm
 // is taken of, so that the backward pass sees the same values; y is rounded
 // once, and the MXFP8 copy is the rounded y's (as the GEMM epilogues do).
+// The row's sum is kept in 64 bits over chunks of 8 squares (exact in 32 bits
+// but for their additions), 1 / sqrt in two floats (norm_value), at no cost in
+// time while six waves per SIMD fit (five: 3% slower).
 // Bound by memory: 16384 x 7168 with residual and MXFP8 copy 0.20 ms, 5.3 TB/s,
 // the rate of a large copy; one row is one round trip to memory (the weights
 // are fetched with the row) and a workgroup-wide sum.
 template <int NT, int NC>
-__global__ __launch_bounds__(NT) void add_rmsnorm_kernel(NormArgs p) {
-  __shared__ float tmp[NT / 64];
+__global__ __launch_bounds__(NT, NT == 1024 ? 4 : NC <= 4 ? 6 : 4) void add_rmsnorm_kernel(NormArgs p) {
+  __shared__ double tmp[NT / 64];
   constexpr bool kEarly = NT == 1024;
   const int nch = p.H >> 3;
   for (long long r = blockIdx.x; r < p.T; r += gridDim.x) {
     uint4 wt[NC];
     float v[NC][8];
-    float sq = 0.0f;
+    double sq = 0.0;   // of chunks' sums
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int ch = c * NT + threadIdx.x;
@@ -708,10 +724,17 @@ __global__ __launch_bounds__(NT) void add_rmsnorm_kernel(NormArgs p) {
       } else if (p.h) {
         *reinterpret_cast<uint4*>(p.h + at) = pack8(v[c]);
       }
+      float s8 = 0.0f;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) sq = fmaf(v[c][q], v[c][q], sq);
+      for (int q = 0; q < 8; ++q) s8 = fmaf(v[c][q], v[c][q], s8);
+      sq += (double)s8;
     }
-    const float rstd = 1.0f / sqrtf(block_sum<NT / 64>(sq, tmp) / (float)p.H + p.eps);
+    // 1 / sqrt in 32 bits and one Newton step in 64
+    const double mean = block_sum<NT / 64>(sq, tmp) * p.inv_h + (double)p.eps;
+    const float m32 = (float)mean, r32 = 1.0f / sqrtf(m32);
+    double rd = (double)r32;
+    if (m32 > 1e-30f && m32 < 1e30f) rd = rd * (1.5 - 0.5 * mean * rd * rd);
+    const float rstd = (float)rd, rlow = m32 > 1e-30f && m32 < 1e30f ? (float)(rd - (double)rstd) : 0.0f;
     if (p.rstd && threadIdx.x == 0) p.rstd[r] = rstd;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -721,7 +744,7 @@ __global__ __launch_bounds__(NT) void add_rmsnorm_kernel(NormArgs p) {
       float w[8];
       unpack8(kEarly ? wt[c] : *reinterpret_cast<const uint4*>(p.weight + ch * 8), w);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) w[q] = v[c][q] * rstd * w[q];
+      for (int q = 0; q < 8; ++q) w[q] = norm_value(v[c][q], rstd, rlow, w[q]);
       const uint4 yv = pack8(w);
       if (p.y) *reinterpret_cast<uint4*>(p.y + at) = yv;
       if (p.q) {

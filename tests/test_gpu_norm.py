@@ -165,6 +165,37 @@ def test_add_rmsnorm_bwd(G, T, H, with_dh):
     assert torch.equal(dx2, dx[:T]) and torch.equal(dw3, dwt[:H])
 
 
+def test_add_rmsnorm_zeros_keep_their_sign(G):
+    import torch
+    rng = np.random.default_rng(8)
+    x, wt = _bits(rng, 5, 256), _bits(rng, 256)
+    x[:, ::3] = 0x0000
+    x[:, 1::3] = 0x8000
+    x[4] = 0x8000                                     # a row of zeros alone
+    y = empty_bits((5, 256))
+    G.moe_add_rmsnorm(dev_bits(x), dev_bits(wt), 5, 256, 1e-5, y=y)
+    torch.cuda.synchronize()
+    got = host_bits(y)
+    zero = (x & 0x7FFF) == 0
+    assert np.array_equal(got[zero], ((x ^ wt) & 0x8000)[zero]) and np.all((got & 0x7FFF)[~zero] != 0)
+
+
+def test_add_rmsnorm_rounds_once(G):
+    """y is rounded to fp32 and then to bf16, from a product kept in two floats."""
+    import torch
+    rng = np.random.default_rng(9)
+    T, H = 96, 7168
+    x, wt = _bits(rng, T, H), _bits(rng, H)
+    y = empty_bits((T, H))
+    G.moe_add_rmsnorm(dev_bits(x), dev_bits(wt), T, H, 2.0 ** -20, y=y)
+    torch.cuda.synchronize()
+    _, _, want = P.add_rmsnorm(x, wt, 2.0 ** -20)
+    got = F.bf16_bits_to_f64(host_bits(y))
+    step = np.exp2(np.floor(np.log2(np.maximum(np.abs(want), 2.0 ** -126))) - 7)
+    # half a step of bf16, and half a step of fp32 (2^-17 of it), half as much again for the parts left out
+    assert np.all(np.abs(got - want) <= step * (0.5 + 1.5 * 2.0 ** -17))
+
+
 def test_add_rmsnorm_bwd_no_rows(G):
     import torch
     one = empty_bits((1, 64))
