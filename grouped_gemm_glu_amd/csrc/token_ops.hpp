@@ -369,11 +369,17 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
     if (W > 8) merge([](float v) { return dpp<0x140>(v); });
     if (W > 16) merge([](float v) { return __shfl_xor(v, 16, 64); });
     if (W > 32) merge([](float v) { return __shfl_xor(v, 32, 64); });
-    // (fmax and fmin drop a NaN: such rows are done again below)
+    // (fmax and fmin drop a NaN, of a logit or of the bias, and the number beside it
+    // counts twice: such tokens are done again below)
+    bool no_number = false;
+    each([&](float, float v) {
+      no_number = no_number || v != v;
+      return v;
+    });
 #pragma unroll
     for (int i = 0; i < NI; ++i)
       key[i] = 4 * (l + L * i) < p.E ? rank_key32(p.top2 ? v0[i] + v1[i] : v0[i]) : 0u;
-    redo = lanes_max<L>(nan ? 1u : 0u) != 0u;
+    redo = lanes_max<L>(no_number ? 1u : 0u) != 0u;
     // the kept groups, best first, ties to the lower id; the last kept and the
     // first left out tell whether 32 bits decide
     open = 0;

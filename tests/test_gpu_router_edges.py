@@ -1,0 +1,53 @@
+"""The router where 32 bits do not hold what decides: NaN and infinities in the
+bias.  Against the float64 oracle, with the tolerances of test_gpu_router."""
+import numpy as np
+import pytest
+
+from tests.test_gpu_router import G, _run  # noqa: F401  (G: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- NaN and infinities in the bias
+# (a quad with a NaN: its one number must not count twice; the group sizes of the kernels in 32 bits and, E % 4
+# != 0 or groups of 3, in 64; up to and past 2048 tokens)
+@pytest.mark.parametrize("T", [40, 2100])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("group_score", ["top2", "max"])
+@pytest.mark.parametrize("E,k,groups,keep", [(16, 3, 4, 1), (64, 4, 4, 2), (12, 3, 4, 2), (256, 8, 8, 3)])
+def test_router_nan_bias(G, E, k, groups, keep, group_score, score, bf16, T):  # noqa: F811
+    rng = np.random.default_rng(E + groups)
+    size = E // groups
+    x = rng.standard_normal((T, E)).astype(np.float32)
+    bias = (rng.standard_normal(E) * 0.3).astype(np.float32)
+    x[:, 0] += 3.0                                  # the number beside the NaN is its group's best
+    bias[1] = np.nan
+    bias[2 * size:3 * size] = np.nan                # a group of NaN alone
+    bias[3 * size + size // 2:4 * size] = np.nan    # half a group
+    _run(G, x, k, bf16, bias, None, score=score, n_groups=groups, topk_groups=keep, group_score=group_score)
+
+
+def test_router_nan_bias_worked_case(G):  # noqa: F811
+    """Group 0: 0.88 beside 0.5; group 1: twice 0.73.  The second is chosen."""
+    x = np.zeros((1, 16), np.float32)
+    x[0, 0], x[0, 3], x[0, 4], x[0, 5] = 2.0, -0.5, 1.0, 1.0
+    x[0, 8:] = -5.0
+    bias = np.zeros(16, np.float32)
+    bias[1] = np.nan
+    _run(G, x, 2, False, bias, None, score="sigmoid", n_groups=4, topk_groups=1, group_score="top2")
+
+
+@pytest.mark.parametrize("group_score", ["top2", "max"])
+@pytest.mark.parametrize("groups,keep", [(1, 1), (4, 2), (4, 3)])
+@pytest.mark.parametrize("T", [30, 2100])
+def test_router_infinite_and_nan_bias(G, T, groups, keep, group_score):  # noqa: F811
+    E = 32
+    rng = np.random.default_rng(T)
+    x = rng.standard_normal((T, E)).astype(np.float32)
+    for put in ({3: -np.inf}, {3: np.inf, 9: np.inf}, {3: np.inf, 4: -np.inf, 8: np.nan}, {e: -np.inf for e in range(8, 24)},
+                {e: -np.inf for e in range(E)}, {e: np.nan for e in range(E)}):
+        bias = np.zeros(E, np.float32)
+        for e, v in put.items():
+            bias[e] = v
+        _run(G, x, 5, False, bias, None, score="sigmoid", n_groups=groups, topk_groups=keep, group_score=group_score)
