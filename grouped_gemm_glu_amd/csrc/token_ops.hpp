@@ -250,8 +250,9 @@ __device__ __forceinline__ float of_rank_key32(uint32_t k) {
 // exponential by (|x| + 2) 2^-24 of itself, s (1 - s) |x| <= 0.23, a quotient and
 // two sums), 2^-19.5 for a softmax (a sum of E terms, in 20 roundings); a token
 // with two neighbours among its k + 1 best closer than twice that (and a
-// little), or groups closer than four times that at the border, is done again
-// in 64 bits by the whole wave.
+// little), or a kept and another group whose values are not further apart than
+// their errors (twice that each, and the sum's rounding), is done again in 64 bits
+// by the whole wave.
 // Bound by instructions and their latency: a round of the choice is about 80 for
 // 64 / L tokens.  256 experts in 8 groups, k = 8, sigmoid and bias: one token 5.0
 // us (a launch that does nothing takes 3.6), 16384 tokens 19 us, of which the
@@ -322,10 +323,10 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
     inv = 1.0f / sum;
   }
   bool redo = false;
-  // the relative width within which 32-bit choice values say nothing
-  // (for a group's sum of two scores, and for one score)
-  const float tol2 = p.sigmoid ? 0x1p-19f : 0x1p-17f, tol1 = p.sigmoid ? 0x1p-20f : 0x1p-18f;
-  auto close = [](float hi, float lo, float tol) {   // (true for NaN)
+  // the relative width within which two 32-bit choice values say nothing, and the
+  // relative error of a group's sum of two of them (and a little)
+  const float tol = p.sigmoid ? 0x1p-20f : 0x1p-18f;
+  auto close = [=](float hi, float lo) {   // (true for NaN)
     return !(hi - lo > tol * fmaxf(1.0f, fmaxf(fabsf(hi), fabsf(lo))));
   };
   auto each = [&](auto f) {
@@ -380,19 +381,13 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
     for (int i = 0; i < NI; ++i)
       key[i] = 4 * (l + L * i) < p.E ? rank_key32(p.top2 ? v0[i] + v1[i] : v0[i]) : 0u;
     redo = lanes_max<L>(no_number ? 1u : 0u) != 0u;
-    // the kept groups, best first, ties to the lower id; the last kept and the
-    // first left out tell whether 32 bits decide
+    // the kept groups, best first, ties to the lower id
     open = 0;
-    float last = 0.0f;
-    for (int g = 0; g <= p.topk_groups; ++g) {
+    for (int g = 0; g < p.topk_groups; ++g) {
       uint32_t b = 0;
 #pragma unroll
       for (int i = 0; i < NI; ++i) b = max(b, key[i]);
       b = lanes_max<L>(b);
-      if (g == p.topk_groups) {
-        if (by_score && b != 0u && close(last, of_rank_key32(b), tol2)) redo = true;
-        break;
-      }
       int at = 0x7FFFFFFF;   // group id
 #pragma unroll
       for (int i = NI - 1; i >= 0; --i)
@@ -404,7 +399,23 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
           key[i] = 0;
           open |= 1u << i;
         }
-      last = of_rank_key32(b);
+    }
+    // 32 bits decide if every kept group's value less its error is above every
+    // other's with its error, which goes by the two values' own sizes: their sum
+    // may cancel.  (A value that is infinite is so in 64 bits too.)
+    if (by_score && p.topk_groups < p.n_groups) {
+      uint32_t kept = 0, left = 0;   // of -(value - error), of value + error
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        if (4 * (l + L * i) >= p.E) continue;
+        const float v = p.top2 ? v0[i] + v1[i] : v0[i];
+        const float err = fabsf(v) < INFINITY ? tol * fmaxf(1.0f, p.top2 ? fmaxf(fabsf(v0[i]), fabsf(v1[i])) : fabsf(v)) : 0.0f;
+        if ((open >> i) & 1u) kept = max(kept, rank_key32(err - v));
+        else left = max(left, rank_key32(v + err));
+      }
+      kept = lanes_max<L>(kept);
+      left = lanes_max<L>(left);
+      redo = redo || !(-of_rank_key32(kept) > of_rank_key32(left));
     }
     if (!p.bias && p.top2) {   // without a bias the experts' order is the logits'
 #pragma unroll
@@ -429,7 +440,7 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
     b = lanes_max<L>(b);
     if (check) {
       const float v = of_rank_key32(b);
-      if (j > 0 && b != 0u && close(last, v, tol1)) redo = true;
+      if (j > 0 && b != 0u && close(last, v)) redo = true;
       last = v;
       if (j == p.k) break;
     }

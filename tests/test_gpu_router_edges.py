@@ -1,5 +1,6 @@
 """The router where 32 bits do not hold what decides: NaN and infinities in the
-bias.  Against the float64 oracle, with the tolerances of test_gpu_router."""
+bias, groups whose two best values cancel.  Against the float64 oracle, with
+the tolerances of test_gpu_router."""
 import numpy as np
 import pytest
 
@@ -51,3 +52,20 @@ def test_router_infinite_and_nan_bias(G, T, groups, keep, group_score):  # noqa:
         for e, v in put.items():
             bias[e] = v
         _run(G, x, 5, False, bias, None, score="sigmoid", n_groups=groups, topk_groups=keep, group_score=group_score)
+
+
+# ---------------------------------------------------------------- groups whose two best values cancel
+@pytest.mark.parametrize("T", [2000, 4096])
+@pytest.mark.parametrize("big", [1000.0, 30000.0])
+def test_router_groups_of_large_opposite_choice_values(G, T, big):  # noqa: F811
+    """Group 0's two best choice values are about +big and -big, so that in 32
+    bits each is off by up to big 2^-24 and so is their sum, of about 1; group
+    1's are scores alone.  The sums differ by up to twice that."""
+    rng = np.random.default_rng(int(big) + T)
+    x = rng.uniform(-1.0, 0.0, (T, 8))
+    s = 1 / (1 + np.exp(-x))
+    need = s[:, 0] + s[:, 1] + rng.uniform(-1, 1, T) * big * 2.0 ** -23 - s[:, 4]     # the score of expert 5
+    x[:, 5] = np.log(need / (1 - need))
+    x[:, [2, 3, 6, 7]] = -9.0
+    bias = np.array([big, -big, -4 * big, -4 * big, 0, 0, 0, 0], np.float32)
+    _run(G, x.astype(np.float32), 2, False, bias, None, score="sigmoid", n_groups=2, topk_groups=1, group_score="top2")
