@@ -478,12 +478,16 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
   }
 }
 
-// d(logits) from d(weights) and the ids that were chosen.  With s the scores,
-// S = sum of the chosen ones (1 without renormalisation) and g = dw scale / S:
-//   ds_j = g_j - renorm (sum_i g_i s_i) / S
-//   sigmoid: dx = ds_j s_j (1 - s_j) at the chosen experts, 0 elsewhere
-//   softmax: dx_e = s_e (ds_e [e chosen] - sum_i ds_i s_i); renormalised
-//   softmax is the softmax over the chosen logits, so only those count.
+// d(logits) from d(weights) and the ids that were chosen.  With s the scores, w =
+// s / S (S = sum of the chosen ones, or 1 without renormalisation), dw the
+// weights' gradients and m = sum_i dw_i w_i (0 without renormalisation), the
+// chosen experts' part is d_j = scale w_j (dw_j - m), and
+//   sigmoid: dx = d_j (1 - s_j) at the chosen experts, 0 elsewhere
+//   softmax: dx_e = d_e [e chosen] - s_e sum_i d_i; renormalised softmax is the
+//   softmax over the chosen logits, so only those count, and sum_i d_i = 0.
+// 1 / S stands only in w: dw / S could pass fp32's range where dx does not.  A
+// token with a chosen sigmoid score near or below what fp32 holds has its
+// weights formed in 64 bits, as the forward pass does.
 // An id outside [0, E) takes no part; an id that stands twice counts twice.
 template <int VPL, bool BF16>
 __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs p, const int* __restrict__ ids,
@@ -496,7 +500,7 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs p, const int
   float xs = 0.0f, g = 0.0f;
   if (lane < p.k) {
     id = ids[tok * p.k + lane];
-    g = dw[tok * p.k + lane] * p.scale;
+    g = dw[tok * p.k + lane];
     if (id < 0 || id >= p.E) id = -1;
     else xs = load_logit<BF16>(p.logits, tok * p.E + id);
   }
@@ -526,13 +530,24 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs p, const int
   if (in) s = p.sigmoid ? 1.0f / (1.0f + expf(-xs)) : expf(xs - m) / sum;
   const bool empty = !p.sigmoid && m == -INFINITY && !__any(nan);   // no softmax: constant weights
   if (empty) s = 0.0f;
-  const float S = p.renorm ? wave_sum(s) : 1.0f;
-  const float inv = S == 0.0f ? 0.0f : 1.0f / S;
-  float ds = in ? g * inv : 0.0f;
-  if (p.renorm) ds -= wave_sum(in ? ds * s : 0.0f) * inv;
+  float w;
+  bool none = empty;   // the weights are 0
+  if (p.sigmoid && __any(in && s < 1e-30f && xs != -INFINITY)) {
+    const double sd = in ? 1.0 / (1.0 + exp(-(double)xs)) : 0.0;
+    const double S = p.renorm ? wave_sum(sd) : 1.0;
+    none = S == 0.0;
+    w = (float)(sd / S);
+  } else {
+    const float S = p.renorm ? wave_sum(s) : 1.0f;
+    none = none || S == 0.0f;
+    w = s / S;
+  }
+  const float mean = p.renorm ? wave_sum(in ? g * w : 0.0f) : 0.0f;
   float d = 0.0f, dot = 0.0f;
-  if (in && S != 0.0f && !empty)
-    d = p.sigmoid ? ds * s * (1.0f / (1.0f + expf(xs))) : ds * s;
+  if (in && !none) {
+    d = p.scale * w * (g - mean);
+    if (p.sigmoid) d *= 1.0f / (1.0f + expf(xs));
+  }
   if (full) dot = wave_sum(d);
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {

@@ -1,6 +1,7 @@
-"""The router where 32 bits do not hold what decides: NaN and infinities in the
-bias, groups whose two best values cancel.  Against the float64 oracle, with
-the tolerances of test_gpu_router."""
+"""The router and its gradient where 32 bits do not hold what decides: NaN and
+infinities in the bias, groups whose two best values cancel, scores near the
+end of fp32.  Against the float64 oracle, with the tolerances of
+test_gpu_router."""
 import numpy as np
 import pytest
 
@@ -69,3 +70,37 @@ def test_router_groups_of_large_opposite_choice_values(G, T, big):  # noqa: F811
     x[:, [2, 3, 6, 7]] = -9.0
     bias = np.array([big, -big, -4 * big, -4 * big, 0, 0, 0, 0], np.float32)
     _run(G, x.astype(np.float32), 2, False, bias, None, score="sigmoid", n_groups=2, topk_groups=1, group_score="top2")
+
+
+# ---------------------------------------------------------------- scores and scales that fp32 does not hold
+@pytest.mark.parametrize("renorm", [True, False])
+def test_router_gradient_of_small_sigmoid_scores(G, renorm):  # noqa: F811
+    """Every chosen score below, at and above what fp32 holds: the forward's weights are ratios of scores in 64
+    bits, and so is the gradient."""
+    rng = np.random.default_rng(1)
+    E, k = 24, 4
+    top = np.array([-5, -30, -60, -70, -80, -87, -87.5, -88.0, -88.4, -88.8, -90, -100, -104, -120, -200, -500, -700],
+                   np.float32)
+    x = top[:, None] - rng.uniform(0, 3, (len(top), E)).astype(np.float32)
+    _run(G, x, k, False, None, rng.standard_normal((len(top), k)), score="sigmoid", renorm=renorm, scale=2.5)
+    # some chosen scores small, others not
+    x[:, :2] = rng.standard_normal((len(top), 2))
+    _run(G, x, k, False, None, rng.standard_normal((len(top), k)), score="sigmoid", renorm=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_router_gradient_of_small_scores_beside_a_bias(G, score):  # noqa: F811
+    E = 64
+    rng = np.random.default_rng(14)
+    x = (rng.standard_normal((24, E)) * 2).astype(np.float32)
+    x[:, :8] -= np.linspace(0, 230, 24, dtype=np.float32)[:, None]
+    bias = np.where(np.arange(E) < 8, 2.0, 0.0).astype(np.float32)
+    for renorm in (True, False):
+        _run(G, x, 4, False, bias, rng.standard_normal((24, 4)), score=score, renorm=renorm)
+
+
+def test_router_gradient_of_large_weight_gradients(G):  # noqa: F811
+    """dweights / S passes fp32's range, the gradient does not."""
+    rng = np.random.default_rng(3)
+    x = -60 - rng.uniform(0, 2, (6, 8)).astype(np.float32)
+    _run(G, x, 3, False, None, rng.standard_normal((6, 3)) * 1e15, score="sigmoid", scale=2.0)
