@@ -526,12 +526,27 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs p, const int
   } else if (!p.sigmoid) {
     m = wave_max(in ? xs : -INFINITY);
   }
+  // A renormalised softmax whose choice is not by logits alone may have chosen
+  // experts that are so far below the row's largest logit that their scores are 0
+  // in 64 bits, and the weights with them: those rows are looked through.
+  bool under = false;
+  if (!p.sigmoid && p.renorm && (p.bias || (p.n_groups > 1 && p.top2))) {
+    float top = -INFINITY;
+    for (int e = lane; e < p.E; e += 64) top = fmaxf(top, load_logit<BF16>(p.logits, tok * p.E + e));
+    top = wave_max(top);
+    if (m > -INFINITY && m - top < -700.0f) {
+      double all = 0.0;
+      for (int e = lane; e < p.E; e += 64) all += exp((double)load_logit<BF16>(p.logits, tok * p.E + e) - (double)top);
+      all = wave_sum(all);
+      under = exp((double)m - (double)top) / all == 0.0;
+    }
+  }
   float s = 0.0f;
   if (in) s = p.sigmoid ? 1.0f / (1.0f + expf(-xs)) : expf(xs - m) / sum;
   const bool empty = !p.sigmoid && m == -INFINITY && !__any(nan);   // no softmax: constant weights
   if (empty) s = 0.0f;
   float w;
-  bool none = empty;   // the weights are 0
+  bool none = empty || under;   // the weights are 0
   if (p.sigmoid && __any(in && s < 1e-30f && xs != -INFINITY)) {
     const double sd = in ? 1.0 / (1.0 + exp(-(double)xs)) : 0.0;
     const double S = p.renorm ? wave_sum(sd) : 1.0;

@@ -447,8 +447,10 @@ moe_status_t moe_mxfp8_quantize(const void* v, int R, int C, const moe_groups_t*
  * 1) or 1 (renorm = 0):
  *   w_j = scale * s_j / S
  * NaN logits (and choice values) rank below every number; a NaN logit makes
- * the softmax of its row NaN.  Where S is 0, or every logit of a softmax row
- * is -inf, the weights are 0.  (host struct) */
+ * the softmax of its row NaN.  Where S is 0 (the scores taken in 64 bits: a
+ * softmax's below about e^-745 of the row's best, a sigmoid's of logits below
+ * -709), or every logit of a softmax row is -inf, the weights are 0.  (host
+ * struct) */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
 typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score_t;
 typedef struct {
@@ -476,7 +478,8 @@ moe_status_t moe_router_topk(const void* logits, int logits_dtype, int T, int E,
  * dlogits is written.  Ids outside [0, E) take no part; an id that stands
  * twice in a token counts twice.  Where the weights are 0 by the rule above,
  * so is the gradient.  A renormalised softmax is the softmax over the chosen
- * logits and reads only those.  dlogits 16-byte aligned, else as above;
+ * logits and has no gradient at others (which are read only with a bias or
+ * MOE_GROUP_TOP2, to see whether S is 0).  dlogits 16-byte aligned, else as above;
  * dlogits must not overlap the logits. */
 moe_status_t moe_router_topk_bwd(const void* logits, int logits_dtype, int T, int E, int k,
                                  const moe_router_t* router, const int32_t* ids, const float* dweights,

@@ -1,11 +1,12 @@
 """The router and its gradient where 32 bits do not hold what decides: NaN and
 infinities in the bias, groups whose two best values cancel, scores near the
-end of fp32.  Against the float64 oracle, with the tolerances of
-test_gpu_router."""
+end of fp32, chosen experts far below the row's largest logit.  Against the
+float64 oracle, with the tolerances of test_gpu_router."""
 import numpy as np
 import pytest
 
-from tests.test_gpu_router import G, _run  # noqa: F401  (G: the fixture)
+from oracle import operators as P
+from tests.test_gpu_router import G, U, _logits, _run  # noqa: F401  (G: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +105,35 @@ def test_router_gradient_of_large_weight_gradients(G):  # noqa: F811
     rng = np.random.default_rng(3)
     x = -60 - rng.uniform(0, 2, (6, 8)).astype(np.float32)
     _run(G, x, 3, False, None, rng.standard_normal((6, 3)) * 1e15, score="sigmoid", scale=2.0)
+
+
+@pytest.mark.parametrize("group_score", [None, "top2"])
+def test_router_gradient_is_zero_where_the_weights_are(G, group_score):  # noqa: F811
+    """Chosen for their bias alone, with logits so far below the row's largest that their scores are 0 in 64 bits
+    (as under a mask of the type's lowest value): weights and gradient are 0."""
+    import torch
+    rng = np.random.default_rng(4)
+    E, k, T = 16, 3, 8
+    x = rng.standard_normal((T, E)).astype(np.float32)
+    x[:, :8] = np.array([np.finfo(np.float32).min, -1e4, -800, -760], np.float32).repeat(2)[:, None]
+    x[:, :8] -= np.arange(8, dtype=np.float32)
+    bias = np.where(np.arange(E) < 8, 4.0, 0.0).astype(np.float32)
+    kw = dict(score="softmax", renorm=True)
+    if group_score:
+        kw.update(n_groups=4, topk_groups=2, group_score=group_score)
+    _, w = P.router_topk(x.astype(np.float64), k, bias=bias, **kw)
+    assert np.all(w == 0)
+    _run(G, x, k, False, bias, rng.standard_normal((T, k)), **kw)
+    # and just above: ratios again
+    x[:, :8] = -300.0 - rng.uniform(0, 3, (T, 8))
+    _run(G, x, k, False, bias, rng.standard_normal((T, k)), **kw)
+    # the ids alone decide, whoever chose them: the same rows without groups and bias in the struct keep the rule of
+    # a softmax over the chosen logits
+    ids = torch.zeros(T, k, dtype=torch.int32, device="cuda") + torch.arange(k, dtype=torch.int32, device="cuda")
+    lg, v = _logits(x, False)
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    d = torch.full((T, E), 7.0, device="cuda")
+    G.moe_router_topk_bwd(lg, T, E, k, G.router(**dict(score="softmax", renorm=True)), ids, torch.from_numpy(dw).cuda(), d)
+    torch.cuda.synchronize()
+    want = P.router_topk_bwd(v, ids.cpu().numpy(), dw.astype(np.float64))
+    assert np.max(np.abs(d.double().cpu().numpy() - want)) <= 4 * (2 * 3 + 32) * U * 2 * np.abs(dw).sum(1).max()
