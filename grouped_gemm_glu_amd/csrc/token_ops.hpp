@@ -458,11 +458,13 @@ __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restri
   }
   const bool sel = tv && l < p.k;
   float s = 0.0f;
-  bool tiny = false;   // a score near or below what fp32 holds: its ratio to the others may still count
+  // a score, also times the scale, near or below what fp32 holds: its ratio to the
+  // others may still count
+  bool tiny = false;
   if (sel) {
     const float v = load_logit<BF16>(p.logits, tok * p.E + my_id);
     s = p.sigmoid ? 1.0f / (1.0f + expf(-v)) : (empty ? 0.0f : expf(v - m) * inv);
-    tiny = s < 1e-30f && v != -INFINITY && !empty;
+    tiny = s * fminf(fabsf(p.scale), 1.0f) < 1e-30f && v != -INFINITY && !empty && p.scale != 0.0f;
   }
   redo = redo || lanes_max<L>(tiny ? 1u : 0u) != 0u;
   const float total = p.renorm ? lanes_sum<L>(s) : 1.0f;

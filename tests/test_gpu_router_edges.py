@@ -1,7 +1,7 @@
 """The router and its gradient where 32 bits do not hold what decides: NaN and
-infinities in the bias, groups whose two best values cancel, scores near the
-end of fp32, chosen experts far below the row's largest logit.  Against the
-float64 oracle, with the tolerances of test_gpu_router."""
+infinities in the bias, groups whose two best values cancel, scores and
+scales near the end of fp32, chosen experts far below the row's largest logit.
+Against the float64 oracle, with the tolerances of test_gpu_router."""
 import numpy as np
 import pytest
 
@@ -137,3 +137,17 @@ def test_router_gradient_is_zero_where_the_weights_are(G, group_score):  # noqa:
     torch.cuda.synchronize()
     want = P.router_topk_bwd(v, ids.cpu().numpy(), dw.astype(np.float64))
     assert np.max(np.abs(d.double().cpu().numpy() - want)) <= 4 * (2 * 3 + 32) * U * 2 * np.abs(dw).sum(1).max()
+
+
+@pytest.mark.parametrize("scale", [1e-20, -1e-28, 1e30, 0.0])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_router_scale_and_small_scores(G, score, scale):  # noqa: F811
+    """scale * score passes fp32's range, scale * weight does not."""
+    rng = np.random.default_rng(5)
+    E = 32
+    x = (rng.standard_normal((20, E)) * 2).astype(np.float32)
+    x[:, :8] -= np.linspace(0, 66, 20, dtype=np.float32)[:, None]
+    bias = np.where(np.arange(E) < 8, 2.0, 0.0).astype(np.float32)
+    _run(G, x, 4, False, bias, None, score=score, scale=scale)
+    x[:, 8:] -= np.linspace(0, 66, 20, dtype=np.float32)[:, None]
+    _run(G, x, 4, False, None, None, score=score, scale=scale)
