@@ -5,6 +5,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <initializer_list>
+
 #include "aux_kernels.hpp"
 #include "internal.hpp"
 
@@ -17,6 +19,29 @@ int g_num_cus[kMaxDevices];  // 0 = not initialised
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+// A buffer of a call: n bytes from p on (a null pointer: none).
+struct Buf {
+  const void* p;
+  size_t n;
+};
+bool share_bytes(const Buf& a, const Buf& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.n && b.n && (x <= y ? y - x < a.n : x - y < b.n);
+}
+// Whether an output shares bytes with an input or with another output: the
+// kernels read rows that other workgroups' outputs could have replaced.
+bool overlap(std::initializer_list<Buf> outputs, std::initializer_list<Buf> inputs) {
+  for (const Buf* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Buf& i : inputs)
+      if (share_bytes(*o, i)) return true;
+    for (const Buf* o2 = o + 1; o2 != outputs.end(); ++o2)
+      if (share_bytes(*o, *o2)) return true;
+  }
+  return false;
+}
+// bytes of rows x cols elements of bits each
+size_t bytes_of(long long rows, long long cols, int bits = 16) { return (size_t)rows * (size_t)cols * (size_t)bits / 8; }
 
 moe_status_t ensure_init(int* cus) {
   int dev = 0;
@@ -416,6 +441,13 @@ static moe_status_t group_gemm_mxfp4(const moe_operand_t* a_op, const moe_operan
   if (!a_op->scales || !b_op->scales || !c_bf16) return MOE_ERR_NULL;
   if (K % 32 != 0 || K >= kMaxMx4K || N >= kMaxMx4N) return MOE_ERR_SHAPE;
   if (!aligned16(a_op->data) || !aligned16(b_op->data) || !aligned16(c_bf16)) return MOE_ERR_ALIGN;
+  const int M = groups->M_cap, E = groups->E;
+  const long long EN = (long long)E * N;
+  if (overlap({{c_bf16, bytes_of(M, N)}, {groups->offsets_out, bytes_of(1, E + 1, 32)}, {groups->status_out, 4}},
+              {{a_op->data, bytes_of(M, K, a4 ? 4 : 8)}, {a_op->scales, bytes_of(M, K / 32, 8)},
+               {b_op->data, bytes_of(EN, K, 4)}, {b_op->scales, bytes_of(EN, K / 32, 8)},
+               {groups->counts, bytes_of(1, E, 32)}}))
+    return MOE_ERR_UNSUPPORTED;
   int cus;
   moe_status_t st = ensure_init(&cus);
   if (st != MOE_OK) return st;
@@ -677,6 +709,10 @@ moe_status_t moe_router_topk(const void* logits, int logits_dtype, int T, int E,
   if (st != MOE_OK) return st;
   if (!ids || !weights) return MOE_ERR_NULL;
   if (!aligned4(ids) || !aligned4(weights)) return MOE_ERR_ALIGN;
+  const size_t pairs = bytes_of(T, k, 32);
+  if (overlap({{ids, pairs}, {weights, pairs}},
+              {{logits, bytes_of(T, E, logits_dtype == MOE_DT_BF16 ? 16 : 32)}, {a.bias, bytes_of(1, E, 32)}}))
+    return MOE_ERR_UNSUPPORTED;
   int cus;
   if ((st = ensure_init(&cus)) != MOE_OK) return st;
   return launch_router(a, logits_dtype == MOE_DT_BF16, ids, weights, (hipStream_t)stream);
@@ -690,7 +726,8 @@ moe_status_t moe_router_topk_bwd(const void* logits, int logits_dtype, int T, in
   if (st != MOE_OK) return st;
   if (!ids || !dweights || !dlogits) return MOE_ERR_NULL;
   if (!aligned4(ids) || !aligned4(dweights) || !aligned16(dlogits)) return MOE_ERR_ALIGN;
-  if (dlogits == logits) return MOE_ERR_UNSUPPORTED;
+  const size_t pairs = bytes_of(T, k, 32), rows = bytes_of(T, E, logits_dtype == MOE_DT_BF16 ? 16 : 32);
+  if (overlap({{dlogits, rows}}, {{logits, rows}, {ids, pairs}, {dweights, pairs}})) return MOE_ERR_UNSUPPORTED;
   int cus;
   if ((st = ensure_init(&cus)) != MOE_OK) return st;
   return launch_router_bwd(a, logits_dtype == MOE_DT_BF16, ids, dweights, dlogits, (hipStream_t)stream);
@@ -710,7 +747,10 @@ moe_status_t moe_combine(const void* y, int M_cap, int H, const int32_t* dst, co
   if (st != MOE_OK) return st;
   if (!y || !out) return MOE_ERR_NULL;
   if (!aligned16(y) || !aligned16(out) || (residual && !aligned16(residual))) return MOE_ERR_ALIGN;
-  if (out == y) return MOE_ERR_UNSUPPORTED;
+  const size_t pairs = bytes_of(T, k, 32), rows = bytes_of(T, H);
+  if (overlap({{out, rows}}, {{y, bytes_of(M_cap, H)}, {dst, pairs}, {weights, pairs},
+                              {residual == out ? nullptr : residual, rows}}))
+    return MOE_ERR_UNSUPPORTED;
   int cus;
   if ((st = ensure_init(&cus)) != MOE_OK) return st;
   return launch_combine(static_cast<const uint16_t*>(y), M_cap, H, dst, weights, T, k,
@@ -726,7 +766,10 @@ moe_status_t moe_combine_bwd(const void* dout, const void* y, int M_cap, int H, 
   if (!aligned16(dout) || (y && !aligned16(y)) || (dy && !aligned16(dy)) ||
       (dweights && !aligned4(dweights)))
     return MOE_ERR_ALIGN;
-  if (dy && (dy == dout || dy == y)) return MOE_ERR_UNSUPPORTED;
+  const size_t pairs = bytes_of(T, k, 32), rows = bytes_of(M_cap, H);
+  if (overlap({{dy, rows}, {dweights, pairs}},
+              {{dout, bytes_of(T, H)}, {y, rows}, {dst, pairs}, {weights, pairs}}))
+    return MOE_ERR_UNSUPPORTED;
   int cus;
   if ((st = ensure_init(&cus)) != MOE_OK) return st;
   return launch_combine_bwd(static_cast<const uint16_t*>(dout), static_cast<const uint16_t*>(y), M_cap, H,
@@ -746,7 +789,11 @@ moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* we
   if (!aligned16(x) || !aligned16(weight) || (residual && !aligned16(residual)) || (h && !aligned16(h)) ||
       (y && !aligned16(y)) || (rstd && !aligned4(rstd)))
     return MOE_ERR_ALIGN;
-  if (y && (y == h || y == x || y == residual)) return MOE_ERR_UNSUPPORTED;
+  const size_t rows = bytes_of(T, H);
+  if (overlap({{y, rows}, {rstd, bytes_of(T, 1, 32)}, {q ? mx->row_q : nullptr, rows / 2},
+               {q ? mx->row_s : nullptr, rows / 64}, {h, rows}},
+              {{x == h ? nullptr : x, rows}, {residual == h ? nullptr : residual, rows}, {weight, bytes_of(1, H)}}))
+    return MOE_ERR_UNSUPPORTED;
   int cus;
   if ((st = ensure_init(&cus)) != MOE_OK) return st;
   NormArgs a;
@@ -785,7 +832,12 @@ moe_status_t moe_add_rmsnorm_bwd(const void* dy, const void* h, const void* weig
   if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned4(rstd) || (dh && !aligned16(dh)) ||
       (dx && !aligned16(dx)) || (dweight && !aligned4(dweight)) || (workspace && !aligned16(workspace)))
     return MOE_ERR_ALIGN;
-  if (dx && (dx == dy || dx == h)) return MOE_ERR_UNSUPPORTED;
+  const size_t rows = bytes_of(T, H);
+  if (overlap({{dx, rows}, {dweight, bytes_of(1, H, 32)},
+               {dweight ? workspace : nullptr, moe_add_rmsnorm_bwd_workspace_bytes(T, H)}},
+              {{dy, rows}, {h, rows}, {weight, bytes_of(1, H)}, {rstd, bytes_of(T, 1, 32)},
+               {dh == dx ? nullptr : dh, rows}}))
+    return MOE_ERR_UNSUPPORTED;
   int cus;
   moe_status_t st = ensure_init(&cus);
   if (st != MOE_OK) return st;
@@ -811,6 +863,9 @@ moe_status_t moe_mxfp4_quantize(const void* v, int R, int C, const moe_groups_t*
   if (groups && groups->M_cap != R) return MOE_ERR_SHAPE;
   if (R < 0 || C < 32 || C % 32 != 0) return MOE_ERR_SHAPE;
   if (!aligned16(v) || !aligned16(q)) return MOE_ERR_ALIGN;
+  if (overlap({{q, bytes_of(R, C, 4)}, {s, bytes_of(R, C / 32, 8)}},
+              {{v, bytes_of(R, C)}, {groups ? groups->counts : nullptr, groups ? bytes_of(1, groups->E, 32) : 0}}))
+    return MOE_ERR_UNSUPPORTED;
   int cus;
   if ((st = ensure_init(&cus)) != MOE_OK) return st;
   return launch_mx4_rows(static_cast<const uint16_t*>(v), R, C, groups ? groups->counts : nullptr,
@@ -825,6 +880,9 @@ moe_status_t moe_pack_weight_mxfp4(const void* src, int E, int N, int K, int src
   if ((long long)E * N >= (1LL << 31)) return MOE_ERR_SHAPE;
   if (src_layout != MOE_B_NK && src_layout != MOE_B_KN) return MOE_ERR_UNSUPPORTED;
   if (!aligned16(src) || !aligned16(dst_q)) return MOE_ERR_ALIGN;
+  const long long rows = (long long)E * N;
+  if (overlap({{dst_q, bytes_of(rows, K, 4)}, {dst_s, bytes_of(rows, K / 32, 8)}}, {{src, bytes_of(rows, K)}}))
+    return MOE_ERR_UNSUPPORTED;
   int cus;
   moe_status_t st = ensure_init(&cus);
   if (st != MOE_OK) return st;

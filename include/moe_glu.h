@@ -430,6 +430,11 @@ moe_status_t moe_dglu_unfused(const void* g, const void* z, const moe_groups_t* 
 moe_status_t moe_mxfp8_quantize(const void* v, int R, int C, const moe_groups_t* groups,
                                 const moe_mx_out_t* mx, void* stream);
 
+/* The operators around the GEMMs: the calls below and moe_group_gemm_quant with
+ * MXFP4 weights.  An output may not share bytes with an input or with another
+ * output, but where a call says that it may be the same buffer
+ * (MOE_ERR_UNSUPPORTED otherwise). */
+
 /* Router ([MEGA] §2.1: scores p = Softmax(W_r x), the k best experts of each
  * token, and their scores as the weights of the expert outputs).  From a
  * token's logits x [E]:
@@ -479,8 +484,7 @@ moe_status_t moe_router_topk(const void* logits, int logits_dtype, int T, int E,
  * twice in a token counts twice.  Where the weights are 0 by the rule above,
  * so is the gradient.  A renormalised softmax is the softmax over the chosen
  * logits and has no gradient at others (which are read only with a bias or
- * MOE_GROUP_TOP2, to see whether S is 0).  dlogits 16-byte aligned, else as above;
- * dlogits must not overlap the logits. */
+ * MOE_GROUP_TOP2, to see whether S is 0).  dlogits 16-byte aligned, else as above. */
 moe_status_t moe_router_topk_bwd(const void* logits, int logits_dtype, int T, int E, int k,
                                  const moe_router_t* router, const int32_t* ids, const float* dweights,
                                  void* dlogits, void* stream);
@@ -494,8 +498,8 @@ moe_status_t moe_router_topk_bwd(const void* logits, int logits_dtype, int T, in
  * dropped), weights fp32 [T][k] (NULL: all 1, which makes this call the
  * gradient of the row gather), residual bf16 [T][H] (NULL: none; the shared
  * expert's output or the residual stream), out bf16 [T][H], which may be the
- * residual itself but not overlap y.  Requires H % 8 == 0, H <= 2^26, 1 <= k
- * <= 16; y, residual and out 16-byte, dst and weights 4-byte aligned. */
+ * residual itself.  Requires H % 8 == 0, H <= 2^26, 1 <= k <= 16; y, residual
+ * and out 16-byte, dst and weights 4-byte aligned. */
 moe_status_t moe_combine(const void* y, int M_cap, int H, const int32_t* dst, const float* weights, int T,
                          int k, const void* residual, void* out, void* stream);
 
@@ -505,7 +509,7 @@ moe_status_t moe_combine(const void* y, int M_cap, int H, const int32_t* dst, co
  * with 0 in dweights for a pair without a row.  Rows of dy that no pair names
  * are not written.  A row belongs to one token (as moe_route_group's do); if
  * two slots of a token name it, it gets the sum of their gradients.  y is
- * needed for dweights only.  dy must not overlap dout or y. */
+ * needed for dweights only. */
 moe_status_t moe_combine_bwd(const void* dout, const void* y, int M_cap, int H, const int32_t* dst,
                              const float* weights, int T, int k, void* dy, float* dweights, void* stream);
 
@@ -517,9 +521,9 @@ moe_status_t moe_combine_bwd(const void* dout, const void* y, int M_cap, int H, 
  *   mx: row-wise MXFP8 copy of y (mx->row_q, row_s; byte-identical to
  *       moe_mxfp8_quantize of y; the transposed copy is MOE_ERR_UNSUPPORTED)
  * x, residual, h, y: bf16 [T][H]; weight bf16 [H]; rstd fp32 [T].  Each output
- * may be NULL, one is required.  h may be x or residual itself, y none of
- * them.  Requires H % 8 == 0, 8 <= H <= 16384 (H % 32 == 0 with mx), eps >= 0;
- * x, residual, weight, h and y 16-byte, rstd 4-byte aligned. */
+ * may be NULL, one is required.  h may be x or residual itself.  Requires H %
+ * 8 == 0, 8 <= H <= 16384 (H % 32 == 0 with mx), eps >= 0; x, residual, weight,
+ * h and y 16-byte, rstd 4-byte aligned. */
 moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* weight, int T, int H,
                              float eps, void* h, void* y, float* rstd, const moe_mx_out_t* mx, void* stream);
 
@@ -533,7 +537,7 @@ moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* we
  * dweight needs the workspace (moe_add_rmsnorm_bwd_workspace_bytes(T, H)
  * bytes, 16-byte aligned, contents of no meaning before or after; calls that
  * may run at the same time, replays of captured ones too, need one each); its
- * sums are added in a fixed order.  dx may be dh itself, not dy or h. */
+ * sums are added in a fixed order.  dx may be dh itself. */
 size_t moe_add_rmsnorm_bwd_workspace_bytes(int T, int H);
 moe_status_t moe_add_rmsnorm_bwd(const void* dy, const void* h, const void* weight, const float* rstd,
                                  const void* dh, int T, int H, void* dx, float* dweight, int accumulate,
