@@ -438,7 +438,8 @@ static moe_status_t group_gemm_mxfp4(const moe_operand_t* a_op, const moe_operan
   const bool a4 = a_op->dtype == MOE_DT_MXFP4;
   if ((!a4 && a_op->dtype != MOE_DT_MXFP8) || b_op->layout != MOE_B_NK) return MOE_ERR_UNSUPPORTED;
   if (mx && (mx->row_q || mx->col_q)) return MOE_ERR_UNSUPPORTED;
-  if (!a_op->scales || !b_op->scales || !c_bf16) return MOE_ERR_NULL;
+  const bool rows = groups->M_cap > 0;   // without rows A and C may be NULL
+  if (!b_op->scales || (rows && (!a_op->data || !a_op->scales || !c_bf16))) return MOE_ERR_NULL;
   if (K % 32 != 0 || K >= kMaxMx4K || N >= kMaxMx4N) return MOE_ERR_SHAPE;
   if (!aligned16(a_op->data) || !aligned16(b_op->data) || !aligned16(c_bf16)) return MOE_ERR_ALIGN;
   const int M = groups->M_cap, E = groups->E;
@@ -475,7 +476,8 @@ moe_status_t moe_group_gemm_quant(const moe_operand_t* a_op, const moe_operand_t
                                   const moe_mx_out_t* mx, int cu_margin, void* stream) {
   moe_status_t st = check_groups(groups);
   if (st != MOE_OK) return st;
-  if (!a_op || !b_op || !a_op->data || !b_op->data) return MOE_ERR_NULL;
+  if (!a_op || !b_op || !b_op->data) return MOE_ERR_NULL;
+  if (!a_op->data && (b_op->dtype != MOE_DT_MXFP4 || groups->M_cap > 0)) return MOE_ERR_NULL;
   if ((st = check_mx(mx)) != MOE_OK) return st;
   if (N < 64 || N % 64 != 0 || K < 32) return MOE_ERR_SHAPE;
   if (b_op->dtype == MOE_DT_MXFP4)   // MXFP4 weights (K % 32 == 0, checked there)
@@ -674,7 +676,7 @@ moe_status_t moe_mxfp8_quantize(const void* v, int R, int C, const moe_groups_t*
 
 static moe_status_t check_router(const void* logits, int logits_dtype, int T, int E, int k,
                                  const moe_router_t* r, RouterArgs* out) {
-  if (!logits || !r) return MOE_ERR_NULL;
+  if ((!logits && T != 0) || !r) return MOE_ERR_NULL;
   if (T < 0 || T > kMaxRouterTokens || E < 1 || E > kMaxExperts || k < 1 || k > kMaxTopk || k > E)
     return MOE_ERR_SHAPE;
   if (logits_dtype != MOE_DT_BF16 && logits_dtype != MOE_DT_FP32) return MOE_ERR_UNSUPPORTED;
@@ -707,7 +709,7 @@ moe_status_t moe_router_topk(const void* logits, int logits_dtype, int T, int E,
   RouterArgs a;
   moe_status_t st = check_router(logits, logits_dtype, T, E, k, router, &a);
   if (st != MOE_OK) return st;
-  if (!ids || !weights) return MOE_ERR_NULL;
+  if (T != 0 && (!ids || !weights)) return MOE_ERR_NULL;
   if (!aligned4(ids) || !aligned4(weights)) return MOE_ERR_ALIGN;
   const size_t pairs = bytes_of(T, k, 32);
   if (overlap({{ids, pairs}, {weights, pairs}},
@@ -724,7 +726,7 @@ moe_status_t moe_router_topk_bwd(const void* logits, int logits_dtype, int T, in
   RouterArgs a;
   moe_status_t st = check_router(logits, logits_dtype, T, E, k, router, &a);
   if (st != MOE_OK) return st;
-  if (!ids || !dweights || !dlogits) return MOE_ERR_NULL;
+  if (T != 0 && (!ids || !dweights || !dlogits)) return MOE_ERR_NULL;
   if (!aligned4(ids) || !aligned4(dweights) || !aligned16(dlogits)) return MOE_ERR_ALIGN;
   const size_t pairs = bytes_of(T, k, 32), rows = bytes_of(T, E, logits_dtype == MOE_DT_BF16 ? 16 : 32);
   if (overlap({{dlogits, rows}}, {{logits, rows}, {ids, pairs}, {dweights, pairs}})) return MOE_ERR_UNSUPPORTED;
@@ -734,7 +736,7 @@ moe_status_t moe_router_topk_bwd(const void* logits, int logits_dtype, int T, in
 }
 
 static moe_status_t check_combine(int M_cap, int H, const int32_t* dst, int T, int k, const float* weights) {
-  if (!dst) return MOE_ERR_NULL;
+  if (!dst && T != 0) return MOE_ERR_NULL;
   if (M_cap < 0 || T < 0 || k < 1 || k > kMaxTopk || H < 8 || H % 8 != 0 || H > kMaxCombineH)
     return MOE_ERR_SHAPE;
   if (!aligned4(dst) || (weights && !aligned4(weights))) return MOE_ERR_ALIGN;
@@ -745,7 +747,7 @@ moe_status_t moe_combine(const void* y, int M_cap, int H, const int32_t* dst, co
                          int k, const void* residual, void* out, void* stream) {
   moe_status_t st = check_combine(M_cap, H, dst, T, k, weights);
   if (st != MOE_OK) return st;
-  if (!y || !out) return MOE_ERR_NULL;
+  if ((!y && M_cap != 0) || (!out && T != 0)) return MOE_ERR_NULL;
   if (!aligned16(y) || !aligned16(out) || (residual && !aligned16(residual))) return MOE_ERR_ALIGN;
   const size_t pairs = bytes_of(T, k, 32), rows = bytes_of(T, H);
   if (overlap({{out, rows}}, {{y, bytes_of(M_cap, H)}, {dst, pairs}, {weights, pairs},
@@ -762,7 +764,8 @@ moe_status_t moe_combine_bwd(const void* dout, const void* y, int M_cap, int H, 
                              const float* weights, int T, int k, void* dy, float* dweights, void* stream) {
   moe_status_t st = check_combine(M_cap, H, dst, T, k, weights);
   if (st != MOE_OK) return st;
-  if (!dout || (!dy && !dweights) || (dweights && !y)) return MOE_ERR_NULL;
+  if ((!dout && T != 0) || (!dy && !dweights && M_cap != 0 && T != 0) || (dweights && !y && M_cap != 0))
+    return MOE_ERR_NULL;
   if (!aligned16(dout) || (y && !aligned16(y)) || (dy && !aligned16(dy)) ||
       (dweights && !aligned4(dweights)))
     return MOE_ERR_ALIGN;
@@ -770,6 +773,7 @@ moe_status_t moe_combine_bwd(const void* dout, const void* y, int M_cap, int H, 
   if (overlap({{dy, rows}, {dweights, pairs}},
               {{dout, bytes_of(T, H)}, {y, rows}, {dst, pairs}, {weights, pairs}}))
     return MOE_ERR_UNSUPPORTED;
+  if (!dy && !dweights) return MOE_OK;   // no tokens or no rows
   int cus;
   if ((st = ensure_init(&cus)) != MOE_OK) return st;
   return launch_combine_bwd(static_cast<const uint16_t*>(dout), static_cast<const uint16_t*>(y), M_cap, H,
@@ -778,12 +782,12 @@ moe_status_t moe_combine_bwd(const void* dout, const void* y, int M_cap, int H, 
 
 moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* weight, int T, int H,
                              float eps, void* h, void* y, float* rstd, const moe_mx_out_t* mx, void* stream) {
-  if (!x || !weight) return MOE_ERR_NULL;
+  if ((!x && T != 0) || !weight) return MOE_ERR_NULL;
   moe_status_t st = check_mx(mx);
   if (st != MOE_OK) return st;
   if (mx && mx->col_q) return MOE_ERR_UNSUPPORTED;
   const bool q = mx && mx->row_q;
-  if (!h && !y && !rstd && !q) return MOE_ERR_NULL;
+  if (!h && !y && !rstd && !q && T != 0) return MOE_ERR_NULL;
   if (T < 0 || H < 8 || H % 8 != 0 || H > kNormMaxH || (q && H % 32 != 0)) return MOE_ERR_SHAPE;
   if (!(eps >= 0.0f) || !isfinite(eps)) return MOE_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(weight) || (residual && !aligned16(residual)) || (h && !aligned16(h)) ||
@@ -822,7 +826,7 @@ size_t moe_add_rmsnorm_bwd_workspace_bytes(int T, int H) {
 moe_status_t moe_add_rmsnorm_bwd(const void* dy, const void* h, const void* weight, const float* rstd,
                                  const void* dh, int T, int H, void* dx, float* dweight, int accumulate,
                                  void* workspace, size_t workspace_bytes, void* stream) {
-  if (!dy || !h || !weight || !rstd || (!dx && !dweight)) return MOE_ERR_NULL;
+  if (!weight || (T != 0 && (!dy || !h || !rstd || (!dx && !dweight)))) return MOE_ERR_NULL;
   if (T < 0 || H < 8 || H % 8 != 0 || H > kNormMaxH) return MOE_ERR_SHAPE;
   if (accumulate != 0 && accumulate != 1) return MOE_ERR_UNSUPPORTED;
   if (dweight && T > 0) {
@@ -857,7 +861,7 @@ moe_status_t moe_add_rmsnorm_bwd(const void* dy, const void* h, const void* weig
 
 moe_status_t moe_mxfp4_quantize(const void* v, int R, int C, const moe_groups_t* groups, uint8_t* q,
                                 uint8_t* s, void* stream) {
-  if (!v || !q || !s) return MOE_ERR_NULL;
+  if (R != 0 && (!v || !q || !s)) return MOE_ERR_NULL;
   moe_status_t st;
   if (groups && (st = check_groups(groups)) != MOE_OK) return st;
   if (groups && groups->M_cap != R) return MOE_ERR_SHAPE;

@@ -433,7 +433,8 @@ moe_status_t moe_mxfp8_quantize(const void* v, int R, int C, const moe_groups_t*
 /* The operators around the GEMMs: the calls below and moe_group_gemm_quant with
  * MXFP4 weights.  An output may not share bytes with an input or with another
  * output, but where a call says that it may be the same buffer
- * (MOE_ERR_UNSUPPORTED otherwise). */
+ * (MOE_ERR_UNSUPPORTED otherwise).  An array without rows (of T = 0 tokens, of
+ * M_cap or R = 0 rows) may be NULL, as an empty tensor's address is. */
 
 /* Router ([MEGA] §2.1: scores p = Softmax(W_r x), the k best experts of each
  * token, and their scores as the weights of the expert outputs).  From a
@@ -473,7 +474,7 @@ typedef struct {
  * the weights moe_combine (or, grouped, the epilogue's row_scale).  Requires
  * 1 <= k <= 16, k <= E <= 1024, k <= topk_groups * E / n_groups (groups of at
  * least 2 experts for MOE_GROUP_TOP2), T <= 2^25; logits 16-byte, ids, weights
- * and bias 4-byte aligned.  T = 0 does nothing. */
+ * and bias 4-byte aligned.  T = 0 does nothing, here and below. */
 moe_status_t moe_router_topk(const void* logits, int logits_dtype, int T, int E, int k,
                              const moe_router_t* router, int32_t* ids, float* weights, void* stream);
 
@@ -533,7 +534,8 @@ moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* we
  *   dx = bf16(rstd (g - n mean(g n)) + dh)   bf16 [T][H], nullable: the
  *                                            gradient of x and of residual
  *   dweight = sum_t dy n                     fp32 [H], nullable; accumulate = 1
- *                                            adds to it
+ *                                            adds to it (T = 0: sets it to 0,
+ *                                            or adds nothing)
  * dweight needs the workspace (moe_add_rmsnorm_bwd_workspace_bytes(T, H)
  * bytes, 16-byte aligned, contents of no meaning before or after; calls that
  * may run at the same time, replays of captured ones too, need one each); its
