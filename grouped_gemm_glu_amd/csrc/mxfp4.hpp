@@ -436,7 +436,6 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
   constexpr int KB = A4 ? 8 : 4;          // blocks of 32 values per K-tile
   constexpr int KSN = KB / 2;             // k-steps per K-tile
   constexpr int NJB = A4 ? 4 : 2;         // DMA pieces (1 KB) of B per wave and K-tile; of A: 4
-  constexpr int kStores = 16;             // of a tile, per wave
   constexpr uint32_t kDrop = 0xFFFFFFF0u; // an offset behind every range
   constexpr int ABYTES = 32768;           // A's part of a stage, B's after it
   constexpr int SBYTES = ABYTES + 8192 * NJB;
@@ -620,7 +619,7 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
   for (;;) {
     // K-tile 0 of the tile is in stage 0, K-tiles 1 .. NST - 1 are on their way
     // to the other stages; the scales of all of them are stored.  Behind them the
-    // last tile's stores may be on their way (always kStores of a wave)
+    // last tile's stores may be on their way
     const long long ntile = tile + P;
     const bool more = ntile < total;
     Tile nxt_ = cur_;
@@ -717,16 +716,16 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
       // 2 after it may be on its way; with their scales' loads that is less than
       // what is, and waits for the oldest of them too), its scales are stored,
       // and every wave's reads of stage s are done.  FIRST: the tile's first
-      // round, whose K-tiles but the last were asked for before the last tile's
-      // stores, and their scales stored: the counter is in issue order, so the
-      // stores may still be on their way.
+      // round, whose K-tiles' scales are stored.  The last tile's stores came
+      // after its K-tiles' DMA and are waited for with them: their number is the
+      // compiler's choice (it merges and drops stores), so no count may rest on it.
       auto round = [&](auto first, int kt, const Fetch& ff, int fkt) {
         constexpr bool FIRST = decltype(first)::value;
         static_for<NST>([&](auto sc_) {
           constexpr int S = decltype(sc_)::value, NX = (S + 1) % NST;
           static_for<KSN - 1>([&](auto ks) { kstep(ks, sc_, ff, 0); });
           constexpr bool BEFORE = FIRST && S < NST - 1;
-          constexpr int VM = (NST - 2) * (4 + NJB) + (BEFORE ? kStores : 0);
+          constexpr int VM = (NST - 2) * (4 + NJB);
           __builtin_amdgcn_s_waitcnt(0x0F70 | (VM & 15) | ((VM >> 4) << 14));   // vmcnt(VM)
           if constexpr (!BEFORE)
             scale_store(scales(std::integral_constant<int, NX>{}), sv, std::integral_constant<int, NX>{},
@@ -782,17 +781,12 @@ __global__ __launch_bounds__(512, 1) void mx4_gemm_tile_kernel(Mx4Args p) {
           for (int d = 0; d < 8; ++d) w[d] = pack_bf16x2(acc[i][j][2 * d], acc[i][j][2 * d + 1]);
 #pragma unroll
           for (int d = 0; d < 4; ++d) swap16(w[d], w[4 + d]);
-          const uint32_t off = n < p.N - cur.n0 ? row + 2 * n : kDrop - 16 * (8 * i + 2 * j);
-          const uint32_t off16 = n < p.N - cur.n0 ? off + 16 * ((uint32_t)p.N * 2) : kDrop - 16 * (8 * i + 2 * j + 1);
+          const uint32_t off = n < p.N - cur.n0 ? row + 2 * n : kDrop;
+          const uint32_t off16 = n < p.N - cur.n0 ? off + 16 * ((uint32_t)p.N * 2) : kDrop;
           __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[0], w[1], w[2], w[3]}, C, off, 0, 0);
           __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[4], w[5], w[6], w[7]}, C, off16, 0, 0);
         }
       }
-      // (as many stores from either kind of tile, which round counts on: each of
-      // those that store nothing has an offset of its own, since the compiler
-      // drops a store that a later one covers)
-#pragma unroll
-      for (int i = 8 * MI; i < kStores; ++i) __builtin_amdgcn_raw_buffer_store_b128(u32x4{0, 0, 0, 0}, C, kDrop - 16 * i, 0, 0);
       static_for<NST - 1>([&](auto i) {
         constexpr std::integral_constant<int, decltype(i)::value + 1> s{};
         scale_store(scales(s), sv, s, s);
