@@ -778,12 +778,37 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 4 : NC <= 4 ? 6 : 4) void add_rmsn
       for (int q = 0; q < 8; ++q) s8 = fmaf(v[c][q], v[c][q], s8);
       sq += (double)s8;
     }
+    double mean = block_sum<NT / 64>(sq, tmp) * p.inv_h + (double)p.eps;
+    float m32 = (float)mean;
+    double unit = 1.0;
+    if (!(m32 > 1e-30f && m32 < 1e30f)) {   // (the whole workgroup)
+      // squares that pass fp32's range: the sum again of values in another unit,
+      // which small values keep below
+      const bool small = m32 < 1.0f;
+      const float u = small ? 0x1p100f : 0x1p-70f;
+      sq = 0.0;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if (c * NT + (int)threadIdx.x >= nch) continue;
+        float s8 = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float t = v[c][q] * u;
+          s8 = fmaf(t, t, s8);
+          v[c][q] = small ? t : v[c][q];
+        }
+        sq += (double)s8;
+      }
+      unit = (double)u;
+      mean = block_sum<NT / 64>(sq, tmp) * p.inv_h + (double)p.eps * unit * unit;
+      m32 = (float)mean;
+    }
     // 1 / sqrt in 32 bits and one Newton step in 64
-    const double mean = block_sum<NT / 64>(sq, tmp) * p.inv_h + (double)p.eps;
-    const float m32 = (float)mean, r32 = 1.0f / sqrtf(m32);
-    double rd = (double)r32;
-    if (m32 > 1e-30f && m32 < 1e30f) rd = rd * (1.5 - 0.5 * mean * rd * rd);
-    const float rstd = (float)rd, rlow = m32 > 1e-30f && m32 < 1e30f ? (float)(rd - (double)rstd) : 0.0f;
+    double rd = (double)(1.0f / sqrtf(m32));
+    if (m32 > 0.0f && m32 < INFINITY) rd = rd * (1.5 - 0.5 * mean * rd * rd);
+    const float rstd = (float)(rd * unit);
+    if (unit < 1.0) rd *= unit;
+    const float rh = (float)rd, rlow = rd < (double)INFINITY ? (float)(rd - (double)rh) : 0.0f;
     if (p.rstd && threadIdx.x == 0) p.rstd[r] = rstd;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -793,7 +818,7 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 4 : NC <= 4 ? 6 : 4) void add_rmsn
       float w[8];
       unpack8(kEarly ? wt[c] : *reinterpret_cast<const uint4*>(p.weight + ch * 8), w);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) w[q] = norm_value(v[c][q], rstd, rlow, w[q]);
+      for (int q = 0; q < 8; ++q) w[q] = norm_value(v[c][q], rh, rlow, w[q]);
       const uint4 yv = pack8(w);
       if (p.y) *reinterpret_cast<uint4*>(p.y + at) = yv;
       if (p.q) {
