@@ -71,5 +71,10 @@ moe_status_t launch_mx4_rows(const uint16_t* v, int R, int C, const int* counts,
 moe_status_t launch_mx4_weight_kn(const uint16_t* src, int E, int N, int K, uint8_t* q, uint8_t* s,
                                   hipStream_t st);
 moe_status_t launch_mx4_gemm(const Mx4Args& a, bool a4, int cus, hipStream_t st);
+// Whether such a product of cus compute units goes to the 256 x 256 tiles, or to
+// the kernel that streams the weights past 16 rows at a time.  Not part of the
+// public interface; a symbol of its own so that a test of a kernel can tell that
+// its sizes reach it.
+extern "C" int moe_mx4_takes_tiles(int M_cap, int E, int N, int K, int a4, int cus);
 
 }  // namespace moe

@@ -356,7 +356,9 @@ moe_status_t moe_group_gemm_dglu_bwd(const void* dy2, const moe_operand_t* w2, i
  * are MOE_ERR_UNSUPPORTED.  Requires K % 32 == 0, K < 2^24, N % 64 == 0, N <
  * 2^23; codes and c 16-byte aligned, scales any.  The call takes any group
  * sizes, from one row per expert (decoding, where it streams the active
- * experts' weights once) up. */
+ * experts' weights once) up; which of its kernels runs goes by M_cap, since
+ * the host does not know the counts, so a decoding batch is best given the
+ * capacity that it can fill. */
 moe_status_t moe_group_gemm_quant(const moe_operand_t* a, const moe_operand_t* b, int N, int K,
                                   const moe_groups_t* groups, void* c_bf16,
                                   const moe_mx_out_t* mx, int cu_margin, void* stream);
