@@ -133,22 +133,34 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-def _current_stream():
+def _first_current_stream():
     """torch's current stream of the current device, as a raw handle.  The two
     calls that torch's own generated code uses for it take 0.2 us; building the
-    stream object of the public call takes 2.8 us, as long as a small kernel."""
+    stream object of the public call takes 2.8 us, as long as a small kernel.
+    torch's initialisation (and its refusal in a forked child) comes first, once
+    per process."""
     global _current_stream
     import torch
     raw, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    torch.cuda.init()
     if raw is not None and dev is not None:
-        torch.cuda.init()
-
         def _current_stream():
             return raw(dev())
     else:
         def _current_stream():
             return torch.cuda.current_stream().cuda_stream
     return _current_stream()
+
+
+_current_stream = _first_current_stream
+
+
+def _forget_stream():
+    global _current_stream
+    _current_stream = _first_current_stream
+
+
+os.register_at_fork(after_in_child=_forget_stream)
 
 
 def _stream(stream) -> Optional[int]:
