@@ -182,6 +182,17 @@ __device__ __forceinline__ i32x8 mx4_frag(i32x4 v) {
   return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
 }
 
+// What the f8f6f4 MFMA's sums are worth, of random codes against sums in 64 bits:
+// with two e2m1 operands an instruction's products are added to fp32's rounding
+// (2.4e-8 of their sizes' sum).  With an e4m3 operand, products are cut off below
+// the largest one: an instruction of 64 values is off by up to 2^-11.8 of its
+// largest product (6.8e-5 of the sizes' sum), whatever the accumulator holds,
+// whose addition is rounded as fp32's.  The other operand's format and the plain
+// e4m3 MFMA make no difference, so no order of sums avoids it; bf16 products of the
+// decoded values would, at half the MFMA's peak.  Of 16384 x 4096 outputs of 8-bit
+// rows, K = 7168, 0.4% are not the nearest bf16; the MXFP8 products are the same in
+// this.
+
 // ---------------------------------------------------------------- few rows
 // The tiles of BM rows of up to 64 experts, lane e holding expert e's: built
 // and searched by each wave alone, without LDS or barriers.
@@ -417,10 +428,11 @@ __device__ __forceinline__ int mx4_off64(int r, int c) { return r * 64 + ((c ^ (
 // from registers alone, so that its stores and the next tile's first loads
 // overlap.
 // What bounds it, by leaving parts out (16384 rows in 32 groups x 4096 x 7168,
-// 256 CUs): e2m1 rows 275 us (3.5 PFLOP/s), with every operand read from L2
-// again and again 247, without the MFMAs 251, without both 152; the MFMAs alone
-// 151, at the 6.1 PFLOP/s that random codes reach at most, the chip being
-// power-limited.  e4m3 rows 402 us, 364, 330, 212 and 243.  So the operands'
+// 256 CUs): e2m1 rows 283 us (3.4 PFLOP/s), with every operand read from L2
+// again and again 254, without the MFMAs 254, without both 164; the MFMAs alone
+// would take 159, at the 6.05 PFLOP/s that random codes sustain, the chip being
+// power-limited.  e4m3 rows 411 us (390 on another chip), 383, 330, 214 and, at
+// 3.8 PFLOP/s, 253.  So the operands'
 // way through L2 and LDS and the MFMAs, each near the half of it, overlap in part,
 // and misses in L2 cost the rest.  An L2 prefetch two K-tiles ahead made it 5%
 // (weights alone, shared out) to 15% slower: the requests of a CU are scarce.

@@ -254,11 +254,13 @@ __device__ __forceinline__ float of_rank_key32(uint32_t k) {
 // their errors (twice that each, and the sum's rounding), is done again in 64 bits
 // by the whole wave.
 // Bound by instructions and their latency: a round of the choice is about 80 for
-// 64 / L tokens.  256 experts in 8 groups, k = 8, sigmoid and bias: one token 5.0
-// us (a launch that does nothing takes 3.6), 16384 tokens 19 us, of which the
-// few tokens of 64 bits, whose waves end last, are about 5 (without a bias, where
-// none needs them, 10); 65536 tokens 50 us.  A token per wave in 64 bits
-// throughout took 55 us for 16384, and one token 11.
+// 64 / L tokens.  256 experts in 8 groups, k = 8, sigmoid and bias: one token 4.9
+// us (a launch that does nothing takes 3.6), 16384 tokens 20 us, of which the
+// few tokens of 64 bits, whose waves end last, are about 5; 65536 tokens 49 us.
+// Without a bias 16384 tokens take 13.5 us, without groups too 9.5, and no token
+// of the latter needs 64 bits.  Equal choice values among a token's best are not
+// told apart in 32 bits either: a bias of zeros on bf16 logits, which has many, takes
+// 44 us.  A token per wave in 64 bits throughout took 55 us, and one token 11.
 template <int L, int NI, bool BF16>
 __global__ __launch_bounds__(256) void router_kernel(RouterArgs p, int* __restrict__ ids,
                                                      float* __restrict__ weights) {
