@@ -151,3 +151,16 @@ def test_router_scale_and_small_scores(G, score, scale):  # noqa: F811
     _run(G, x, 4, False, bias, None, score=score, scale=scale)
     x[:, 8:] -= np.linspace(0, 66, 20, dtype=np.float32)[:, None]
     _run(G, x, 4, False, None, None, score=score, scale=scale)
+
+
+# ---------------------------------------------------------------- every width of the groups' merges
+@pytest.mark.parametrize("T", [30, 2100])
+@pytest.mark.parametrize("E,groups,keep", [(256, 64, 20), (256, 32, 9), (256, 16, 5), (256, 8, 3), (256, 4, 2), (256, 2, 1),
+                                           (512, 2, 1), (512, 8, 7), (1024, 4, 3), (1024, 8, 2), (96, 3, 2), (640, 5, 2)])
+def test_router_group_widths(G, T, E, groups, keep):  # noqa: F811
+    """Groups of 4 to 256 experts, in 16, 32 and 64 lanes per token."""
+    rng = np.random.default_rng(E + groups)
+    x = rng.standard_normal((T, E))
+    bias = (rng.standard_normal(E) * 0.3).astype(np.float32)
+    _run(G, x, 6, False, bias, None, score="sigmoid", n_groups=groups, topk_groups=keep, group_score="top2")
+    _run(G, x, 6, True, None, None, score="softmax", n_groups=groups, topk_groups=keep, group_score="max")
