@@ -63,6 +63,29 @@ class RouterT(ctypes.Structure):
                 ("renorm", ctypes.c_int32), ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
 
 
+class LoraT(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("r", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("x_ld", ctypes.c_int64), ("y_ld", ctypes.c_int64)]
+
+
+class AdamwTensorT(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("lr_scale", ctypes.c_float),
+                ("weight_decay", ctypes.c_float), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("state_bits", ctypes.c_int32)]
+
+
+class AdamwPlanT(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_tensors", ctypes.c_int32), ("n_chunks", ctypes.c_int64)]
+
+
+class AdamwT(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("step_dev", ctypes.c_void_p),
+                ("lr_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
@@ -104,6 +127,17 @@ _SIGS = {
     "moe_add_rmsnorm_bwd": ([_P, _P, _P, _P, _P, _I, _I, _P, _P, _I, _P, _Z, _P], _I),
     "moe_mxfp4_quantize": ([_P, _I, _I, ctypes.POINTER(GroupsT), _P, _P, _P], _I),
     "moe_pack_weight_mxfp4": ([_P, _I, _I, _I, _I, _P, _P, _P], _I),
+    "moe_lora_fwd_workspace_bytes": ([_I, _I, _I, _I, _I], _Z),
+    "moe_lora_fwd": ([_P, _I, _P, ctypes.POINTER(GroupsT), ctypes.POINTER(LoraT), _P, _P, _P, _P, _Z, _P], _I),
+    "moe_lora_bwd_workspace_bytes": ([_I, _I, _I, _I, _I], _Z),
+    "moe_lora_bwd": ([_P, _P, _I, _P, ctypes.POINTER(GroupsT), ctypes.POINTER(LoraT), _P, _P, _P, _P, _P, _I, _P, _Z,
+                      _P], _I),
+    "moe_adamw_plan_bytes": ([ctypes.POINTER(AdamwTensorT), _I], _Z),
+    "moe_adamw_plan": ([ctypes.POINTER(AdamwTensorT), _I, _P, _Z, ctypes.POINTER(AdamwPlanT)], _I),
+    "moe_adamw_step": ([ctypes.POINTER(AdamwPlanT), ctypes.POINTER(AdamwT), _P], _I),
+    "moe_adamw_unpack": ([_P, _P, _P, _P, ctypes.c_int64, _P, _P, _P], _I),
+    "moe_grad_norm_workspace_bytes": ([], _Z),
+    "moe_grad_norm": ([ctypes.POINTER(AdamwPlanT), _F, _P, _P, _Z, _P], _I),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -228,16 +262,76 @@ def router(score: str = "softmax", bias=None, n_groups: int = 1, topk_groups: in
                          1 if renorm else 0, scale, _ptr(bias)), bias)
 
 
-def _logits_dtype(logits, dtype: Optional[int]) -> int:
-    """The moe_dtype_t of a logits tensor (float32, or bfloat16 also as int16 storage)."""
-    if dtype is not None:
-        return dtype
-    name = str(logits.dtype)
+def _float_dtype(what: str, t) -> int:
+    """The moe_dtype_t of a tensor (float32, or bfloat16 also as int16 storage)."""
+    name = str(t.dtype)
     if name == "torch.float32":
         return DT_FP32
     if name in ("torch.bfloat16", "torch.int16"):
         return DT_BF16
-    raise TypeError(f"router logits are float32 or bfloat16, not {name}")
+    raise TypeError(f"{what} are float32 or bfloat16, not {name}")
+
+
+def _logits_dtype(logits, dtype: Optional[int]) -> int:
+    return _float_dtype("router logits", logits) if dtype is None else dtype
+
+
+def lora(A, B, r: int, K: int, N: int, scale=None, x_ld: int = 0, y_ld: int = 0) -> LoraT:
+    """Builds the moe_lora_t struct: A bfloat16 [E, r, K], B bfloat16 [E, N, r], scale float32 [E]."""
+    return _keep(LoraT(_ptr(A), _ptr(B), _ptr(scale), r, K, N, x_ld, y_ld), A, B, scale)
+
+
+def adamw_tensor(param, grad, m, v, master=None, m_scale=None, v_scale=None, weight_decay: float = 0.0,
+                 lr_scale: float = 1.0) -> AdamwTensorT:
+    """Builds the moe_adamw_tensor_t struct of a step's tensor (contiguous torch tensors of the same number of
+    elements).  States of 8 bits are an int8 m and a uint8 v with their scales; ``param`` None: a gradient that
+    takes part in the norm alone."""
+    n = grad.numel()
+    bits = 32
+    if param is not None:
+        kinds = (str(m.dtype), str(v.dtype))
+        if kinds == ("torch.int8", "torch.uint8"):
+            bits = 8
+        elif kinds != ("torch.float32", "torch.float32"):
+            raise TypeError(f"states are float32, or int8 and uint8, not {kinds[0]} and {kinds[1]}")
+        if master is not None and str(master.dtype) != "torch.float32":
+            raise TypeError(f"a master is float32, not {master.dtype}")
+        blocks = (n + 127) // 128
+        for name, t, size in (("param", param, n), ("master", master, n), ("m", m, n), ("v", v, n),
+                              ("m_scale", m_scale, blocks), ("v_scale", v_scale, blocks)):
+            if t is not None and t.numel() != size:
+                raise ValueError(f"{name} has {t.numel()} elements, not {size}")
+    for t in (param, grad, m, v, master, m_scale, v_scale):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("the tensors of a step are contiguous")
+    return _keep(AdamwTensorT(_ptr(param), _ptr(grad), _ptr(master), _ptr(m), _ptr(v), _ptr(m_scale), _ptr(v_scale),
+                              n, lr_scale, weight_decay,
+                              DT_FP32 if param is None else _float_dtype("parameters", param),
+                              _float_dtype("gradients", grad), bits), param, grad, master, m, v, m_scale, v_scale)
+
+
+def adamw_plan(tensors, device=None) -> AdamwPlanT:
+    """Lays out the tensors of a step (adamw_tensor structs) once, with the table in the memory of ``device`` (the
+    current one), copied before the call returns.  The plan keeps the tensors alive."""
+    import torch
+    tensors = list(tensors)
+    array = (AdamwTensorT * max(1, len(tensors)))(*tensors)
+    size = _lib.moe_adamw_plan_bytes(array, len(tensors))
+    host = torch.zeros(max(8, size), dtype=torch.uint8)
+    plan = AdamwPlanT()
+    _check("moe_adamw_plan", _lib.moe_adamw_plan(array, len(tensors), host.data_ptr(), size, ctypes.byref(plan)))
+    table = host.to("cuda" if device is None else device)
+    torch.cuda.current_stream(table.device).synchronize()
+    plan.table = table.data_ptr()
+    return _keep(plan, table, tensors)
+
+
+def adamw(lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, step: int = 1, step_dev=None,
+          lr_dev=None, grad_scale=None) -> AdamwT:
+    """Builds the moe_adamw_t struct; ``step_dev`` (int32), ``lr_dev`` and ``grad_scale`` (float32) are one-element
+    device tensors that the kernel reads."""
+    return _keep(AdamwT(lr, beta1, beta2, eps, step, _ptr(step_dev), _ptr(lr_dev), _ptr(grad_scale)), step_dev, lr_dev,
+                 grad_scale)
 
 
 def _ref(x):
@@ -421,6 +515,55 @@ def moe_pack_weight_mxfp4(src, E, N, K, src_layout, dst_q, dst_s, stream=None):
     _check("moe_pack_weight_mxfp4",
            _lib.moe_pack_weight_mxfp4(_ptr(src), E, N, K, src_layout, _ptr(dst_q), _ptr(dst_s),
                                       _stream(stream)))
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def moe_lora_fwd_workspace_bytes(M_cap: int, E: int, r: int, K: int, N: int) -> int:
+    return _lib.moe_lora_fwd_workspace_bytes(M_cap, E, r, K, N)
+
+
+def moe_lora_fwd(x, T, grp: GroupsT, lo: LoraT, y, base=None, src=None, u=None, workspace=None, stream=None):
+    """``workspace``: a tensor of at least moe_lora_fwd_workspace_bytes(M_cap, E, r, K, N) bytes."""
+    _check("moe_lora_fwd",
+           _lib.moe_lora_fwd(_ptr(x), T, _ptr(src), ctypes.byref(grp), ctypes.byref(lo), _ptr(base), _ptr(y), _ptr(u),
+                             _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def moe_lora_bwd_workspace_bytes(M_cap: int, E: int, r: int, K: int, N: int) -> int:
+    return _lib.moe_lora_bwd_workspace_bytes(M_cap, E, r, K, N)
+
+
+def moe_lora_bwd(dy, x, T, grp: GroupsT, lo: LoraT, u, dx=None, dx_base=None, dA=None, dB=None,
+                 accumulate: bool = False, src=None, workspace=None, stream=None):
+    """``workspace``: a tensor of at least moe_lora_bwd_workspace_bytes(M_cap, E, r, K, N) bytes."""
+    _check("moe_lora_bwd",
+           _lib.moe_lora_bwd(_ptr(dy), _ptr(x), T, _ptr(src), ctypes.byref(grp), ctypes.byref(lo), _ptr(u),
+                             _ptr(dx_base), _ptr(dx), _ptr(dA), _ptr(dB), 1 if accumulate else 0, _ptr(workspace),
+                             _nbytes(workspace), _stream(stream)))
+
+
+def moe_adamw_step(plan: AdamwPlanT, hyper: AdamwT, stream=None):
+    _check("moe_adamw_step", _lib.moe_adamw_step(ctypes.byref(plan), ctypes.byref(hyper), _stream(stream)))
+
+
+def moe_adamw_unpack(m, m_scale, v, v_scale, n, m_out=None, v_out=None, stream=None):
+    _check("moe_adamw_unpack",
+           _lib.moe_adamw_unpack(_ptr(m), _ptr(m_scale), _ptr(v), _ptr(v_scale), n, _ptr(m_out), _ptr(v_out),
+                                 _stream(stream)))
+
+
+def moe_grad_norm_workspace_bytes() -> int:
+    return _lib.moe_grad_norm_workspace_bytes()
+
+
+def moe_grad_norm(plan: AdamwPlanT, max_norm, out, workspace, stream=None):
+    """``out``: float32 [2], the norm and the clip factor (``out[1:]`` serves as adamw's grad_scale)."""
+    _check("moe_grad_norm",
+           _lib.moe_grad_norm(ctypes.byref(plan), max_norm, _ptr(out), _ptr(workspace), _nbytes(workspace),
+                              _stream(stream)))
 
 
 def raw_call(name: str, *args) -> int:

@@ -29,7 +29,7 @@ LIB = os.path.join(PKG, "libmoeglu.so")
 SOURCES = ([("api.hip", "api", []), ("gemm_fwd.hip", "gemm_fwd", []), ("gemm_bwd.hip", "gemm_bwd", []),
             ("gemm_mx.hip", "gemm_mx", []), ("gemm_wgrad.hip", "gemm_wgrad", []),
             ("gemm_wgrad_mx.hip", "gemm_wgrad_mx", []), ("token_ops.hip", "token_ops", []),
-            ("mxfp4.hip", "mxfp4", [])]
+            ("mxfp4.hip", "mxfp4", []), ("lora.hip", "lora", []), ("adamw.hip", "adamw", [])]
            + [(f"gemm_act_{d}.hip", f"gemm_act_{d}_{a}", [f"-DMOE_ACT={a}"])
               for d in ("bwd", "fwd") for a in range(4)])
 ARCH = "gfx950"

@@ -5,7 +5,9 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <initializer_list>
+#include <new>
 
 #include "aux_kernels.hpp"
 #include "internal.hpp"
@@ -896,6 +898,276 @@ moe_status_t moe_pack_weight_mxfp4(const void* src, int E, int N, int K, int src
   if (src_layout == MOE_B_NK)
     return launch_mx4_rows(w, E * N, K, nullptr, 0, q, sc, cus, (hipStream_t)stream);
   return launch_mx4_weight_kn(w, E, N, K, q, sc, (hipStream_t)stream);
+}
+
+static bool lora_sizes(int M_cap, int E, int r, int K, int N) {
+  return M_cap >= 0 && M_cap <= kMaxLoraRows && E >= 1 && E <= kMaxExperts && r >= 8 && r <= kMaxLoraRank &&
+         r % 8 == 0 && K >= 8 && K % 8 == 0 && K <= kMaxLoraCols && N >= 8 && N % 8 == 0 && N <= kMaxLoraCols;
+}
+
+size_t moe_lora_fwd_workspace_bytes(int M_cap, int E, int r, int K, int N) {
+  return lora_sizes(M_cap, E, r, K, N) ? lora_fwd_workspace({M_cap, E, r, K, N}) : 0;
+}
+size_t moe_lora_bwd_workspace_bytes(int M_cap, int E, int r, int K, int N) {
+  return lora_sizes(M_cap, E, r, K, N) ? lora_bwd_workspace({M_cap, E, r, K, N}) : 0;
+}
+
+static moe_status_t check_lora(int T, const int32_t* src, const moe_groups_t* groups, const moe_lora_t* lora,
+                               LoraArgs* out) {
+  moe_status_t st = check_groups(groups);
+  if (st != MOE_OK) return st;
+  if (!lora || !lora->A || !lora->B) return MOE_ERR_NULL;
+  if (T < 0 || !lora_sizes(groups->M_cap, groups->E, lora->r, lora->K, lora->N)) return MOE_ERR_SHAPE;
+  const long long x_ld = lora->x_ld ? lora->x_ld : lora->K, y_ld = lora->y_ld ? lora->y_ld : lora->N;
+  if (x_ld < lora->K || x_ld % 8 != 0 || x_ld > (1LL << 32) || y_ld < lora->N || y_ld % 8 != 0 || y_ld > (1LL << 32))
+    return MOE_ERR_SHAPE;
+  if (!aligned16(lora->A) || !aligned16(lora->B) || !aligned4(lora->scale) || !aligned4(src)) return MOE_ERR_ALIGN;
+  out->g = {groups->counts, groups->E, groups->M_cap, groups->offsets_out, groups->status_out, src, T};
+  out->A = static_cast<const uint16_t*>(lora->A);
+  out->B = static_cast<const uint16_t*>(lora->B);
+  out->scale = lora->scale;
+  out->r = lora->r;
+  out->K = lora->K;
+  out->N = lora->N;
+  out->x_ld = x_ld;
+  out->y_ld = y_ld;
+  return MOE_OK;
+}
+// bytes from the first to the last element of T rows of cols, ld apart
+static size_t strided_bytes(int T, long long ld, int cols) { return T == 0 ? 0 : bytes_of(T - 1, ld) + bytes_of(1, cols); }
+
+moe_status_t moe_lora_fwd(const void* x, int T, const int32_t* src, const moe_groups_t* groups,
+                          const moe_lora_t* lora, const void* base, void* y, float* u, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  LoraArgs a;
+  moe_status_t st = check_lora(T, src, groups, lora, &a);
+  if (st != MOE_OK) return st;
+  const int M = a.g.M_cap, L = a.g.L;
+  const size_t need = moe_lora_fwd_workspace_bytes(M, L, a.r, a.K, a.N);
+  if (T != 0 && (!x || !y || (M != 0 && !workspace))) return MOE_ERR_NULL;
+  if (T != 0 && M != 0 && workspace_bytes < need) return MOE_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(base) || !aligned16(u) || !aligned16(workspace)) return MOE_ERR_ALIGN;
+  const size_t yb = strided_bytes(T, a.y_ld, a.N);
+  if (overlap({{y, yb}, {u, bytes_of(M, a.r, 32)}, {workspace, T != 0 && M != 0 ? need : 0},
+               {a.g.offsets_out, bytes_of(L + 1, 1, 32)}, {a.g.status_out, 4}},
+              {{x, strided_bytes(T, a.x_ld, a.K)}, {base == y ? nullptr : base, yb}, {src, bytes_of(M, 1, 32)},
+               {a.g.counts, bytes_of(L, 1, 32)}, {a.A, bytes_of(L, (long long)a.r * a.K)},
+               {a.B, bytes_of(L, (long long)a.r * a.N)}, {a.scale, bytes_of(L, 1, 32)}}))
+    return MOE_ERR_UNSUPPORTED;
+  int cus;
+  if ((st = ensure_init(&cus)) != MOE_OK) return st;
+  return launch_lora_fwd(a, static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(base),
+                         static_cast<uint16_t*>(y), u, workspace, (hipStream_t)stream);
+}
+
+moe_status_t moe_lora_bwd(const void* dy, const void* x, int T, const int32_t* src, const moe_groups_t* groups,
+                          const moe_lora_t* lora, const float* u, const void* dx_base, void* dx, float* dA,
+                          float* dB, int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  LoraArgs a;
+  moe_status_t st = check_lora(T, src, groups, lora, &a);
+  if (st != MOE_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_UNSUPPORTED;
+  const int M = a.g.M_cap, L = a.g.L;
+  const bool rows = T != 0 && M != 0;
+  const size_t need = moe_lora_bwd_workspace_bytes(M, L, a.r, a.K, a.N);
+  if ((T != 0 && !dy) || (rows && ((dA && !x) || (dB && !u) || !workspace || (!dx && !dA && !dB)))) return MOE_ERR_NULL;
+  if (rows && workspace_bytes < need) return MOE_ERR_SHAPE;
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(u) || !aligned16(dx_base) || !aligned16(dx) || !aligned16(dA) ||
+      !aligned16(dB) || !aligned16(workspace))
+    return MOE_ERR_ALIGN;
+  const size_t xb = strided_bytes(T, a.x_ld, a.K);
+  const long long wa = (long long)a.r * a.K, wb = (long long)a.r * a.N;
+  if (overlap({{dx, xb}, {dA, bytes_of(L, wa, 32)}, {dB, bytes_of(L, wb, 32)}, {workspace, rows ? need : 0},
+               {a.g.offsets_out, bytes_of(L + 1, 1, 32)}, {a.g.status_out, 4}},
+              {{dy, strided_bytes(T, a.y_ld, a.N)}, {x, xb}, {u, bytes_of(M, a.r, 32)},
+               {dx_base == dx ? nullptr : dx_base, xb}, {src, bytes_of(M, 1, 32)}, {a.g.counts, bytes_of(L, 1, 32)},
+               {a.A, bytes_of(L, wa)}, {a.B, bytes_of(L, wb)}, {a.scale, bytes_of(L, 1, 32)}}))
+    return MOE_ERR_UNSUPPORTED;
+  int cus;
+  if ((st = ensure_init(&cus)) != MOE_OK) return st;
+  return launch_lora_bwd(a, static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x), u,
+                         static_cast<const uint16_t*>(dx_base), static_cast<uint16_t*>(dx), dA, dB, accumulate,
+                         workspace, (hipStream_t)stream);
+}
+
+static moe_status_t check_adamw_tensor(const moe_adamw_tensor_t& t) {
+  if (t.n < 0 || t.n > (1LL << 42)) return MOE_ERR_SHAPE;
+  if (t.n > 0 && !t.grad) return MOE_ERR_NULL;
+  if (t.grad_dtype != MOE_DT_BF16 && t.grad_dtype != MOE_DT_FP32) return MOE_ERR_UNSUPPORTED;
+  if (!aligned16(t.grad)) return MOE_ERR_ALIGN;
+  if (!t.param) return MOE_OK;
+  if (t.param_dtype != MOE_DT_BF16 && t.param_dtype != MOE_DT_FP32) return MOE_ERR_UNSUPPORTED;
+  if (t.state_bits != 32 && t.state_bits != 8) return MOE_ERR_UNSUPPORTED;
+  if (t.master && t.param_dtype != MOE_DT_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!isfinite(t.lr_scale) || !isfinite(t.weight_decay)) return MOE_ERR_SHAPE;
+  if (t.n > 0 && (!t.m || !t.v || (t.state_bits == 8 && (!t.m_scale || !t.v_scale)))) return MOE_ERR_NULL;
+  if (!aligned16(t.param) || !aligned16(t.master) || !aligned16(t.m) || !aligned16(t.v) ||
+      (t.state_bits == 8 && (!aligned4(t.m_scale) || !aligned4(t.v_scale))))
+    return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+static long long adamw_chunks(const moe_adamw_tensor_t& t) { return (t.n + kAdamwChunk - 1) / kAdamwChunk; }
+
+size_t moe_adamw_plan_bytes(const moe_adamw_tensor_t* tensors, int n_tensors) {
+  if (n_tensors <= 0 || !tensors) return 0;
+  size_t chunks = 0;
+  for (int i = 0; i < n_tensors; ++i) {
+    if (tensors[i].n < 0 || tensors[i].n > (1LL << 42)) return 0;
+    chunks += (size_t)adamw_chunks(tensors[i]);
+  }
+  return (size_t)n_tensors * sizeof(AdamwTensor) + chunks * sizeof(AdamwChunk);
+}
+
+// Whether an output of the tensors shares bytes with any other buffer of them:
+// neighbours by address are looked at, with the furthest end so far.
+static moe_status_t adamw_overlap(const moe_adamw_tensor_t* tensors, int n_tensors) {
+  struct Range {
+    uintptr_t begin, end;
+    bool output;
+  };
+  Range* r = new (std::nothrow) Range[(size_t)n_tensors * 7];
+  if (!r) return MOE_ERR_SHAPE;
+  size_t k = 0;
+  for (int i = 0; i < n_tensors; ++i) {
+    const moe_adamw_tensor_t& t = tensors[i];
+    const auto add = [&](const void* p, size_t bytes, bool output) {
+      const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+      if (p && bytes) r[k++] = {b, b + bytes, output};
+    };
+    const auto width = [&](int dtype) { return (size_t)t.n * (dtype == MOE_DT_BF16 ? 2 : 4); };
+    add(t.grad, width(t.grad_dtype), false);
+    if (!t.param) continue;
+    const size_t scales = (size_t)((t.n + kAdamwBlock - 1) / kAdamwBlock) * 4;
+    const size_t state = (size_t)t.n * (t.state_bits / 8);
+    add(t.param, width(t.param_dtype), true);
+    add(t.master, (size_t)t.n * 4, true);
+    add(t.m, state, true);
+    add(t.v, state, true);
+    if (t.state_bits == 8) {
+      add(t.m_scale, scales, true);
+      add(t.v_scale, scales, true);
+    }
+  }
+  std::sort(r, r + k, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t end_all = 0, end_out = 0;           // furthest end of the buffers before, of the outputs before
+  bool bad = false;
+  for (size_t i = 0; i < k; ++i) {
+    bad = bad || r[i].begin < end_out || (r[i].output && r[i].begin < end_all);
+    end_all = std::max(end_all, r[i].end);
+    if (r[i].output) end_out = std::max(end_out, r[i].end);
+  }
+  delete[] r;
+  return bad ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+moe_status_t moe_adamw_plan(const moe_adamw_tensor_t* tensors, int n_tensors, void* table, size_t table_bytes,
+                            moe_adamw_plan_t* plan) {
+  if (n_tensors < 0 || n_tensors > (1 << 24)) return MOE_ERR_SHAPE;
+  if (!plan || (n_tensors > 0 && (!tensors || !table))) return MOE_ERR_NULL;
+  if (n_tensors > 0 && (reinterpret_cast<uintptr_t>(table) & 7) != 0) return MOE_ERR_ALIGN;
+  for (int i = 0; i < n_tensors; ++i) {
+    const moe_status_t st = check_adamw_tensor(tensors[i]);
+    if (st != MOE_OK) return st;
+  }
+  if (table_bytes < moe_adamw_plan_bytes(tensors, n_tensors)) return MOE_ERR_SHAPE;
+  if (n_tensors > 0) {
+    const moe_status_t st = adamw_overlap(tensors, n_tensors);
+    if (st != MOE_OK) return st;
+  }
+  AdamwTensor* out = static_cast<AdamwTensor*>(table);
+  AdamwChunk* chunk = reinterpret_cast<AdamwChunk*>(out + n_tensors);
+  long long total = 0;
+  for (int i = 0; i < n_tensors; ++i) {
+    const moe_adamw_tensor_t& t = tensors[i];
+    memset(&out[i], 0, sizeof(out[i]));
+    out[i].param = t.param;
+    out[i].grad = t.grad;
+    out[i].master = t.master;
+    out[i].m = t.m;
+    out[i].v = t.v;
+    out[i].m_scale = t.m_scale;
+    out[i].v_scale = t.v_scale;
+    out[i].n = t.n;
+    out[i].lr_scale = t.lr_scale;
+    out[i].decay = t.weight_decay;
+    out[i].param_bf16 = t.param_dtype == MOE_DT_BF16;
+    out[i].grad_bf16 = t.grad_dtype == MOE_DT_BF16;
+    out[i].state8 = t.state_bits == 8;
+    const long long n = adamw_chunks(t);
+    for (long long c = 0; c < n; ++c) chunk[total++] = {i, (int)c};
+  }
+  plan->table = nullptr;
+  plan->n_tensors = n_tensors;
+  plan->n_chunks = total;
+  return MOE_OK;
+}
+
+static moe_status_t check_plan(const moe_adamw_plan_t* plan) {
+  if (!plan) return MOE_ERR_NULL;
+  if (plan->n_tensors < 0 || plan->n_chunks < 0) return MOE_ERR_SHAPE;
+  if (plan->n_chunks > 0 && !plan->table) return MOE_ERR_NULL;
+  if (!aligned16(plan->table)) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+moe_status_t moe_adamw_step(const moe_adamw_plan_t* plan, const moe_adamw_t* h, void* stream) {
+  moe_status_t st = check_plan(plan);
+  if (st != MOE_OK) return st;
+  if (!h) return MOE_ERR_NULL;
+  if (!(h->beta1 >= 0.0 && h->beta1 < 1.0) || !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(h->eps >= 0.0) ||
+      !isfinite(h->eps) || !isfinite(h->lr) || (!h->step_dev && h->step < 1))
+    return MOE_ERR_SHAPE;
+  if (!aligned4(h->step_dev) || !aligned4(h->lr_dev) || !aligned4(h->grad_scale)) return MOE_ERR_ALIGN;
+  int cus;
+  if ((st = ensure_init(&cus)) != MOE_OK) return st;
+  AdamwArgs a;
+  a.tensors = static_cast<const AdamwTensor*>(plan->table);
+  a.chunks = reinterpret_cast<const AdamwChunk*>(a.tensors + plan->n_tensors);
+  a.n_chunks = plan->n_chunks;
+  a.lr = h->lr;
+  a.beta1 = h->beta1;
+  a.beta2 = h->beta2;
+  a.eps = h->eps;
+  a.bias1 = h->step_dev ? 1.0 : 1.0 - pow(h->beta1, (double)h->step);
+  a.bias2 = h->step_dev ? 1.0 : 1.0 - pow(h->beta2, (double)h->step);
+  a.step = h->step_dev;
+  a.lr_dev = h->lr_dev;
+  a.grad_scale = h->grad_scale;
+  return launch_adamw(a, cus, (hipStream_t)stream);
+}
+
+moe_status_t moe_adamw_unpack(const int8_t* m, const float* m_scale, const uint8_t* v, const float* v_scale,
+                              int64_t n, float* m_out, float* v_out, void* stream) {
+  if (n < 0 || n > (1LL << 42)) return MOE_ERR_SHAPE;
+  if (n > 0 && ((!m_out && !v_out) || (m_out && (!m || !m_scale)) || (v_out && (!v || !v_scale)))) return MOE_ERR_NULL;
+  if (!aligned16(m) || !aligned16(v) || !aligned16(m_out) || !aligned16(v_out) || !aligned4(m_scale) ||
+      !aligned4(v_scale))
+    return MOE_ERR_ALIGN;
+  const size_t scales = (size_t)((n + kAdamwBlock - 1) / kAdamwBlock) * 4;
+  if (overlap({{m_out, (size_t)n * 4}, {v_out, (size_t)n * 4}},
+              {{m, (size_t)n}, {v, (size_t)n}, {m_scale, scales}, {v_scale, scales}}))
+    return MOE_ERR_UNSUPPORTED;
+  int cus;
+  const moe_status_t st = ensure_init(&cus);
+  if (st != MOE_OK) return st;
+  return launch_adamw_unpack(m, m_scale, v, v_scale, n, m_out, v_out, (hipStream_t)stream);
+}
+
+size_t moe_grad_norm_workspace_bytes(void) { return kNormParts * sizeof(double); }
+
+moe_status_t moe_grad_norm(const moe_adamw_plan_t* plan, float max_norm, float* out, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  moe_status_t st = check_plan(plan);
+  if (st != MOE_OK) return st;
+  if (!out || !workspace) return MOE_ERR_NULL;
+  if (workspace_bytes < moe_grad_norm_workspace_bytes() || !(max_norm > 0.0f)) return MOE_ERR_SHAPE;
+  if (!aligned4(out) || !aligned16(workspace)) return MOE_ERR_ALIGN;
+  if (overlap({{out, 8}, {workspace, moe_grad_norm_workspace_bytes()}}, {})) return MOE_ERR_UNSUPPORTED;
+  int cus;
+  if ((st = ensure_init(&cus)) != MOE_OK) return st;
+  const AdamwTensor* t = static_cast<const AdamwTensor*>(plan->table);
+  return launch_grad_norm(t, reinterpret_cast<const AdamwChunk*>(t + plan->n_tensors), plan->n_chunks, max_norm, out,
+                          static_cast<double*>(workspace), (hipStream_t)stream);
 }
 
 }  // extern "C"

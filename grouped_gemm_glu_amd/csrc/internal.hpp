@@ -65,6 +65,26 @@ constexpr int kNormBwdParts = 512;
 int norm_bwd_parts(int T);
 moe_status_t launch_add_rmsnorm_bwd(const NormBwdArgs& a, float* dweight, int accumulate, hipStream_t s);
 
+// Low-rank adapters (lora.hip).  The sizes of a call, from which its launches and
+// its workspace follow; the same for every device.
+struct LoraShape {
+  int M_cap, L, r, K, N;
+};
+size_t lora_fwd_workspace(const LoraShape& s);
+size_t lora_bwd_workspace(const LoraShape& s);
+moe_status_t launch_lora_fwd(const LoraArgs& a, const uint16_t* x, const uint16_t* base, uint16_t* y, float* u,
+                             void* ws, hipStream_t s);
+moe_status_t launch_lora_bwd(const LoraArgs& a, const uint16_t* dy, const uint16_t* x, const float* u,
+                             const uint16_t* dx_base, uint16_t* dx, float* dA, float* dB, int accumulate, void* ws,
+                             hipStream_t s);
+
+// AdamW and the gradients' norm (adamw.hip)
+moe_status_t launch_adamw(const AdamwArgs& a, int cus, hipStream_t s);
+moe_status_t launch_adamw_unpack(const int8_t* m, const float* m_scale, const uint8_t* v, const float* v_scale,
+                                 long long n, float* m_out, float* v_out, hipStream_t s);
+moe_status_t launch_grad_norm(const AdamwTensor* tensors, const AdamwChunk* chunks, long long n_chunks, float max_norm,
+                              float* out, double* part, hipStream_t s);
+
 // MXFP4 (mxfp4.hip); a4: e2m1 rows, else e4m3
 moe_status_t launch_mx4_rows(const uint16_t* v, int R, int C, const int* counts, int E, uint8_t* q,
                              uint8_t* s, int cus, hipStream_t st);

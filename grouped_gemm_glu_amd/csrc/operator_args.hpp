@@ -1,5 +1,5 @@
-// Arguments of the router, norm and MXFP4 kernels, shared by the entry points
-// and the launchers.
+// Arguments of the router, norm, MXFP4, adapter and optimizer kernels, shared by
+// the entry points and the launchers.
 #pragma once
 
 #include <stdint.h>
@@ -13,6 +13,9 @@ constexpr int kNormMaxH = 16384;
 constexpr int kMaxCombineH = 1 << 26;       // 2048 columns per row of the grid
 constexpr int kMaxMx4K = 1 << 24;           // a tile's 256 rows of codes, and of outputs, within a
 constexpr int kMaxMx4N = 1 << 23;           // descriptor's 2^32 bytes
+constexpr int kMaxLoraRank = 128;
+constexpr int kMaxLoraRows = 1 << 25;       // a launch of 256 threads per 16 rows stays below 2^32
+constexpr int kMaxLoraCols = 1 << 17;       // 1024 of r times as many per row of the grid
 
 struct RouterArgs {
   const void* logits;       // fp32 or bf16 [T][E]
@@ -62,6 +65,57 @@ struct Mx4Args {
   int* offsets_out;
   int* status_out;
   uint16_t* C;              // [M_cap][N]
+};
+
+// Rows of adapters: group e's are grouped rows o_e .. o_e + counts[e].
+struct LoraGroups {
+  const int* counts;        // [L]
+  int L, M_cap;
+  int* offsets_out;
+  int* status_out;
+  const int* src;           // [M_cap]: grouped row -> row of x and y, or null: the same
+  int T;                    // rows of x and y
+};
+
+struct LoraArgs {
+  LoraGroups g;
+  const uint16_t* A;        // [L][r][K]
+  const uint16_t* B;        // [L][N][r]
+  const float* scale;       // [L] or null
+  int r, K, N;
+  long long x_ld, y_ld;
+};
+
+// One tensor of an AdamW step, as the device's table holds it.
+struct AdamwTensor {
+  void* param;              // null: the tensor takes part in the norm alone
+  const void* grad;
+  float* master;            // null: the parameter is its own
+  void* m;
+  void* v;
+  float* m_scale;           // 8-bit states: one of each per kAdamwBlock elements
+  float* v_scale;
+  long long n;
+  float lr_scale, decay;
+  int param_bf16, grad_bf16, state8, pad;
+};
+// A piece of a tensor: elements kAdamwChunk index .. of it.
+struct AdamwChunk {
+  int tensor, index;
+};
+constexpr int kAdamwBlock = 128;
+constexpr int kAdamwChunk = 4096;
+constexpr int kNormParts = 1024;            // workgroups, at most, of the gradients' norm
+
+struct AdamwArgs {
+  const AdamwTensor* tensors;
+  const AdamwChunk* chunks;
+  long long n_chunks;
+  double lr, beta1, beta2, eps;
+  double bias1, bias2;      // 1 - beta^step, where the step is not the device's
+  const int* step;          // device, or null
+  const float* lr_dev;      // device, or null
+  const float* grad_scale;  // device, or null
 };
 
 }  // namespace moe

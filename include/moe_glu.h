@@ -571,6 +571,140 @@ moe_status_t moe_mxfp4_quantize(const void* v, int R, int C, const moe_groups_t*
 moe_status_t moe_pack_weight_mxfp4(const void* src, int E, int N, int K, int src_layout, void* dst_q,
                                    void* dst_s, void* stream);
 
+/* Low-rank adapters of many requests beside a shared projection: for the rows
+ * of group e (moe_groups_t: counts [E], one group per adapter, or per expert)
+ *   u_i = A_e x_i                         fp32, the narrow product
+ *   y_i = bf16(base_i + scale_e B_e u_i)
+ * A bf16 [E][r][K] and B bf16 [E][N][r] as such adapters are stored, scale fp32
+ * [E] (alpha / r; NULL: 1).  Adapters of a smaller rank are padded with zeros.
+ * x_ld, y_ld: elements from one row of x (and dx) and of y (base, dy) to the
+ * next, 0 = K and N; more than that for columns of a wider matrix.  Requires r
+ * % 8 == 0, 8 <= r <= 128, K and N % 8 == 0, 8 <= K, N <= 2^17, x_ld >= K and
+ * y_ld >= N multiples of 8.  (host struct) */
+typedef struct {
+  const void* A;
+  const void* B;
+  const float* scale;       /* nullable */
+  int32_t r, K, N;
+  int64_t x_ld, y_ld;
+} moe_lora_t;
+
+/* The adapters' products onto the shared projection's output.  x: bf16 [T][K],
+ * base, y: bf16 [T][N] (base NULL: 0; y may be base itself).  src int32 [M_cap]
+ * names the row of x and y that a grouped row is, as moe_route_group's src does
+ * (adapter ids as topk_ids, k = 1; one grouping serves every projection of a
+ * step), NULL: the grouped row itself; no row stands in it twice.  Rows that no
+ * group holds, and grouped rows whose src lies outside [0, T), are left as they
+ * were.  u: fp32 [M_cap][r] or NULL, kept for the backward pass (0 in rows whose
+ * src lies outside).  All sums are fp32; the product with B takes u to 2^-17 of
+ * its value.  workspace: moe_lora_fwd_workspace_bytes(M_cap, E, r, K, N) bytes,
+ * 16-byte aligned, contents of no meaning before or after; calls that may run at
+ * the same time, replays of captured ones too, need one each.  Requires M_cap <=
+ * 2^25; x, A, B, base, y, u 16-byte, src and scale 4-byte aligned.  T = 0 does
+ * nothing but report the groups. */
+size_t moe_lora_fwd_workspace_bytes(int M_cap, int E, int r, int K, int N);
+moe_status_t moe_lora_fwd(const void* x, int T, const int32_t* src, const moe_groups_t* groups,
+                          const moe_lora_t* lora, const void* base, void* y, float* u, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Its gradients from dy (bf16 [T][N]) and the saved u, with w_i = B_e^T dy_i:
+ *   dx_i = bf16(dx_base_i + scale_e A_e^T w_i)      bf16 [T][K], nullable; dx may
+ *                                                   be dx_base itself (NULL: 0)
+ *   dA_e = scale_e sum_i w_i x_i^T                  fp32 [E][r][K], nullable
+ *   dB_e = scale_e sum_i dy_i u_i^T                 fp32 [E][N][r], nullable
+ * dy has y's row distance, dx and dx_base x's.  accumulate = 1 adds to dA and
+ * dB; 0 writes them (0 for a group without rows; T = 0 too).  x is needed for dA
+ * only, u for dB only.  Sums are fp32, in a fixed order.  The workspace (of
+ * moe_lora_bwd_workspace_bytes) and the rest as above; rows of dx that no group
+ * holds are left as they were. */
+size_t moe_lora_bwd_workspace_bytes(int M_cap, int E, int r, int K, int N);
+moe_status_t moe_lora_bwd(const void* dy, const void* x, int T, const int32_t* src, const moe_groups_t* groups,
+                          const moe_lora_t* lora, const float* u, const void* dx_base, void* dx, float* dA,
+                          float* dB, int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* A tensor of an AdamW step: n elements of a parameter, its gradient (e.g. the
+ * fp32 dW of moe_group_gemm_wgrad) and its states.
+ *   param   fp32 or bf16 (param_dtype MOE_DT_FP32 or MOE_DT_BF16); NULL: the
+ *           tensor takes part in moe_grad_norm alone
+ *   grad    fp32 or bf16 (grad_dtype)
+ *   master  fp32 [n], the value that a bf16 parameter is the rounding of; NULL:
+ *           the parameter's own value is updated and rounded (to nearest even,
+ *           so that updates below half its step are lost)
+ *   m, v    state_bits 32: fp32 [n].  state_bits 8: m int8 [n], v uint8 [n] and
+ *           per 128 elements m_scale and v_scale fp32 [ceil(n/128)]:
+ *             m = sign(c) (c / 127)^2 m_scale,  sqrt(v) = (c / 255)^2 v_scale
+ *           m_scale the block's largest |m|, v_scale its largest sqrt(v).  All
+ *           zeros is the state before the first step.
+ * param, grad, master, m and v 16-byte, the scales 4-byte aligned.  (host
+ * struct) */
+typedef struct {
+  void* param;
+  const void* grad;
+  float* master;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;                /* 0 <= n <= 2^42 */
+  float lr_scale;           /* multiplies the step's learning rate */
+  float weight_decay;
+  int32_t param_dtype;
+  int32_t grad_dtype;
+  int32_t state_bits;
+} moe_adamw_tensor_t;
+
+/* The tensors of a step, laid out once: moe_adamw_plan fills `table` (host
+ * memory of moe_adamw_plan_bytes(tensors, n_tensors) bytes, 8-byte aligned) and
+ * plan's sizes; the caller copies the table to device memory (16-byte aligned)
+ * and sets plan->table.  The plan holds as long as the tensors' addresses do;
+ * their contents may change.  An output of a tensor (param, master, m, v,
+ * scales) that shares bytes with any other buffer of the plan is
+ * MOE_ERR_UNSUPPORTED.  (host struct) */
+typedef struct {
+  const void* table;        /* device */
+  int32_t n_tensors;
+  int64_t n_chunks;
+} moe_adamw_plan_t;
+size_t moe_adamw_plan_bytes(const moe_adamw_tensor_t* tensors, int n_tensors);
+moe_status_t moe_adamw_plan(const moe_adamw_tensor_t* tensors, int n_tensors, void* table, size_t table_bytes,
+                            moe_adamw_plan_t* plan);
+
+/* The step's numbers.  (host struct) */
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int64_t step;             /* number of this step, from 1; ignored with step_dev */
+  const int32_t* step_dev;  /* nullable device int32 (below 1 counts as 1): for captured steps */
+  const float* lr_dev;      /* nullable device fp32, in the place of lr */
+  const float* grad_scale;  /* nullable device fp32 that multiplies every gradient (moe_grad_norm's
+                               factor); where it is NaN the call changes nothing */
+} moe_adamw_t;
+
+/* One AdamW step over every tensor of the plan, in one launch.  With g = grad *
+ * grad_scale, a = lr * lr_scale and t the step:
+ *   m' = beta1 m + (1 - beta1) g,   v' = beta2 v + (1 - beta2) g^2
+ *   p' = p (1 - a weight_decay) - a (m' / (1 - beta1^t)) / (sqrt(v' / (1 - beta2^t)) + eps)
+ * in fp32.  8-bit states: m' and v' are formed in 64 bits, p' takes them before
+ * they are rounded to codes, and the code is the nearest under the square root
+ * (the lower of two as near; at least 1 for v' > 0), scales rounded to fp32.  A
+ * block in which m' or v' is not finite gets scales NaN and codes 0.  Requires
+ * 0 <= beta < 1, eps >= 0, all finite. */
+moe_status_t moe_adamw_step(const moe_adamw_plan_t* plan, const moe_adamw_t* hyper, void* stream);
+
+/* 8-bit states read out as fp32 (to save, inspect or widen them): m_out, v_out
+ * [n], each nullable with its codes; 16-byte aligned codes and outputs. */
+moe_status_t moe_adamw_unpack(const int8_t* m, const float* m_scale, const uint8_t* v, const float* v_scale,
+                              int64_t n, float* m_out, float* v_out, void* stream);
+
+/* The norm of all gradients of a plan, and the factor that clips them:
+ *   out[0] = sqrt(sum of squares),  out[1] = min(1, max_norm / (out[0] + 1e-6))
+ * fp32, from sums in 64 bits in a fixed order; out[1] is NaN where out[0] is not
+ * finite, so that a step given it as grad_scale is left out.  max_norm > 0 (inf:
+ * no clipping).  workspace: moe_grad_norm_workspace_bytes() bytes, 16-byte
+ * aligned, one per call that may run at the same time; out 4-byte aligned. */
+size_t moe_grad_norm_workspace_bytes(void);
+moe_status_t moe_grad_norm(const moe_adamw_plan_t* plan, float max_norm, float* out, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
