@@ -2,9 +2,9 @@
 // gradients.  Each element's parameter, master, gradient and states are read and
 // written once: the kernels are bound by memory.
 //
-// A table on the device lists the tensors and cuts them into chunks of 4096
-// elements, so that a workgroup finds its elements with two dependent loads
-// however many tensors there are.  A thread takes four consecutive elements of
+// A table on the device lists the tensors and cuts them into chunks of 4096 elements
+// (2048 where there are few), so that a workgroup finds its elements with two
+// dependent loads however many tensors there are.  A thread takes four consecutive elements of
 // each 1024: 16 bytes of fp32, 8 of bf16, 4 of 8-bit codes.
 #pragma once
 
@@ -14,9 +14,9 @@
 namespace moe {
 
 struct AdamwHyper {
-  float beta1, c1, beta2, c2, eps, step_size, root_scale, shrink;   // fp32 forms
-  double beta1d, c1d, beta2d, c2d;
-  float grad_scale;
+  float beta1, c1, beta2, c2, eps, step_size, root_scale, shrink, grad_scale;
+  bool exact_root;             // an eps so small that denormal roots count
+  double beta1d, c1d, beta2d, c2d;   // 64-bit forms; c1d and c2d take the gradient's factor in
 };
 
 template <bool BF16>
@@ -85,16 +85,16 @@ __device__ __forceinline__ void store_codes4(void* p, long long i, int n, uint32
 //   sqrt(v) = (c / 255)^2 v_scale          c uint8, at least 1 for v > 0
 // The square spreads the codes: a step is 1.6% of the block's largest value near
 // it and still 16% at a hundredth of it.  An element's second moment never
-// becomes 0 beside a first that did not.  The nearest code under the square root
-// (the lower of two as near) is found in 32 bits and put right by comparing with
-// its borders in 64, so it is the one that the definition gives.
+// becomes 0 beside a first that did not.  The code is the nearest under the square
+// root (the lower of two as near) as 64 bits decide it: it is found in 32 bits, and
+// only where they come near a border (or their range ends) compared with it in 64.
 __device__ __forceinline__ double m_of_code(int c, double scale) {
   return (double)(c * (c < 0 ? -c : c)) * (1.0 / 16129.0) * scale;
 }
 __device__ __forceinline__ double root_of_code(int c, double scale) { return (double)(c * c) * (1.0 / 65025.0) * scale; }
 
-__device__ __forceinline__ int nearest_m(double a, double scale, float guess) {   // a = |m|
-  int c = (int)rintf(127.0f * sqrtf(guess));
+__device__ __forceinline__ int code_m_exact(double a, double scale) {   // a = |m|, scale > 0
+  int c = (int)rint(127.0 * sqrt(a / scale));
   c = c > 127 ? 127 : c;
   const double t = a * 64516.0;                 // 4 * 127^2
   const int up = 2 * c + 1, down = 2 * c - 1;
@@ -102,118 +102,215 @@ __device__ __forceinline__ int nearest_m(double a, double scale, float guess) { 
   else if (c > 0 && t <= (double)(down * down) * scale) --c;
   return c > 127 ? 127 : c;
 }
-__device__ __forceinline__ int nearest_root(double v, double scale, float guess) {
-  int c = (int)rintf(255.0f * sqrtf(sqrtf(guess)));
+__device__ __forceinline__ int code_root_exact(double v, double scale) {
+  int c = (int)rint(255.0 * sqrt(sqrt(v) / scale));
   c = c > 255 ? 255 : c;
   const double t = v * 67652010000.0, s2 = scale * scale;   // 510^4
   const double up = (double)((2 * c + 1) * (2 * c + 1)), down = (double)((2 * c - 1) * (2 * c - 1));
   if (t > up * up * s2) ++c;
   else if (c > 0 && t <= down * down * s2) --c;
-  c = c > 255 ? 255 : c;
-  return c < 1 && v > 0.0 ? 1 : c;
+  return c > 255 ? 255 : c;
 }
-// over the 32 lanes of a block
+// With u = 2^-24: m, 1 / m_scale (2 u) and their product make the ratio in x = 127
+// sqrt(m / m_scale) right to 4 u, the hardware's root (2 u) and the product x to 5 u;
+// v, its block's largest (1 u each), the reciprocal, the product and v_scale's rounding
+// (2 u) make the ratio in y = 255 sqrt(sqrt(v) / v_scale) right to 7 u, two roots and the
+// product y to 6 u.  Nearer than that to the middle between two codes, 127 * 5 u = 3.8e-5
+// and 255 * 6 u = 9.2e-5, the 64-bit comparison decides.
+__device__ __forceinline__ bool near_border(float x, float near) {
+  return fabsf(fabsf(x - rintf(x)) - 0.5f) < near;
+}
+constexpr float kNearM = 5e-5f, kNearRoot = 1.2e-4f;
+
+// over the 32 lanes of a block: rotations within 16 lanes, then the other 16
+template <int CTRL>
+__device__ __forceinline__ uint32_t rotate(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+__device__ __forceinline__ float half_max(float v) {
+  v = fmaxf(v, __uint_as_float(rotate<0x128>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(rotate<0x124>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(rotate<0x122>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(rotate<0x121>(__float_as_uint(v))));
+  return fmaxf(v, __shfl_xor(v, 16, 64));
+}
+template <int CTRL>
+__device__ __forceinline__ double max_rotated(double v) {
+  const unsigned long long b = __builtin_bit_cast(unsigned long long, v);
+  const unsigned long long o = (unsigned long long)rotate<CTRL>((uint32_t)(b >> 32)) << 32 | rotate<CTRL>((uint32_t)b);
+  return fmax(v, __builtin_bit_cast(double, o));
+}
 __device__ __forceinline__ double half_max(double v) {
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) v = fmax(v, __shfl_xor(v, d, 64));
-  return v;
+  v = max_rotated<0x128>(v);
+  v = max_rotated<0x124>(v);
+  v = max_rotated<0x122>(v);
+  v = max_rotated<0x121>(v);
+  return fmax(v, __shfl_xor(v, 16, 64));
+}
+// fp32 of the square root of a 64-bit value
+__device__ __forceinline__ float root_of(double v) {
+  if (!(v > 1e-30 && v < 1e30)) return (float)sqrt(v);
+  // a 1-ulp root and the middles between it and its neighbours, whose squares have
+  // 50 bits
+  const float s = __builtin_amdgcn_sqrtf((float)v);
+  const float up = __uint_as_float(__float_as_uint(s) + 1), down = __uint_as_float(__float_as_uint(s) - 1);
+  const double mu = 0.5 * ((double)s + (double)up), md = 0.5 * ((double)s + (double)down);
+  return v > mu * mu ? up : v < md * md ? down : s;
 }
 
-// One chunk.  PARAM: 0 fp32, 1 bf16, 2 bf16 with an fp32 master.
-template <int PARAM, bool GRAD16, bool STATE8>
-__device__ __forceinline__ void adamw_chunk(const AdamwTensor& t, long long first, const AdamwHyper& h) {
-  const long long left = t.n - first;
-#pragma unroll
-  for (int s = 0; s < kAdamwChunk / 1024; ++s) {
-    const long long at = 1024LL * s + 4 * threadIdx.x;
-    if (1024LL * s >= left) break;              // the same for the whole workgroup
-    const long long i = first + at;
-    const int n = at >= left ? 0 : left - at < 4 ? (int)(left - at) : 4;
-    float g[4], p[4], m[4], v[4];
-    load4<GRAD16>(t.grad, i, n, g);
-    if constexpr (PARAM == 1) load4<true>(t.param, i, n, p);
-    else load4<false>(PARAM == 2 ? t.master : t.param, i, n, p);
-    if constexpr (!STATE8) {
-      load4<false>(t.m, i, n, m);
-      load4<false>(t.v, i, n, v);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float gk = g[k] * h.grad_scale;
-        m[k] = h.beta1 * m[k] + h.c1 * gk;
-        v[k] = h.beta2 * v[k] + h.c2 * (gk * gk);
-      }
-      store4<false>(t.m, i, n, m);
-      store4<false>(t.v, i, n, v);
-    } else {
-      const long long block = i / kAdamwBlock;
-      const uint32_t cm = load_codes4(t.m, i, n), cv = load_codes4(t.v, i, n);
-      const double ms = n ? t.m_scale[block] : 0.0f, vs = n ? t.v_scale[block] : 0.0f;
-      double md[4], vd[4];
-      double ma = 0.0, va = 0.0;
-      bool bad = false;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const double gk = (double)g[k] * (double)h.grad_scale;
-        const double root = root_of_code((int)(cv >> (8 * k) & 0xFF), vs);
-        md[k] = h.beta1d * m_of_code((int)(int8_t)(cm >> (8 * k)), ms) + h.c1d * gk;
-        vd[k] = h.beta2d * (root * root) + h.c2d * (gk * gk);
-        if (k >= n) md[k] = vd[k] = 0.0;
-        m[k] = (float)md[k];
-        v[k] = (float)vd[k];
-        ma = fmax(ma, fabs(md[k]));
-        va = fmax(va, vd[k]);
-        bad = bad || !(fabsf(m[k]) < INFINITY) || !(vd[k] < (double)INFINITY);
-      }
-      ma = half_max(ma);
-      va = half_max(va);
-      const float root_max = (float)sqrt(va);
-      const unsigned long long any = __ballot(bad || !(root_max < INFINITY));
-      const bool lost = (threadIdx.x & 32 ? any >> 32 : any & 0xFFFFFFFFull) != 0;
-      // a NaN or an infinity leaves no codes: the block's states are NaN from here
-      const float m_scale = lost ? __uint_as_float(0x7FC00000u) : (float)ma;
-      const float v_scale = lost ? __uint_as_float(0x7FC00000u) : root_max;
-      const double im = m_scale > 0.0f ? 1.0 / (double)m_scale : 0.0, iv = v_scale > 0.0f ? 1.0 / va : 0.0;
-      uint32_t om = 0, ov = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        int c = m_scale > 0.0f ? nearest_m(fabs(md[k]), (double)m_scale, (float)(fabs(md[k]) * im)) : 0;
-        c = md[k] < 0.0 ? -c : c;
-        const int d = v_scale > 0.0f ? nearest_root(vd[k], (double)v_scale, (float)(vd[k] * iv)) : 0;
-        om |= (uint32_t)(c & 0xFF) << (8 * k);
-        ov |= (uint32_t)d << (8 * k);
-      }
-      store_codes4(t.m, i, n, om);
-      store_codes4(t.v, i, n, ov);
-      if ((threadIdx.x & 31) == 0 && n) {
-        t.m_scale[block] = m_scale;
-        t.v_scale[block] = v_scale;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float update = m[k] * h.step_size / (sqrtf(v[k] * h.root_scale) + h.eps);
-      p[k] = p[k] * h.shrink - update;
-    }
-    if constexpr (PARAM == 2) store4<false>(t.master, i, n, p);
-    if constexpr (PARAM == 0) store4<false>(t.param, i, n, p);
-    else store4<true>(t.param, i, n, p);
+// Four elements of a thread, as memory holds them.  PARAM: 0 fp32, 1 bf16, 2 bf16
+// with an fp32 master.
+template <bool STATE8>
+struct AdamwFour {
+  float g[4], p[4], m[4], v[4];
+};
+template <>
+struct AdamwFour<true> {
+  float g[4], p[4], m_scale, v_scale;
+  uint32_t m, v;
+};
+// elements i .. i + n of the tensor, n <= 4 (WHOLE: n = 4, with nothing skipped, so
+// that the compiler can count the loads on their way)
+template <int PARAM, bool GRAD16, bool STATE8, bool WHOLE>
+__device__ __forceinline__ void adamw_load(const AdamwTensor& t, long long i, int n, AdamwFour<STATE8>& f) {
+  if constexpr (WHOLE) n = 4;
+  load4<GRAD16>(t.grad, i, n, f.g);
+  if constexpr (PARAM == 1) load4<true>(t.param, i, n, f.p);
+  else load4<false>(PARAM == 2 ? t.master : t.param, i, n, f.p);
+  if constexpr (STATE8) {
+    f.m = load_codes4(t.m, i, n);
+    f.v = load_codes4(t.v, i, n);
+    f.m_scale = n > 0 ? t.m_scale[i / kAdamwBlock] : 0.0f;
+    f.v_scale = n > 0 ? t.v_scale[i / kAdamwBlock] : 0.0f;
+  } else {
+    load4<false>(t.m, i, n, f.m);
+    load4<false>(t.v, i, n, f.v);
   }
 }
-
-template <int PARAM>
-__device__ __forceinline__ void adamw_chunk_of(const AdamwTensor& t, long long first, const AdamwHyper& h) {
-  if (t.state8) {
-    if (t.grad_bf16) adamw_chunk<PARAM, true, true>(t, first, h);
-    else adamw_chunk<PARAM, false, true>(t, first, h);
+template <int PARAM, bool STATE8, bool WHOLE>
+__device__ __forceinline__ void adamw_update(const AdamwTensor& t, long long i, int n, const AdamwHyper& h,
+                                             const AdamwFour<STATE8>& f) {
+  if constexpr (WHOLE) n = 4;
+  float m[4], v[4], p[4];
+  if constexpr (!STATE8) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float gk = f.g[k] * h.grad_scale;
+      m[k] = h.beta1 * f.m[k] + h.c1 * gk;
+      v[k] = h.beta2 * f.v[k] + h.c2 * (gk * gk);
+    }
+    store4<false>(t.m, i, n, m);
+    store4<false>(t.v, i, n, v);
   } else {
-    if (t.grad_bf16) adamw_chunk<PARAM, true, false>(t, first, h);
-    else adamw_chunk<PARAM, false, false>(t, first, h);
+    const double ms = f.m_scale, vs = f.v_scale;
+    const double km = h.beta1d * (1.0 / 16129.0) * ms, kv = h.beta2d * (1.0 / (65025.0 * 65025.0)) * vs * vs;
+    double md[4], vd[4];
+    float ma = 0.0f;
+    double va = 0.0;
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = (int)(int8_t)(f.m >> (8 * k)), d = (int)(f.v >> (8 * k) & 0xFF);
+      const double gk = (double)f.g[k], d2 = (double)(d * d);
+      md[k] = (double)(c * (c < 0 ? -c : c)) * km + gk * h.c1d;
+      vd[k] = d2 * d2 * kv + gk * gk * h.c2d;
+      if (!WHOLE && k >= n) md[k] = vd[k] = 0.0;
+      m[k] = (float)md[k];
+      v[k] = (float)vd[k];
+      ma = fmaxf(ma, fabsf(m[k]));
+      va = fmax(va, vd[k]);
+    }
+    // sums of sizes, which a NaN or an infinity (or values near fp32's end) leave
+    if (!((fabsf(m[0]) + fabsf(m[1])) + (fabsf(m[2]) + fabsf(m[3])) < INFINITY) ||
+        !((vd[0] + vd[1]) + (vd[2] + vd[3]) < (double)INFINITY))
+#pragma unroll
+      for (int k = 0; k < 4; ++k) bad = bad || !(fabsf(m[k]) < INFINITY) || !(vd[k] < (double)INFINITY);
+    ma = half_max(ma);
+    va = half_max(va);
+    const float root_max = root_of(va);
+    const unsigned long long any = __ballot(bad || !(root_max < INFINITY));
+    const bool lost = (threadIdx.x & 32 ? any >> 32 : any & 0xFFFFFFFFull) != 0;
+    // a NaN or an infinity leaves no codes: the block's states are NaN from here
+    const float m_scale = lost ? __uint_as_float(0x7FC00000u) : ma;
+    const float v_scale = lost ? __uint_as_float(0x7FC00000u) : root_max;
+    // outside of these the ratios below leave the normal numbers of 32 bits
+    const bool m_in = ma > 1e-25f && ma < 1e30f, v_in = va > 1e-25 && va < 1e30;
+    const float im = __builtin_amdgcn_rcpf(ma), iv = __builtin_amdgcn_rcpf((float)va);
+    int om[4], ov[4];
+    bool unsure = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x = 127.0f * __builtin_amdgcn_sqrtf(fabsf(m[k]) * im);
+      const float y = 255.0f * __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(v[k] * iv));
+      unsure = unsure || near_border(x, kNearM) || near_border(y, kNearRoot);
+      om[k] = (int)fminf(rintf(x), 127.0f);
+      ov[k] = (int)fminf(rintf(y), 255.0f);
+    }
+    if (unsure || !m_in || !v_in) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        om[k] = m_scale > 0.0f ? code_m_exact(fabs(md[k]), (double)m_scale) : 0;
+        ov[k] = v_scale > 0.0f ? code_root_exact(vd[k], (double)v_scale) : 0;
+      }
+    }
+    uint32_t wm = 0, wv = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = lost ? 0 : md[k] < 0.0 ? -om[k] : om[k];
+      const int d = lost || !(v_scale > 0.0f) ? 0 : vd[k] > 0.0 ? max(ov[k], 1) : 0;
+      wm |= (uint32_t)(c & 0xFF) << (8 * k);
+      wv |= (uint32_t)d << (8 * k);
+    }
+    store_codes4(t.m, i, n, wm);
+    store_codes4(t.v, i, n, wv);
+    if ((threadIdx.x & 31) == 0 && n > 0) {
+      t.m_scale[i / kAdamwBlock] = m_scale;
+      t.v_scale[i / kAdamwBlock] = v_scale;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float w = v[k] * h.root_scale;
+    // the hardware's root and reciprocal, 1 ulp each; they flush denormals, which
+    // matter beside an eps near 0 alone
+    const float update = h.exact_root ? m[k] * h.step_size / (sqrtf(w) + h.eps)
+                                      : m[k] * h.step_size * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(w) + h.eps);
+    p[k] = f.p[k] * h.shrink - update;
+  }
+  if constexpr (PARAM == 2) store4<false>(t.master, i, n, p);
+  if constexpr (PARAM == 0) store4<false>(t.param, i, n, p);
+  else store4<true>(t.param, i, n, p);
+}
+
+// One chunk: its whole steps two at a time, their loads together, then what is left.
+template <int PARAM, bool GRAD16, bool STATE8>
+__device__ __forceinline__ void adamw_chunk(const AdamwTensor& t, long long first, int chunk, const AdamwHyper& h) {
+  constexpr int STEPS = 2;
+  const long long left = min(t.n - first, (long long)chunk);
+  const int whole = (int)left / kAdamwStep;
+  const long long i = first + 4 * threadIdx.x;
+  int s = 0;
+  for (; s + STEPS <= whole; s += STEPS) {
+    AdamwFour<STATE8> f[STEPS];
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) adamw_load<PARAM, GRAD16, STATE8, true>(t, i + kAdamwStep * (s + k), 4, f[k]);
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) adamw_update<PARAM, STATE8, true>(t, i + kAdamwStep * (s + k), 4, h, f[k]);
+  }
+  for (; kAdamwStep * s < left; ++s) {
+    const long long at = (long long)kAdamwStep * s + 4 * threadIdx.x;
+    const int n = at >= left ? 0 : left - at < 4 ? (int)(left - at) : 4;
+    AdamwFour<STATE8> f;
+    adamw_load<PARAM, GRAD16, STATE8, false>(t, first + at, n, f);
+    adamw_update<PARAM, STATE8, false>(t, first + at, n, h, f);
   }
 }
 
 // m' = b1 m + (1 - b1) g, v' = b2 v + (1 - b2) g^2, p' = p (1 - lr decay) - lr
-// (m' / (1 - b1^t)) / (sqrt(v' / (1 - b2^t)) + eps).
-__global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
+// (m' / (1 - b1^t)) / (sqrt(v' / (1 - b2^t)) + eps).  The chunks of 32-bit and of
+// 8-bit states lie apart, each with a kernel of its own.
+template <bool STATE8>
+__global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a, long long first_chunk, long long end_chunk) {
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
   if (gs != gs) return;                        // gradients without a norm: no step
   const double lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
@@ -225,26 +322,34 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
   }
   AdamwHyper h;
   h.beta1d = a.beta1;
-  h.c1d = 1.0 - a.beta1;
+  h.c1d = (1.0 - a.beta1) * (double)gs;
   h.beta2d = a.beta2;
-  h.c2d = 1.0 - a.beta2;
-  h.beta1 = (float)h.beta1d;
-  h.c1 = (float)h.c1d;
-  h.beta2 = (float)h.beta2d;
-  h.c2 = (float)h.c2d;
+  h.c2d = (1.0 - a.beta2) * (double)gs * (double)gs;
+  h.beta1 = (float)a.beta1;
+  h.c1 = (float)(1.0 - a.beta1);
+  h.beta2 = (float)a.beta2;
+  h.c2 = (float)(1.0 - a.beta2);
   h.eps = (float)a.eps;
+  h.exact_root = a.eps < 1e-15;
   h.root_scale = (float)(1.0 / bias2);
   h.grad_scale = gs;
-  for (long long c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
-    const AdamwChunk ch = a.chunks[c];
+  AdamwChunk ch = a.chunks[first_chunk + blockIdx.x];   // (a workgroup has one chunk at least)
+  for (long long c = first_chunk + blockIdx.x; c < end_chunk; c += gridDim.x) {
     const AdamwTensor t = a.tensors[ch.tensor];
+    const long long first = (long long)ch.index * a.chunk;
+    if (c + gridDim.x < end_chunk) ch = a.chunks[c + gridDim.x];
     if (!t.param) continue;
     h.step_size = (float)(lr * (double)t.lr_scale / bias1);
     h.shrink = (float)(1.0 - lr * (double)t.lr_scale * (double)t.decay);
-    const long long first = (long long)ch.index * kAdamwChunk;
-    if (t.master) adamw_chunk_of<2>(t, first, h);
-    else if (t.param_bf16) adamw_chunk_of<1>(t, first, h);
-    else adamw_chunk_of<0>(t, first, h);
+    if (t.grad_bf16) {
+      if (t.master) adamw_chunk<2, true, STATE8>(t, first, a.chunk, h);
+      else if (t.param_bf16) adamw_chunk<1, true, STATE8>(t, first, a.chunk, h);
+      else adamw_chunk<0, true, STATE8>(t, first, a.chunk, h);
+    } else {
+      if (t.master) adamw_chunk<2, false, STATE8>(t, first, a.chunk, h);
+      else if (t.param_bf16) adamw_chunk<1, false, STATE8>(t, first, a.chunk, h);
+      else adamw_chunk<0, false, STATE8>(t, first, a.chunk, h);
+    }
   }
 }
 
@@ -289,11 +394,11 @@ __device__ __forceinline__ double block_sum(double v, double* tmp) {   // tmp: 4
   return tmp[0] + tmp[1] + tmp[2] + tmp[3];
 }
 template <bool BF16>
-__device__ __forceinline__ void add_squares(const AdamwTensor& t, long long first, double* sum) {
-  const long long left = t.n - first;
-#pragma unroll
-  for (int s = 0; s < kAdamwChunk / 1024; ++s) {
-    const long long at = 1024LL * s + 4 * threadIdx.x;
+__device__ __forceinline__ void add_squares(const AdamwTensor& t, long long first, int chunk, double* sum) {
+  const long long left = min(t.n - first, (long long)chunk);
+#pragma unroll 4
+  for (int s = 0; s * kAdamwStep < chunk; ++s) {
+    const long long at = (long long)kAdamwStep * s + 4 * threadIdx.x;
     const int n = at >= left ? 0 : left - at < 4 ? (int)(left - at) : 4;
     float g[4];
     load4<BF16>(t.grad, first + at, n, g);
@@ -302,16 +407,16 @@ __device__ __forceinline__ void add_squares(const AdamwTensor& t, long long firs
   }
 }
 __global__ __launch_bounds__(256) void grad_norm_kernel(const AdamwTensor* __restrict__ tensors,
-                                                        const AdamwChunk* __restrict__ chunks, long long n_chunks,
+                                                        const AdamwChunk* __restrict__ chunks, int chunk, long long n_chunks,
                                                         double* __restrict__ part) {
   __shared__ double tmp[4];
   double sum[4] = {};
   for (long long c = blockIdx.x; c < n_chunks; c += gridDim.x) {
     const AdamwChunk ch = chunks[c];
     const AdamwTensor t = tensors[ch.tensor];
-    const long long first = (long long)ch.index * kAdamwChunk;
-    if (t.grad_bf16) add_squares<true>(t, first, sum);
-    else add_squares<false>(t, first, sum);
+    const long long first = (long long)ch.index * chunk;
+    if (t.grad_bf16) add_squares<true>(t, first, chunk, sum);
+    else add_squares<false>(t, first, chunk, sum);
   }
   const double s = block_sum((sum[0] + sum[1]) + (sum[2] + sum[3]), tmp);
   if (threadIdx.x == 0) part[blockIdx.x] = s;

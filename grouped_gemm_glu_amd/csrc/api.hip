@@ -1006,15 +1006,23 @@ static moe_status_t check_adamw_tensor(const moe_adamw_tensor_t& t) {
     return MOE_ERR_ALIGN;
   return MOE_OK;
 }
-static long long adamw_chunks(const moe_adamw_tensor_t& t) { return (t.n + kAdamwChunk - 1) / kAdamwChunk; }
+// Elements of a chunk: half as many for a plan that would leave compute units without
+// one (1.1M elements, 32 bits: 8.5 us with 4096, 7.3 with 2048; 1.6M in 300 tensors, 8
+// bits: 17.1 and 15.0; 531M: 3.10 ms and 3.14).
+static int adamw_chunk(const moe_adamw_tensor_t* tensors, int n_tensors) {
+  long long total = 0;
+  for (int i = 0; i < n_tensors; ++i) total += tensors[i].n;
+  return total < (4 << 20) ? 2 * kAdamwStep : 4 * kAdamwStep;
+}
+static long long adamw_chunks(const moe_adamw_tensor_t& t, int chunk) { return (t.n + chunk - 1) / chunk; }
 
 size_t moe_adamw_plan_bytes(const moe_adamw_tensor_t* tensors, int n_tensors) {
   if (n_tensors <= 0 || !tensors) return 0;
-  size_t chunks = 0;
-  for (int i = 0; i < n_tensors; ++i) {
+  for (int i = 0; i < n_tensors; ++i)
     if (tensors[i].n < 0 || tensors[i].n > (1LL << 42)) return 0;
-    chunks += (size_t)adamw_chunks(tensors[i]);
-  }
+  const int chunk = adamw_chunk(tensors, n_tensors);
+  size_t chunks = 0;
+  for (int i = 0; i < n_tensors; ++i) chunks += (size_t)adamw_chunks(tensors[i], chunk);
   return (size_t)n_tensors * sizeof(AdamwTensor) + chunks * sizeof(AdamwChunk);
 }
 
@@ -1093,18 +1101,29 @@ moe_status_t moe_adamw_plan(const moe_adamw_tensor_t* tensors, int n_tensors, vo
     out[i].param_bf16 = t.param_dtype == MOE_DT_BF16;
     out[i].grad_bf16 = t.grad_dtype == MOE_DT_BF16;
     out[i].state8 = t.state_bits == 8;
-    const long long n = adamw_chunks(t);
-    for (long long c = 0; c < n; ++c) chunk[total++] = {i, (int)c};
   }
+  // first the chunks of 32-bit states (and of gradients alone), then those of 8-bit
+  long long total8 = 0;
+  const int size = adamw_chunk(tensors, n_tensors);
+  for (int bits8 = 0; bits8 < 2; ++bits8)
+    for (int i = 0; i < n_tensors; ++i) {
+      if ((tensors[i].param && tensors[i].state_bits == 8) != (bits8 != 0)) continue;
+      const long long n = adamw_chunks(tensors[i], size);
+      for (long long c = 0; c < n; ++c) chunk[total++] = {i, (int)c};
+      if (bits8) total8 += n;
+    }
   plan->table = nullptr;
   plan->n_tensors = n_tensors;
+  plan->chunk = size;
   plan->n_chunks = total;
+  plan->n_chunks8 = total8;
   return MOE_OK;
 }
 
 static moe_status_t check_plan(const moe_adamw_plan_t* plan) {
   if (!plan) return MOE_ERR_NULL;
-  if (plan->n_tensors < 0 || plan->n_chunks < 0) return MOE_ERR_SHAPE;
+  if (plan->n_tensors < 0 || plan->n_chunks8 < 0 || plan->n_chunks < plan->n_chunks8) return MOE_ERR_SHAPE;
+  if (plan->n_chunks > 0 && (plan->chunk < kAdamwStep || plan->chunk % kAdamwStep != 0)) return MOE_ERR_SHAPE;
   if (plan->n_chunks > 0 && !plan->table) return MOE_ERR_NULL;
   if (!aligned16(plan->table)) return MOE_ERR_ALIGN;
   return MOE_OK;
@@ -1123,7 +1142,9 @@ moe_status_t moe_adamw_step(const moe_adamw_plan_t* plan, const moe_adamw_t* h, 
   AdamwArgs a;
   a.tensors = static_cast<const AdamwTensor*>(plan->table);
   a.chunks = reinterpret_cast<const AdamwChunk*>(a.tensors + plan->n_tensors);
+  a.chunk = plan->chunk;
   a.n_chunks = plan->n_chunks;
+  a.n_chunks8 = plan->n_chunks8;
   a.lr = h->lr;
   a.beta1 = h->beta1;
   a.beta2 = h->beta2;
@@ -1166,7 +1187,8 @@ moe_status_t moe_grad_norm(const moe_adamw_plan_t* plan, float max_norm, float* 
   int cus;
   if ((st = ensure_init(&cus)) != MOE_OK) return st;
   const AdamwTensor* t = static_cast<const AdamwTensor*>(plan->table);
-  return launch_grad_norm(t, reinterpret_cast<const AdamwChunk*>(t + plan->n_tensors), plan->n_chunks, max_norm, out,
+  return launch_grad_norm(t, reinterpret_cast<const AdamwChunk*>(t + plan->n_tensors), plan->chunk, plan->n_chunks, max_norm,
+                          out,
                           static_cast<double*>(workspace), (hipStream_t)stream);
 }
 

@@ -5,8 +5,8 @@
 // again (dx_i = base_i + s_e A_e^T w_i) and two sums over a group's rows
 // (dA_e = s_e sum w_i x_i^T, dB_e = s_e sum dy_i u_i^T).  r is 8 to 128 where the
 // rows are thousands long, so all of them are bound by memory: each row of x,
-// y, dy and dx is read or written once, by MFMA fragments that lanes load and
-// store directly.
+// y, dy and dx is read or written once a kernel, by MFMA fragments that lanes load
+// and store directly.
 //
 // v_mfma_f32_16x16x32_bf16: lane l holds row (or column) l % 16 and the eight k
 // from 8 (l / 16) on of each operand, and of the product column l % 16 and
@@ -49,10 +49,11 @@ struct LoraTile {
 };
 
 // Piece number `tile` when every group is cut into pieces of bm rows, a group
-// without rows into `least` of none.  Each wave finds it for itself, without LDS
-// or barriers: the groups' counts are cut so that they fit M_cap (a negative one
-// is none), lanes hold PER of them each.
-template <int PER>
+// without rows into `least` of none; with MANY the tile-th of the groups that have
+// more than one piece (its first).  Each wave finds it for itself, without LDS or
+// barriers: the groups' counts are cut so that they fit M_cap (a negative one is
+// none), lanes hold PER of them each.
+template <int PER, bool MANY, bool EVEN>
 __device__ __forceinline__ LoraTile find_piece(const LoraGroups& g, int bm, int least, uint32_t tile) {
   const int lane = threadIdx.x & 63;
   const uint32_t cap = (uint32_t)g.M_cap;
@@ -75,7 +76,7 @@ __device__ __forceinline__ LoraTile find_piece(const LoraGroups& g, int bm, int 
     c[i] = min(c[i], cap - run);
     run += c[i];
     const uint32_t n = lane * PER + i < g.L ? max((c[i] + bm - 1) / bm, (uint32_t)least) : 0;
-    pieces += n;
+    pieces += MANY ? n > 1 : n;
     many += n > 1 ? n : 0;
   }
   constexpr uint32_t kNoCap = 0x7FFFFFFF;
@@ -92,16 +93,18 @@ __device__ __forceinline__ LoraTile find_piece(const LoraGroups& g, int bm, int 
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const uint32_t n = lane * PER + i < g.L ? max((c[i] + bm - 1) / bm, (uint32_t)least) : 0;
-    if (!found && tile - before < n) {
+    const uint32_t units = MANY ? n > 1 : n;
+    if (!found && tile - before < units) {
       found = true;
-      index = (int)(tile - before);
+      index = MANY ? 0 : (int)(tile - before);
       e = lane * PER + i;
       n_of = (int)n;
-      start = (int)row + index * bm;
-      rows = min(bm, (int)c[i] - index * bm);
+      const int len = EVEN && n > 0 ? ((int)((c[i] + n - 1) / n) + 31) / 32 * 32 : bm;
+      start = (int)row + index * len;
+      rows = min(len, (int)c[i] - index * len);
       base = (int)slot + index;
     }
-    before += n;
+    before += units;
     slot += n > 1 ? n : 0;
     row += c[i];
   }
@@ -113,8 +116,18 @@ __device__ __forceinline__ LoraTile find_piece(const LoraGroups& g, int bm, int 
   t.slot = of_lane(base, at);
   return t;
 }
-__device__ __forceinline__ LoraTile lora_tile(const LoraGroups& g, int bm, int least, uint32_t tile) {
-  return g.L <= 64 ? find_piece<1>(g, bm, least, tile) : find_piece<kMaxExperts / 64>(g, bm, least, tile);
+__device__ __forceinline__ LoraTile lora_tile(const LoraGroups& g, int bm, uint32_t tile) {
+  return g.L <= 64 ? find_piece<1, false, false>(g, bm, 0, tile)
+                   : find_piece<kMaxExperts / 64, false, false>(g, bm, 0, tile);
+}
+// pieces of at most bm rows (a multiple of 32), equal within a group but for 32 rows
+__device__ __forceinline__ LoraTile lora_piece(const LoraGroups& g, int bm, int least, uint32_t tile) {
+  return g.L <= 64 ? find_piece<1, false, true>(g, bm, least, tile)
+                   : find_piece<kMaxExperts / 64, false, true>(g, bm, least, tile);
+}
+__device__ __forceinline__ LoraTile lora_many(const LoraGroups& g, int bm, uint32_t which) {
+  return g.L <= 64 ? find_piece<1, true, false>(g, bm, 0, which)
+                   : find_piece<kMaxExperts / 64, true, false>(g, bm, 0, which);
 }
 
 // offsets_out and status_out of moe_groups_t, by one wave.
@@ -171,227 +184,469 @@ __device__ __forceinline__ bf16x8 zero8() {
   return __builtin_bit_cast(bf16x8, z);
 }
 
-// ---------------------------------------------------------------- u = x A^T
-// A tile of 16 MB rows and a slice of K per workgroup; its four waves take runs
-// of 128 columns in turn and their sums meet in LDS.  The slices' sums go to
-// out + slice * M_cap * r (one slice: the result itself); the next kernel adds
-// them in that order.  Rows that src does not name get 0.
-template <int RB, int MB>
-__global__ __launch_bounds__(256) void lora_narrow_kernel(LoraGroups g, const uint16_t* __restrict__ x, long long x_ld,
-                                                          const uint16_t* __restrict__ A, int r, int K, int slice,
-                                                          float* __restrict__ out, bool report) {
-  constexpr int BM = 16 * MB, RP = 16 * RB, LD = RP + 4;
-  __shared__ float red[4 * BM * LD];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int row16 = lane & 15, q = lane >> 4;
-  if (report && blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) lora_report(g);
-  const LoraTile t = lora_tile(g, BM, 0, blockIdx.x);
-  if (t.e < 0) return;
-  const uint16_t* xr[MB];
-#pragma unroll
-  for (int m = 0; m < MB; ++m) {
-    const int at = 16 * m + row16;
-    const int row = lora_row(g, t.row + at, at < t.rows);
-    xr[m] = x + (long long)max(row, 0) * x_ld;   // a row that is none: any, its sums are dropped
-  }
-  const uint16_t* ar[RB];
-#pragma unroll
-  for (int b = 0; b < RB; ++b) ar[b] = A + ((long long)t.e * r + min(16 * b + row16, r - 1)) * K;
-  const int k_end = min(K, (int)(blockIdx.y + 1) * slice);
-  f32x4 acc[MB][RB] = {};
-  for (int k0 = blockIdx.y * slice + 128 * wave; k0 < k_end; k0 += 512) {
-    if (k0 + 128 <= k_end) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = k0 + 32 * j + 8 * q;
-        bf16x8 xv[MB], av[RB];
-#pragma unroll
-        for (int m = 0; m < MB; ++m) xv[m] = load8(xr[m] + k);
-#pragma unroll
-        for (int b = 0; b < RB; ++b) av[b] = load8(ar[b] + k);
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-          for (int b = 0; b < RB; ++b)
-            acc[m][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[b], xv[m], acc[m][b], 0, 0, 0);
-      }
-    } else {
-      for (int j = 0; j < 4; ++j) {
-        const int k = k0 + 32 * j + 8 * q;
-        const bool in = k < k_end;               // slices and K are multiples of 8
-        bf16x8 xv[MB], av[RB];
-#pragma unroll
-        for (int m = 0; m < MB; ++m) xv[m] = in ? load8(xr[m] + k) : zero8();
-#pragma unroll
-        for (int b = 0; b < RB; ++b) av[b] = in ? load8(ar[b] + k) : zero8();
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-          for (int b = 0; b < RB; ++b)
-            acc[m][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[b], xv[m], acc[m][b], 0, 0, 0);
-      }
-    }
-  }
-#pragma unroll
-  for (int m = 0; m < MB; ++m)
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-      *reinterpret_cast<f32x4*>(&red[(wave * BM + 16 * m + row16) * LD + 16 * b + 4 * q]) = acc[m][b];
-  __syncthreads();
-  float* o = out + (long long)blockIdx.y * g.M_cap * r;
-  const int quads = r / 4;
-  for (int i = threadIdx.x; i < t.rows * quads; i += 256) {
-    const int row = i / quads, c = 4 * (i - row * quads);
-    f32x4 s = *reinterpret_cast<const f32x4*>(&red[row * LD + c]);
-#pragma unroll
-    for (int w = 1; w < 4; ++w) s += *reinterpret_cast<const f32x4*>(&red[(w * BM + row) * LD + c]);
-    if (lora_row(g, t.row + row, true) < 0) s = f32x4{0, 0, 0, 0};
-    *reinterpret_cast<f32x4*>(o + (long long)(t.row + row) * r + c) = s;
-  }
-}
-
-// ---------------------------------------------------------------- y = base + s u B^T
 // fp32 as a sum of bf16 values: the upper half of its bits (no rounding, so that
-// nothing overflows), then what is left.  Two parts hold a value to 2^-17, far
-// below the bf16 rounding of y; an infinity is its first part alone.
+// nothing overflows), then what is left.  An infinity is its first part alone.
 __device__ __forceinline__ uint32_t upper_half(float v) { return __float_as_uint(v) >> 16; }
 __device__ __forceinline__ float rest_of(float v) {
   const float hi = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
   return v == hi ? 0.0f : v - hi;
 }
 
-// A tile of 16 MB rows and a slice of N per workgroup.  The rows' u (the slices'
-// sums added in order, times s) is staged in LDS as its two bf16 parts, [upper r
-// | rest r | zeros], which is one reduction of KS MFMA steps against the weight
-// row taken twice.  A wave takes 32 columns at a time: the rows of two MFMAs are
-// chosen so that a lane's eight products are eight consecutive columns.
-template <int KS, int MB>
-__global__ __launch_bounds__(256) void lora_wide_kernel(LoraGroups g, const float* __restrict__ u_in, int slices,
-                                                        float* __restrict__ u_out, const uint16_t* __restrict__ B,
-                                                        const float* __restrict__ scale, int r, int N, int slice,
-                                                        const uint16_t* base, uint16_t* y, long long y_ld) {
-  constexpr int BM = 16 * MB, LD = 32 * KS + 8;
-  __shared__ __attribute__((aligned(16))) uint16_t us[BM * LD];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Four consecutive elements of each of four rows of LDS, crosswise: in every 16
+// lanes, lane l gives the address of row l / 4, elements 4 (l % 4) .. + 3, and
+// gets element l of the four rows.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ bf16x8 read_crosswise(const uint16_t* rows0, const uint16_t* rows4) {
+  typedef __attribute__((address_space(3))) s16x4* lds_t;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)rows0);
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)rows4);
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// ---------------------------------------------------------------- u = x W^T
+// A tile of 64 MB rows and a slice of K per workgroup, 128 columns of K at a
+// time, the next step's x and the weights after it in flight.  A wave loads its 16 MB rows as
+// runs of 256 bytes (16 lanes a row) and turns them into fragments through a piece
+// of LDS of its own; the weights come through LDS for all waves (two stages), so
+// that a row block reads them once.  W is [r][K], or with TURNED [K][r] (the
+// backward's w = dy B), whose fragments are read crosswise.  The slices' sums go
+// to out + slice * M_cap * r (one slice: the result itself); the next kernel adds
+// them in that order.  Rows that src does not name get 0.
+template <int RB, int MB, bool TURNED>
+__global__ __launch_bounds__(256, RB <= 4 ? 2 : 1) void lora_narrow_kernel(LoraGroups g, const uint16_t* __restrict__ x, long long x_ld,
+                                                          const uint16_t* __restrict__ W, int r, int K, int slice,
+                                                          float* __restrict__ out) {
+  constexpr int BM = 64 * MB, RP = 16 * RB, KT = 128;
+  constexpr int LD = TURNED ? RP + 8 : KT + 8, STAGE = (TURNED ? KT : RP) * LD;
+  __shared__ __attribute__((aligned(16))) uint16_t ws[2 * STAGE];
+  __shared__ __attribute__((aligned(16))) uint16_t xs[4 * MB * 16 * KT];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int row16 = lane & 15, q = lane >> 4;
-  const LoraTile t = lora_tile(g, BM, 0, blockIdx.x);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) lora_report(g);
+  const LoraTile t = lora_tile(g, BM, blockIdx.x);
   if (t.e < 0) return;
-  const float s = scale ? scale[t.e] : 1.0f;
-  const int quads = r / 4;
-  for (int i = threadIdx.x; i < BM * 8 * KS; i += 256) {   // 4 r of a row, zeros past the two parts
-    const int row = i / (8 * KS), c = i - row * (8 * KS);
-    if (c < quads) {
-      f32x4 v = {0, 0, 0, 0};
-      if (row < t.rows) {
-        const float* p = u_in + (long long)(t.row + row) * r + 4 * c;
-        v = *reinterpret_cast<const f32x4*>(p);
-        for (int k = 1; k < slices; ++k) v += *reinterpret_cast<const f32x4*>(p + (long long)k * g.M_cap * r);
-        if (u_out && blockIdx.y == 0) *reinterpret_cast<f32x4*>(u_out + (long long)(t.row + row) * r + 4 * c) = v;
-      }
-      v *= s;
-      uint2 hi, lo;
-      hi.x = upper_half(v[0]) | upper_half(v[1]) << 16;
-      hi.y = upper_half(v[2]) | upper_half(v[3]) << 16;
-      lo.x = pack_bf16x2(rest_of(v[0]), rest_of(v[1]));
-      lo.y = pack_bf16x2(rest_of(v[2]), rest_of(v[3]));
-      *reinterpret_cast<uint2*>(&us[row * LD + 4 * c]) = hi;
-      *reinterpret_cast<uint2*>(&us[row * LD + r + 4 * c]) = lo;
-    } else if (c >= 2 * quads) {
-      *reinterpret_cast<uint2*>(&us[row * LD + 4 * c]) = make_uint2(0, 0);
-    }
-  }
-  __syncthreads();
-  bf16x8 uv[MB][KS];
+  const int wave_row = 16 * MB * wave;
+  const uint16_t* xr[MB][4];     // rows 4 i + q of each 16
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
-    for (int k = 0; k < KS; ++k) uv[m][k] = load8(&us[(16 * m + row16) * LD + 32 * k + 8 * q]);
-  int at[KS];             // this lane's place in a weight row at each step; -1: past both parts
+    for (int i = 0; i < 4; ++i) {
+      const int at = wave_row + 16 * m + 4 * i + q;
+      const int row = lora_row(g, t.row + at, at < t.rows);
+      xr[m][i] = x + (long long)max(row, 0) * x_ld;   // a row that is none: any, its sums are dropped
+    }
+  const uint16_t* We = W + (long long)t.e * r * K;
+  const int k_begin = blockIdx.y * slice, k_end = min(K, k_begin + slice);   // multiples of 8
+  // Every load is made, at a place that exists, and what lies past the slice is
+  // replaced by zeros where it is used: a load that may be skipped keeps the
+  // compiler from counting how many are on their way, and it waits for all.
+  u32x4 wv[RB];
+  const auto load_w = [&](int k0) {
 #pragma unroll
-  for (int k = 0; k < KS; ++k) {
-    const int c = 8 * (4 * k + q);
-    at[k] = c < r ? c : c < 2 * r ? c - r : -1;
+    for (int c = 0; c < RB; ++c) {
+      const int i = tid + 256 * c;
+      if constexpr (TURNED) {
+        const int row = i / (2 * RB), rc = 8 * (i - row * (2 * RB));
+        wv[c] = *reinterpret_cast<const u32x4*>(We + (long long)min(k0 + row, k_end - 1) * r + min(rc, r - 8));
+      } else {
+        wv[c] = *reinterpret_cast<const u32x4*>(We + (long long)min(i >> 4, r - 1) * K + min(k0 + 8 * (i & 15), k_end - 8));
+      }
+    }
+  };
+  const auto store_w = [&](int stage, int k0) {
+    uint16_t* d = ws + stage * STAGE;
+#pragma unroll
+    for (int c = 0; c < RB; ++c) {
+      const int i = tid + 256 * c;
+      if constexpr (TURNED) {
+        const int row = i / (2 * RB), rc = 8 * (i - row * (2 * RB));
+        *reinterpret_cast<u32x4*>(d + row * LD + rc) = k0 + row < k_end ? wv[c] : u32x4{0, 0, 0, 0};
+      } else {
+        *reinterpret_cast<u32x4*>(d + (i >> 4) * LD + 8 * (i & 15)) = k0 + 8 * (i & 15) < k_end ? wv[c] : u32x4{0, 0, 0, 0};
+      }
+    }
+  };
+  const auto load_x = [&](int k0, u32x4 (&v)[MB][4]) {
+    const int k = min(k0 + 8 * row16, k_end - 8);
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[m][i] = *reinterpret_cast<const u32x4*>(xr[m][i] + k);
+  };
+  u32x4 xa[MB][4], xb[MB][4];
+  f32x4 acc[MB][RB] = {};
+  uint16_t* mine = xs + wave * (MB * 16 * KT);
+  // 16-byte piece c of row i of a wave's LDS lies at place c ^ i
+  const auto compute = [&](int stage, int k0, const u32x4 (&v)[MB][4]) {
+    const bool in = k0 + 8 * row16 < k_end;
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * i + q;
+        *reinterpret_cast<u32x4*>(mine + (16 * m + row) * KT + 8 * (row16 ^ row)) = in ? v[m][i] : u32x4{0, 0, 0, 0};
+      }
+    const uint16_t* d = ws + stage * STAGE;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      bf16x8 xf[MB];
+#pragma unroll
+      for (int m = 0; m < MB; ++m) xf[m] = load8(mine + (16 * m + row16) * KT + 8 * ((4 * j + q) ^ row16));
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        bf16x8 wf;
+        if constexpr (TURNED) {
+          const uint16_t* p = d + (32 * j + 8 * q + (row16 >> 2)) * LD + 16 * b + 4 * (row16 & 3);
+          wf = read_crosswise(p, p + 4 * LD);
+        } else {
+          wf = load8(d + (16 * b + row16) * LD + 32 * j + 8 * q);
+        }
+#pragma unroll
+        for (int m = 0; m < MB; ++m) acc[m][b] = mfma16(wf, xf[m], acc[m][b]);
+      }
+    }
+  };
+  // a step, while the next one's x and the weights after it are on their way; true:
+  // it was the last
+  const auto step = [&](int stage, int k0, const u32x4 (&v)[MB][4], u32x4 (&next)[MB][4]) {
+    __syncthreads();
+    store_w(stage ^ 1, k0 + KT);
+    load_w(k0 + 2 * KT);
+    load_x(k0 + KT, next);
+    compute(stage, k0, v);
+    return k0 + KT >= k_end;                     // the same for the whole workgroup
+  };
+  load_w(k_begin);
+  load_x(k_begin, xa);
+  store_w(0, k_begin);
+  load_w(k_begin + KT);
+  for (int k0 = k_begin;; k0 += 2 * KT) {
+    if (step(0, k0, xa, xb)) break;
+    if (step(1, k0 + KT, xb, xa)) break;
   }
-  long long yo[MB];
-  bool there[MB];
+  float* o = out + (long long)blockIdx.y * g.M_cap * r;
 #pragma unroll
   for (int m = 0; m < MB; ++m) {
-    const int i = 16 * m + row16;
-    const int row = lora_row(g, t.row + i, i < t.rows);
-    there[m] = row >= 0;
-    yo[m] = (long long)max(row, 0) * y_ld;
-  }
-  const uint16_t* Be = B + (long long)t.e * N * r;
-  const int n_end = min(N, (int)(blockIdx.y + 1) * slice);
-  const int nw = 8 * (row16 >> 2) + (row16 & 3);   // weight row of the first MFMA; the second's: + 4
-  for (int n0 = blockIdx.y * slice + 32 * wave; n0 < n_end; n0 += 128) {
-    f32x4 acc[MB][2] = {};
+    const int at = wave_row + 16 * m + row16;
+    if (at >= t.rows) continue;
+    const bool there = lora_row(g, t.row + at, true) >= 0;
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int n = min(n0 + nw + 4 * j, N - 1);
-        const bf16x8 bv = at[k] >= 0 ? load8(Be + (long long)n * r + at[k]) : zero8();
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-          acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv, uv[m][k], acc[m][j], 0, 0, 0);
-      }
-    const int n = n0 + 8 * q;
-    if (n < n_end)
-#pragma unroll
-      for (int m = 0; m < MB; ++m)
-        if (there[m]) {
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = acc[m][i >> 2][i & 3];
-          if (base) {
-            const u32x4 b = *reinterpret_cast<const u32x4*>(base + yo[m] + n);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[2 * i] += __uint_as_float(b[i] << 16);
-              v[2 * i + 1] += __uint_as_float(b[i] & 0xFFFF0000u);
-            }
-          }
-          u32x4 o;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-          *reinterpret_cast<u32x4*>(y + yo[m] + n) = o;
-        }
+    for (int b = 0; b < RB; ++b) {
+      const int c = 16 * b + 4 * q;               // r is a multiple of 8: all four or none
+      if (c < r)
+        *reinterpret_cast<f32x4*>(o + (long long)(t.row + at) * r + c) = there ? acc[m][b] : f32x4{0, 0, 0, 0};
+    }
   }
 }
 
-// ---------------------------------------------------------------- weights turned round
-// dst[c][r] = src[r][c] (rows x cols), for the groups that have rows: the
-// backward's products read the adapters in the forward's layout.  A tile of 64 x
-// 64 through LDS.
-__global__ __launch_bounds__(256) void lora_turn_kernel(LoraGroups g, const uint16_t* __restrict__ src, int rows,
-                                                        int cols, uint16_t* __restrict__ dst) {
-  __shared__ uint16_t tile[64][66];
-  const int e = blockIdx.z;
-  if (g.counts[e] <= 0) return;
-  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-  const uint16_t* s = src + (long long)e * rows * cols;
-  uint16_t* d = dst + (long long)e * rows * cols;
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int r = i >> 6, c = i & 63;
-    if (r0 + r < rows && c0 + c < cols) tile[r][c] = s[(long long)(r0 + r) * cols + c0 + c];
+// The u of a row from value c (of 8) of its two parts, as a fragment: the slices'
+// sums added in order, times s; the upper half of their bits for c < r, what is left
+// for c < 2 r, else 0.  Two parts hold u to 2^-17 of its value, far below the
+// rounding of y.  out (nullable): where the sum itself goes.
+__device__ __forceinline__ bf16x8 u_fragment(const float* u, long long slice_len, int slices, int r, int c, float s,
+                                             bool inside, float* out) {
+  f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+  if (inside && c < 2 * r) {
+    const int at = c < r ? c : c - r;
+    const float* p = u + at;
+    int i = 0;
+    for (; i + 4 <= slices; i += 4) {
+      f32x4 a[4], b[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        a[k] = *reinterpret_cast<const f32x4*>(p + (i + k) * slice_len);
+        b[k] = *reinterpret_cast<const f32x4*>(p + (i + k) * slice_len + 4);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        lo += a[k];
+        hi += b[k];
+      }
+    }
+    for (; i < slices; ++i) {
+      lo += *reinterpret_cast<const f32x4*>(p + i * slice_len);
+      hi += *reinterpret_cast<const f32x4*>(p + i * slice_len + 4);
+    }
+    if (out && c < r) {
+      *reinterpret_cast<f32x4*>(out + at) = lo;
+      *reinterpret_cast<f32x4*>(out + at + 4) = hi;
+    }
   }
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = s * (i < 4 ? lo[i] : hi[i - 4]);
+  u32x4 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    f[i] = c < r ? upper_half(v[2 * i]) | upper_half(v[2 * i + 1]) << 16
+                 : pack_bf16x2(rest_of(v[2 * i]), rest_of(v[2 * i + 1]));
+  if (c >= 2 * r) f = u32x4{0, 0, 0, 0};          // (an infinite s)
+  return __builtin_bit_cast(bf16x8, f);
+}
+// Eight sums and eight bf16 values of base, rounded once.
+__device__ __forceinline__ u32x4 add_base(const float* v, u32x4 base) {
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = pack_bf16x2(v[2 * i] + __uint_as_float(base[i] << 16), v[2 * i + 1] + __uint_as_float(base[i] & 0xFFFF0000u));
+  return o;
+}
+__device__ __forceinline__ uint32_t pick16(uint32_t lo, uint32_t hi, bool upper) {
+  return __builtin_amdgcn_perm(hi, lo, upper ? 0x07060302u : 0x05040100u);
+}
+
+// ---------------------------------------------------------------- y = base + s u W^T
+// A tile of 64 rows and a slice of N per workgroup, 128 columns at a time, the next
+// step's base and the weights after it in flight.  A wave holds its 16 rows' u as
+// two bf16 parts, [upper r | rest r | zeros], one reduction of KS MFMA steps against
+// the weights taken twice.  The weights come through LDS (two
+// stages) as [column][r], W [N][r] as it is or with TURNED [r][N] (the backward's dx
+// = w A) taken apart by byte permutations.  Column 8 i + j of a step lies in row 16
+// j + i of LDS: MFMA j then gives a lane column j of its eight, so that 16 lanes
+// load and store 256 bytes of a row.
+template <int KS, bool TURNED>
+__global__ __launch_bounds__(256, KS <= 4 ? 3 : 2) void lora_wide_kernel(LoraGroups g, const float* __restrict__ u_in, int slices,
+                                                        float* __restrict__ u_out, const uint16_t* __restrict__ W,
+                                                        const float* __restrict__ scale, int r, int N, int slice,
+                                                        const uint16_t* base, uint16_t* y, long long y_ld) {
+  constexpr int BM = 64, RP = 16 * KS, NT = 128, LD = RP + 8, STAGE = NT * LD;
+  __shared__ __attribute__((aligned(16))) uint16_t ws[2 * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int row16 = lane & 15, q = lane >> 4;
+  const LoraTile t = lora_tile(g, BM, blockIdx.x);
+  if (t.e < 0) return;
+  const uint16_t* We = W + (long long)t.e * N * r;
+  const int n_begin = blockIdx.y * slice, n_end = min(N, n_begin + slice);
+  // TURNED: a thread takes eight columns of a pair of weight rows, KS / 2 times (KS
+  // = 1: half of the threads, once)
+  constexpr int NW = TURNED ? (KS == 1 ? 2 : KS) : KS;
+  u32x4 wv[NW];
+  const auto load_w = [&](int n0) {             // as in the narrow kernel: every load is made
+#pragma unroll
+    for (int c = 0; c < NW; ++c) {
+      if constexpr (TURNED) {
+        const int i = tid + 256 * (c / 2), row = 2 * (i >> 4) + (c & 1);
+        wv[c] = *reinterpret_cast<const u32x4*>(We + (long long)min(row, r - 1) * N + min(n0 + 8 * (i & 15), n_end - 8));
+      } else {
+        const int i = tid + 256 * c, row = i / (2 * KS), rc = 8 * (i - row * (2 * KS));
+        wv[c] = *reinterpret_cast<const u32x4*>(We + (long long)min(n0 + row, n_end - 1) * r + min(rc, r - 8));
+      }
+    }
+  };
+  const auto store_w = [&](int stage) {
+    uint16_t* d = ws + stage * STAGE;
+    if constexpr (TURNED) {
+#pragma unroll
+      for (int c = 0; c < NW; c += 2) {
+        const int i = tid + 256 * (c / 2), row = 2 * (i >> 4);
+        if (row < RP)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint32_t*>(d + (16 * j + (i & 15)) * LD + row) =
+                pick16(wv[c][j / 2], wv[c + 1][j / 2], j & 1);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        const int i = tid + 256 * c, row = i / (2 * KS), rc = 8 * (i - row * (2 * KS));
+        *reinterpret_cast<u32x4*>(d + (16 * (row & 7) + (row >> 3)) * LD + rc) = wv[c];
+      }
+    }
+  };
+  load_w(n_begin);
+  const int wave_row = 16 * wave;
+  long long yo[4];             // rows 4 q + i of the wave's; -1: none
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = wave_row + 4 * q + i;
+    const int row = lora_row(g, t.row + at, at < t.rows);
+    yo[i] = row >= 0 ? (long long)row * y_ld : -1;
+  }
+  const uint16_t* from_base = base ? base : y;  // without a base: read, not used
+  const auto load_base = [&](int n0, u32x4 (&v)[4]) {
+    const int n = min(n0 + 8 * row16, n_end - 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const u32x4*>(from_base + max(yo[i], 0LL) + n);
+  };
+  u32x4 ba[4], bb[4];
+  load_base(n_begin, ba);
+  const float s = scale ? scale[t.e] : 1.0f;
+  bf16x8 uv[KS];
+  {
+    const int at = wave_row + row16;
+    const long long p = (long long)(t.row + at) * r;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+      uv[k] = u_fragment(u_in + p, (long long)g.M_cap * r, slices, r, 8 * (4 * k + q), s, at < t.rows,
+                         u_out && blockIdx.y == 0 ? u_out + p : nullptr);
+  }
+  int from[KS];           // this lane's place in a weight row at each step; -1: past both parts
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    const int c = 8 * (4 * k + q);
+    from[k] = c < r ? c : c < 2 * r ? c - r : -1;
+  }
+  const auto compute = [&](int stage, int n0, const u32x4 (&v)[4]) {
+    const uint16_t* d = ws + stage * STAGE + row16 * LD;
+    f32x4 acc[8] = {};
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bf16x8 wf = from[k] >= 0 ? load8(d + 16 * j * LD + from[k]) : zero8();
+        acc[j] = mfma16(uv[k], wf, acc[j]);
+      }
+    const bool in = n0 + 8 * row16 < n_end;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = acc[j][i];
+      const u32x4 out = add_base(o, base ? v[i] : u32x4{0, 0, 0, 0});
+      if (in && yo[i] >= 0) *reinterpret_cast<u32x4*>(y + yo[i] + n0 + 8 * row16) = out;
+    }
+  };
+  // a step, while the next one's base and the weights after it are on their way; true:
+  // it was the last
+  const auto step = [&](int stage, int n0, const u32x4 (&v)[4], u32x4 (&next)[4]) {
+    __syncthreads();
+    store_w(stage ^ 1);
+    load_w(n0 + 2 * NT);
+    load_base(n0 + NT, next);
+    compute(stage, n0, v);
+    return n0 + NT >= n_end;                      // the same for the whole workgroup
+  };
+  store_w(0);
+  load_w(n_begin + NT);
+  for (int n0 = n_begin;; n0 += 2 * NT) {
+    if (step(0, n0, ba, bb)) break;
+    if (step(1, n0 + NT, bb, ba)) break;
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+// The same two products for a decoding batch, where what counts is how soon every
+// weight is on its way: tiles of 16 rows whose operands go straight from memory to
+// the MFMA.  The narrow one: 512 columns of K per workgroup, whose four waves' sums
+// meet in LDS.
+template <int RB>
+__global__ __launch_bounds__(256) void lora_few_narrow_kernel(LoraGroups g, const uint16_t* __restrict__ x,
+                                                              long long x_ld, const uint16_t* __restrict__ A, int r,
+                                                              int K, float* __restrict__ out) {
+  constexpr int RP = 16 * RB, LD = RP + 4;
+  __shared__ __attribute__((aligned(16))) float red[4 * 16 * LD];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int row16 = lane & 15, q = lane >> 4;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) lora_report(g);
+  const LoraTile t = lora_tile(g, 16, blockIdx.x);
+  if (t.e < 0) return;
+  const int k0 = 512 * blockIdx.y + 128 * wave + 8 * q;
+  bf16x8 av[4][RB], xv[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      const int k = k0 + 32 * j;
+      av[j][b] = k < K ? load8(A + ((long long)t.e * r + min(16 * b + row16, r - 1)) * K + k) : zero8();
+    }
+  const int row = lora_row(g, t.row + row16, row16 < t.rows);
+  const uint16_t* xr = x + (long long)max(row, 0) * x_ld;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) xv[j] = k0 + 32 * j < K ? load8(xr + k0 + 32 * j) : zero8();
+  f32x4 acc[RB] = {};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int b = 0; b < RB; ++b) acc[b] = mfma16(av[j][b], xv[j], acc[b]);
+  if (row < 0)
+#pragma unroll
+    for (int b = 0; b < RB; ++b) acc[b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int b = 0; b < RB; ++b) *reinterpret_cast<f32x4*>(&red[(wave * 16 + row16) * LD + 16 * b + 4 * q]) = acc[b];
   __syncthreads();
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int c = i >> 6, r = i & 63;
-    if (r0 + r < rows && c0 + c < cols) d[(long long)(c0 + c) * rows + r0 + r] = tile[r][c];
+  float* o = out + ((long long)blockIdx.y * g.M_cap + t.row) * r;
+  const int quads = r / 4;
+  for (int i = tid; i < t.rows * quads; i += 256) {
+    const int at = i / quads, c = 4 * (i - at * quads);
+    f32x4 v = *reinterpret_cast<const f32x4*>(&red[at * LD + c]);
+#pragma unroll
+    for (int w = 1; w < 4; ++w) v += *reinterpret_cast<const f32x4*>(&red[(w * 16 + at) * LD + c]);
+    *reinterpret_cast<f32x4*>(o + (long long)at * r + c) = v;
+  }
+}
+
+// The wide one: NB times 32 columns of y per wave; the rows of two MFMAs are chosen
+// so that a lane's eight products are eight consecutive columns.
+template <int KS, int NB>
+__global__ __launch_bounds__(256) void lora_few_wide_kernel(LoraGroups g, const float* __restrict__ u_in, int slices,
+                                                            float* __restrict__ u_out, const uint16_t* __restrict__ B,
+                                                            const float* __restrict__ scale, int r, int N,
+                                                            const uint16_t* base, uint16_t* y, long long y_ld) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int row16 = lane & 15, q = lane >> 4;
+  const LoraTile t = lora_tile(g, 16, blockIdx.x);
+  const int n0 = 32 * NB * (4 * blockIdx.y + wave);
+  if (t.e < 0 || n0 >= N) return;
+  const float s = scale ? scale[t.e] : 1.0f;
+  bf16x8 bv[NB][KS][2];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const int c = 8 * (4 * k + q);
+      const int from = c < r ? c : c < 2 * r ? c - r : -1;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int n = min(n0 + 32 * b + 8 * (row16 >> 2) + (row16 & 3) + 4 * j, N - 1);
+        const bf16x8 v = load8(B + ((long long)t.e * N + n) * r + max(from, 0));
+        bv[b][k][j] = from >= 0 ? v : zero8();
+      }
+    }
+  const int row = lora_row(g, t.row + row16, row16 < t.rows);
+  const long long yo = (long long)max(row, 0) * y_ld;
+  u32x4 old[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int n = n0 + 32 * b + 8 * q;
+    old[b] = u32x4{0, 0, 0, 0};
+    if (base && row >= 0 && n < N) old[b] = *reinterpret_cast<const u32x4*>(base + yo + n);
+  }
+  f32x4 acc[NB][2] = {};
+  const long long p = (long long)(t.row + row16) * r;
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    const bf16x8 uv = u_fragment(u_in + p, (long long)g.M_cap * r, slices, r, 8 * (4 * k + q), s, row16 < t.rows,
+                                 u_out && blockIdx.y == 0 && wave == 0 ? u_out + p : nullptr);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[b][j] = mfma16(bv[b][k][j], uv, acc[b][j]);
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int n = n0 + 32 * b + 8 * q;
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = acc[b][i >> 2][i & 3];
+    if (row >= 0 && n < N) *reinterpret_cast<u32x4*>(y + yo + n) = add_base(o, old[b]);
   }
 }
 
 // ---------------------------------------------------------------- dA, dB
 // The sums over a group's rows of (s u_i) v_i^T, u fp32 [M_cap][r], v bf16 rows of
-// C columns: dA from w and x, dB from u and dy.  A piece of at most `piece` rows
-// of a group and a block of 16 CW columns per workgroup, whose four waves take 32
-// rows in turn; their sums meet in LDS.  The MFMA wants eight rows of one column
-// per lane where memory has columns side by side: a lane loads CW columns of its
-// eight rows and takes them apart with byte permutations, one MFMA for each.  u
-// goes in as three bf16 parts, 24 bits of it, so that the sums are those of
-// fp32 products.
+// C columns: dA from w and x, dB from u and dy.  A piece of a group's rows and 64 CW
+// columns per workgroup, 16 CW for each wave, 32 rows at a time.  The MFMA wants
+// eight rows of one column per lane where memory has columns side by side: a lane
+// loads CW columns of its eight rows and takes them apart with byte permutations,
+// one MFMA for each (CW 8, 4 where eight ranks' sums would not fit the registers).  u goes in as three bf16 parts, 24 bits of it,
+// so that the sums are those of fp32 products; the parts of 32 rows are made once
+// for the four waves, in LDS (two stages).
 struct LoraSum {
   const float* u;
   const uint16_t* v;
@@ -401,111 +656,121 @@ struct LoraSum {
   float* part;       // [slots][r][C] likewise, of groups of more than one piece
   int turned;
 };
-
-__device__ __forceinline__ uint32_t pick16(uint32_t lo, uint32_t hi, bool upper) {
-  return __builtin_amdgcn_perm(hi, lo, upper ? 0x07060302u : 0x05040100u);
-}
+constexpr int kLoraPiece = 2048;   // rows of a piece, at most
 
 template <int RB, int CW>
-__global__ __launch_bounds__(256) void lora_sum_kernel(LoraGroups g, LoraSum a, LoraSum b, int a_blocks,
+__global__ __launch_bounds__(256, RB <= 2 ? 2 : 1) void lora_sum_kernel(LoraGroups g, LoraSum a, LoraSum b, int a_blocks,
                                                        const float* __restrict__ scale, int r, int piece,
                                                        int accumulate) {
-  __shared__ float red[2 * RB * CW * 4 * 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int RP = 16 * RB, LD = 40, PART = RP * LD, STAGE = 3 * PART;
+  __shared__ __attribute__((aligned(16))) int rows[kLoraPiece + 32];
+  __shared__ __attribute__((aligned(16))) uint16_t us[2 * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int row16 = lane & 15, q = lane >> 4;
-  const LoraTile t = lora_tile(g, piece, accumulate ? 0 : 1, blockIdx.x);
+  const LoraTile t = lora_piece(g, piece, accumulate ? 0 : 1, blockIdx.x);
   if (t.e < 0) return;
   const bool first = (int)blockIdx.y < a_blocks;
-  const LoraSum& p = first ? a : b;
-  const int c0 = (first ? blockIdx.y : blockIdx.y - a_blocks) * 16 * CW;
-  const int c = c0 + CW * row16;
-  const bool col_in = c < p.C;                  // C is a multiple of 8
+  const float* u = first ? a.u : b.u;
+  const uint16_t* vp = first ? a.v : b.v;
+  const long long v_ld = first ? a.v_ld : b.v_ld;
+  const int C = first ? a.C : b.C;
+  const int c = ((first ? blockIdx.y : blockIdx.y - a_blocks) * 64 + 16 * wave + row16) * CW;
+  const bool col_in = c < C;                     // C is a multiple of 8
   const float s = scale ? scale[t.e] : 1.0f;
-  f32x4 acc[RB][CW] = {};
-  for (int i0 = 32 * wave; i0 < t.rows; i0 += 128) {
-    uint32_t raw[8][CW / 2];
-    int grow[8];
+  for (int i = tid; i < t.rows + 32; i += 256) rows[i] = lora_row(g, t.row + i, i < t.rows);
+  __syncthreads();
+  // thread: value ri of row pairs
+  const int ri = tid % RP, pair0 = tid / RP;
+  float uv[RB][2];
+  const auto load_u = [&](int i0) {              // as in the narrow kernel: every load is made
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = i0 + 8 * q + i;
-      grow[i] = t.row + at;
-      const int row = lora_row(g, grow[i], at < t.rows);
-      if (row < 0) grow[i] = -1;
+    for (int k = 0; k < RB; ++k)
 #pragma unroll
-      for (int w = 0; w < CW / 2; ++w) raw[i][w] = 0;
-      if (row >= 0 && col_in) {
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(p.v + (long long)row * p.v_ld + c);
-        if constexpr (CW == 8) {
-          const u32x4 v = *reinterpret_cast<const u32x4*>(src);
-          raw[i][0] = v[0]; raw[i][1] = v[1]; raw[i][2] = v[2]; raw[i][3] = v[3];
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(src);
-          raw[i][0] = v.x; raw[i][1] = v.y;
-        }
+      for (int h = 0; h < 2; ++h) {
+        const int at = min(i0 + 2 * (pair0 + k * (256 / RP)) + h, t.rows - 1);
+        uv[k][h] = u[(long long)(t.row + at) * r + min(ri, r - 1)];
       }
+  };
+  const auto store_u = [&](int stage, int i0) {
+    uint16_t* d = us + stage * STAGE + ri * LD;
+#pragma unroll
+    for (int k = 0; k < RB; ++k) {
+      const int at = i0 + 2 * (pair0 + k * (256 / RP));
+      const float v0 = rows[at] >= 0 ? s * uv[k][0] : 0.0f, v1 = rows[at + 1] >= 0 ? s * uv[k][1] : 0.0f;
+      const float r0 = rest_of(v0), r1 = rest_of(v1);
+      uint32_t* o = reinterpret_cast<uint32_t*>(d) + pair0 + k * (256 / RP);
+      o[0] = upper_half(v0) | upper_half(v1) << 16;
+      o[PART / 2] = upper_half(r0) | upper_half(r1) << 16;
+      o[PART] = pack_bf16x2(rest_of(r0), rest_of(r1));
     }
+  };
+  typedef uint32_t cols_t __attribute__((ext_vector_type(CW / 2)));
+  const uint16_t* vc = vp + min(c, C - CW);
+  const auto load_v = [&](int i0, cols_t (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = *reinterpret_cast<const cols_t*>(vc + (long long)max(rows[min(i0, t.rows - 1) + 8 * q + i], 0) * v_ld);
+  };
+  f32x4 acc[RB][CW] = {};
+  const auto compute = [&](int stage, int i0, const cols_t (&w)[8]) {
     bf16x8 col[CW];
+    cols_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = rows[i0 + 8 * q + i] >= 0 ? w[i] : cols_t(0);
 #pragma unroll
     for (int j = 0; j < CW; ++j) {
       u32x4 f;
 #pragma unroll
-      for (int d = 0; d < 4; ++d) f[d] = pick16(raw[2 * d][j / 2], raw[2 * d + 1][j / 2], j & 1);
+      for (int d = 0; d < 4; ++d) f[d] = pick16(v[2 * d][j / 2], v[2 * d + 1][j / 2], j & 1);
       col[j] = __builtin_bit_cast(bf16x8, f);
     }
+    const uint16_t* d = us + stage * STAGE + row16 * LD + 8 * q;
 #pragma unroll
-    for (int k = 0; k < RB; ++k) {
-      const int ri = 16 * k + row16;
-      u32x4 p0, p1, p2;
+    for (int k = 0; k < RB; ++k)
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        float v[2];
+      for (int part = 2; part >= 0; --part) {
+        const bf16x8 uf = load8(d + part * PART + 16 * k * LD);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int gr = grow[2 * d + h];
-          v[h] = gr >= 0 && ri < r ? s * p.u[(long long)gr * r + ri] : 0.0f;
-        }
-        const float r0 = rest_of(v[0]), r1 = rest_of(v[1]);
-        p0[d] = upper_half(v[0]) | upper_half(v[1]) << 16;
-        p1[d] = upper_half(r0) | upper_half(r1) << 16;
-        p2[d] = pack_bf16x2(rest_of(r0), rest_of(r1));
+        for (int j = 0; j < CW; ++j) acc[k][j] = mfma16(uf, col[j], acc[k][j]);
       }
-#pragma unroll
-      for (int j = 0; j < CW; ++j) {
-        acc[k][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, p2), col[j], acc[k][j], 0, 0, 0);
-        acc[k][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, p1), col[j], acc[k][j], 0, 0, 0);
-        acc[k][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, p0), col[j], acc[k][j], 0, 0, 0);
+  };
+  if (t.rows > 0) {
+    cols_t va[8], vb[8];
+    load_u(0);
+    load_v(0, va);
+    store_u(0, 0);
+    load_u(32);
+    // while 32 rows are computed: the next ones' v and the parts of u after them;
+    // true: they were the last
+    const auto step = [&](int i0, int stage, const cols_t (&v)[8], cols_t (&next)[8]) {
+      __syncthreads();
+      if (i0 + 32 >= t.rows) {                   // the same for the whole workgroup
+        compute(stage, i0, v);
+        return true;
       }
+      store_u(stage ^ 1, i0 + 32);
+      load_u(i0 + 64);
+      load_v(i0 + 32, next);
+      compute(stage, i0, v);
+      return false;
+    };
+    for (int i0 = 0;; i0 += 64) {
+      if (step(i0, 0, va, vb)) break;
+      if (step(i0 + 32, 1, vb, va)) break;
     }
   }
-  // waves 2 and 3 onto 0 and 1, then 1 onto 0
-  f32x4* box = reinterpret_cast<f32x4*>(red);
-#pragma unroll
-  for (int step = 2; step >= 1; step >>= 1) {
-    if (wave >= step && wave < 2 * step)
-#pragma unroll
-      for (int k = 0; k < RB; ++k)
-#pragma unroll
-        for (int j = 0; j < CW; ++j) box[(((wave - step) * RB + k) * CW + j) * 64 + lane] = acc[k][j];
-    __syncthreads();
-    if (wave < step)
-#pragma unroll
-      for (int k = 0; k < RB; ++k)
-#pragma unroll
-        for (int j = 0; j < CW; ++j) acc[k][j] += box[((wave * RB + k) * CW + j) * 64 + lane];
-    __syncthreads();
-  }
-  if (wave != 0 || !col_in) return;
+  if (!col_in) return;
   const bool whole = t.pieces == 1;
-  float* o = (whole ? p.out + (long long)t.e * r * p.C : p.part + (long long)t.slot * r * p.C);
+  float* o = whole ? (first ? a.out : b.out) + (long long)t.e * r * C : (first ? a.part : b.part) + (long long)t.slot * r * C;
   const bool add = whole && accumulate;
 #pragma unroll
   for (int k = 0; k < RB; ++k) {
-    const int ri = 16 * k + 4 * q;              // r is a multiple of 8: all four or none
-    if (ri >= r) continue;
-    if (p.turned) {
+    const int rk = 16 * k + 4 * q;               // r is a multiple of 8: all four or none
+    if (rk >= r) continue;
+    if (first ? a.turned : b.turned) {
 #pragma unroll
       for (int j = 0; j < CW; ++j) {
-        f32x4* d = reinterpret_cast<f32x4*>(o + (long long)(c + j) * r + ri);
+        f32x4* d = reinterpret_cast<f32x4*>(o + (long long)(c + j) * r + rk);
         *d = add ? *d + acc[k][j] : acc[k][j];
       }
     } else {
@@ -513,7 +778,7 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(LoraGroups g, LoraSum a, 
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < CW; j += 4) {
-          f32x4* d = reinterpret_cast<f32x4*>(o + (long long)(ri + i) * p.C + c + j);
+          f32x4* d = reinterpret_cast<f32x4*>(o + (long long)(rk + i) * C + c + j);
           const f32x4 v = {acc[k][j][i], acc[k][j + 1][i], acc[k][j + 2][i], acc[k][j + 3][i]};
           *d = add ? *d + v : v;
         }
@@ -521,38 +786,29 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(LoraGroups g, LoraSum a, 
   }
 }
 
-// The pieces of the groups that have more than one, added in their order.
+// The pieces of the groups that have more than one, added in their order: a
+// workgroup takes 1024 values of the blockIdx.y-th such group.
 __global__ __launch_bounds__(256) void lora_join_kernel(LoraGroups g, LoraSum a, LoraSum b, int a_blocks, int r,
                                                         int piece, int accumulate) {
-  // the first piece of group e, found by walking to it
-  const int e = blockIdx.x;
-  const int lane = threadIdx.x & 63;
-  long long run = 0;
-  int slot = 0, mine = 0;
-  for (int f0 = 0; f0 <= e; f0 += 64) {
-    // 64 counts at a time, every lane walks them
-    const int f = f0 + lane;
-    const int v = f < g.L ? g.counts[f] : 0;
-    for (int i = 0; i < 64 && f0 + i <= e; ++i) {
-      const int c = __builtin_amdgcn_readlane(v, i);
-      const long long room = g.M_cap - run;
-      const int m = c <= 0 || room <= 0 ? 0 : (int)(c < room ? c : room);
-      run += c < 0 ? 0 : c;
-      const int n = (m + piece - 1) / piece;
-      if (f0 + i == e) mine = n;
-      else slot += n > 1 ? n : 0;
-    }
-  }
-  if (mine <= 1) return;
-  const bool first = (int)blockIdx.y < a_blocks;
+  const LoraTile t = lora_many(g, piece, blockIdx.y);
+  if (t.e < 0) return;
+  const bool first = (int)blockIdx.x < a_blocks;
   const LoraSum& p = first ? a : b;
   const long long size = (long long)r * p.C;
-  const long long i = 4 * ((long long)(first ? blockIdx.y : blockIdx.y - a_blocks) * 256 + threadIdx.x);
+  const long long i = 4 * ((long long)(first ? blockIdx.x : blockIdx.x - a_blocks) * 256 + threadIdx.x);
   if (i >= size) return;
-  const float* src = p.part + (long long)slot * size + i;
+  const float* src = p.part + (long long)t.slot * size + i;
   f32x4 s = *reinterpret_cast<const f32x4*>(src);
-  for (int k = 1; k < mine; ++k) s += *reinterpret_cast<const f32x4*>(src + (long long)k * size);
-  f32x4* d = reinterpret_cast<f32x4*>(p.out + (long long)e * size + i);
+  int k = 1;
+  for (; k + 8 <= t.pieces; k += 8) {
+    f32x4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const f32x4*>(src + (k + j) * size);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += v[j];
+  }
+  for (; k < t.pieces; ++k) s += *reinterpret_cast<const f32x4*>(src + k * size);
+  f32x4* d = reinterpret_cast<f32x4*>(p.out + (long long)t.e * size + i);
   *d = accumulate ? *d + s : s;
 }
 

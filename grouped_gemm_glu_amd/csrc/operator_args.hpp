@@ -99,18 +99,19 @@ struct AdamwTensor {
   float lr_scale, decay;
   int param_bf16, grad_bf16, state8, pad;
 };
-// A piece of a tensor: elements kAdamwChunk index .. of it.
+// A piece of a tensor: elements chunk * index .. of it.
 struct AdamwChunk {
   int tensor, index;
 };
 constexpr int kAdamwBlock = 128;
-constexpr int kAdamwChunk = 4096;
+constexpr int kAdamwStep = 1024;            // elements of a workgroup's step; a chunk is 2 or 4 of them
 constexpr int kNormParts = 1024;            // workgroups, at most, of the gradients' norm
 
 struct AdamwArgs {
   const AdamwTensor* tensors;
   const AdamwChunk* chunks;
-  long long n_chunks;
+  int chunk;                // elements of a chunk
+  long long n_chunks, n_chunks8;   // all, those of 8-bit states (the last ones)
   double lr, beta1, beta2, eps;
   double bias1, bias2;      // 1 - beta^step, where the step is not the device's
   const int* step;          // device, or null

@@ -663,7 +663,9 @@ typedef struct {
 typedef struct {
   const void* table;        /* device */
   int32_t n_tensors;
-  int64_t n_chunks;
+  int32_t chunk;            /* elements of a piece */
+  int64_t n_chunks;         /* pieces of the tensors, as the table lists them */
+  int64_t n_chunks8;        /* of them, the last ones: those of tensors with 8-bit states */
 } moe_adamw_plan_t;
 size_t moe_adamw_plan_bytes(const moe_adamw_tensor_t* tensors, int n_tensors);
 moe_status_t moe_adamw_plan(const moe_adamw_tensor_t* tensors, int n_tensors, void* table, size_t table_bytes,

@@ -180,6 +180,12 @@ CASES = {
     "rank 120": ([37, 0, 20], 64, 120, 328, 1032),
     "rank 128": ([65, 130], 195, 128, 768, 384),
     "pieces": ([600, 0, 129, 128], 860, 16, 264, 136),
+    "many rows, rank 8": ([1300, 0, 77], 1400, 8, 264, 392),
+    "many rows, rank 16": ([2200], 2200, 16, 520, 1160),
+    "many rows, rank 24": ([130, 700, 129, 640], 1600, 24, 776, 136),
+    "many rows, rank 32": ([1, 900, 200, 300], 1500, 32, 1032, 1544),
+    "many small groups": ([17, 3, 64, 65, 0, 30, 1, 20, 70, 66, 127, 128] * 4, 2400, 16, 392, 264),
+    "many small groups, rank 24": ([17, 3, 64, 65, 0, 30, 1, 20, 70, 66, 100, 128] * 4, 2300, 24, 136, 520),
     "65 groups": ([i % 3 for i in range(65)], 70, 16, 72, 40),
     "1024 groups": ([1 if i % 11 == 5 else 0 for i in range(1024)], 100, 8, 64, 64),
 }
