@@ -944,7 +944,7 @@ moe_status_t moe_lora_fwd(const void* x, int T, const int32_t* src, const moe_gr
   if (st != MOE_OK) return st;
   const int M = a.g.M_cap, L = a.g.L;
   const size_t need = moe_lora_fwd_workspace_bytes(M, L, a.r, a.K, a.N);
-  if (T != 0 && (!x || !y || (M != 0 && !workspace))) return MOE_ERR_NULL;
+  if (T != 0 && (!x || !y || (M != 0 && need > 0 && !workspace))) return MOE_ERR_NULL;
   if (T != 0 && M != 0 && workspace_bytes < need) return MOE_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(y) || !aligned16(base) || !aligned16(u) || !aligned16(workspace)) return MOE_ERR_ALIGN;
   const size_t yb = strided_bytes(T, a.y_ld, a.N);

@@ -33,9 +33,22 @@ int sum_piece(const LoraShape& s) {
   const long long p = (long long)s.M_cap * (sum_blocks(s.r, s.K) + sum_blocks(s.r, s.N)) / 512;
   return p <= 128 ? 128 : p >= kLoraPiece ? kLoraPiece : div_up(p, 64) * 64;
 }
-// Pieces of groups that have more than one: ceil(m / p) <= 2 m / p for m > p.
-size_t sum_slots(const LoraShape& s) { return 2 * (size_t)s.M_cap / (size_t)sum_piece(s); }
-// Whether a call of the forward goes by tiles of 16 rows.
+// Groups of more rows than a piece, at most, and their pieces: ceil(m / p) <= m / p + 1.
+int many_groups(const LoraShape& s) {
+  const int n = s.M_cap / (sum_piece(s) + 1);
+  return n < s.L ? n : s.L;
+}
+size_t sum_slots(const LoraShape& s) { return (size_t)(s.M_cap / sum_piece(s)) + (size_t)many_groups(s); }
+// Whether one launch does both products of the forward: every workgroup of a tile
+// reads the whole A, which pays while that is short beside a launch (3.2 us on the
+// host).  Two launches against one, N 4096: 1 row, r 16: K 512 9.5 / 7.0 us, K 2880 9.5 /
+// 6.9, K 7168 9.2 / 10.9; r 64: K 512 9.5 / 7.7, K 1024 10.1 / 9.6; 64 rows in 32 groups,
+// r 16: K 2880 9.3 / 8.7, K 7168 9.9 / 14.7; r 32, K 2880 11.4 / 12.4; and N 2880, 4 groups,
+// r 16, K 2880: 1024 rows 16.3 / 11.6, 4096 22.7 / 24.9; r 64, K 512: 1024 rows 20.3 / 15.6,
+// 4096 35.2 / 52.4.
+bool fused_rows(const LoraShape& s) { return s.r * s.K <= (1 << 16) && tile_bound(s.M_cap, s.L, 16) <= 128; }
+// Else, whether it goes by tiles of 16 rows (64 rows in 32 groups, r 16, K 2880, N 5760:
+// 9.6 us; 2048 rows in 64 groups, K and N 2880: 30.5 us, with tiles of 64 rows 22.3).
 bool few_rows(const LoraShape& s) { return s.M_cap <= 64 || s.M_cap <= 4LL * s.L; }
 
 template <typename F>
@@ -91,6 +104,7 @@ moe_status_t report(const LoraGroups& g, hipStream_t st) {
 }  // namespace
 
 size_t lora_fwd_workspace(const LoraShape& s) {
+  if (fused_rows(s)) return 0;
   return few_rows(s) ? aligned((size_t)div_up(s.K, 512) * (size_t)s.M_cap * (size_t)s.r * 4) : partial_bytes(s, s.K);
 }
 size_t lora_bwd_workspace(const LoraShape& s) { return bwd_layout(s).end; }
@@ -99,9 +113,17 @@ moe_status_t launch_lora_fwd(const LoraArgs& a, const uint16_t* x, const uint16_
                              void* ws, hipStream_t st) {
   const LoraShape s = {a.g.M_cap, a.g.L, a.r, a.K, a.N};
   if (a.g.M_cap == 0 || a.g.T == 0) return report(a.g, st);
+  const unsigned tiles = tile_bound(s.M_cap, s.L, 16);
+  if (fused_rows(s)) {
+    const int slice = div_up(div_up(a.N, (int)(256 / tiles)), 256) * 256;   // (128 tiles at most)
+    for_rank_blocks(s.r, [&](auto n) {
+      hipLaunchKernelGGL((lora_few_kernel<decltype(n)::value>), dim3(tiles, (unsigned)div_up(a.N, slice)), dim3(512), 0, st,
+                         a.g, x, a.x_ld, a.A, a.B, a.scale, a.r, a.K, a.N, slice, base, y, a.y_ld, u);
+    });
+    return launched();
+  }
   if (few_rows(s)) {
     const int slices = div_up(a.K, 512);
-    const unsigned tiles = tile_bound(s.M_cap, s.L, 16);
     float* part = slices == 1 && u ? u : static_cast<float*>(ws);
     for_rank_blocks(s.r, [&](auto n) {
       constexpr int RB = decltype(n)::value;
@@ -137,6 +159,19 @@ moe_status_t launch_lora_bwd(const LoraArgs& a, const uint16_t* dy, const uint16
   const BwdLayout l = bwd_layout(s);
   char* base = static_cast<char*>(ws);
   float* w = reinterpret_cast<float*>(base + l.w);
+  const int piece = sum_piece(s);
+  const LoraSum sa = {w, x, a.x_ld, a.K, dA, reinterpret_cast<float*>(base + l.sumA), 0};
+  const LoraSum sb = {u, dy, a.y_ld, a.N, dB, reinterpret_cast<float*>(base + l.sumB), 1};
+  const auto sums = [&](bool wa, bool wb) {
+    const int na = wa ? sum_blocks(s.r, a.K) : 0, nb = wb ? sum_blocks(s.r, a.N) : 0;
+    if (na + nb == 0) return;
+    const dim3 grid((unsigned)(s.M_cap / piece + s.L), (unsigned)(na + nb));
+    for_rank_blocks(s.r, [&](auto n) {
+      constexpr int RB = decltype(n)::value;
+      hipLaunchKernelGGL((lora_sum_kernel<RB, RB <= 4 ? 8 : 4>), grid, dim3(256), 0, st, a.g, sa, sb, na, a.scale, s.r,
+                         piece, accumulate);
+    });
+  };
   if (dx || dA) {
     int slice = narrow_slice(s, a.N);
     if (!dx) slice = div_up(a.N, 128) * 128;    // nothing adds slices up: one
@@ -144,26 +179,15 @@ moe_status_t launch_lora_bwd(const LoraArgs& a, const uint16_t* dy, const uint16
     float* part = slices == 1 ? w : reinterpret_cast<float*>(base + l.narrow);
     narrow<true>(a.g, s, dy, a.y_ld, a.B, a.N, slice, part, st);
     if (dx) wide<true>(a.g, s, part, slices, part == w ? nullptr : w, a.A, a.K, a.scale, dx_base, dx, a.x_ld, st);
+    sums(dA != nullptr, dB != nullptr);
+  } else {
+    if (report(a.g, st) != MOE_OK) return MOE_ERR_LAUNCH;
+    sums(false, dB != nullptr);
   }
-  if (!dx && !dA && report(a.g, st) != MOE_OK) return MOE_ERR_LAUNCH;
-  if (dA || dB) {
-    const int piece = sum_piece(s);
-    const LoraSum sa = {w, x, a.x_ld, a.K, dA, reinterpret_cast<float*>(base + l.sumA), 0};
-    const LoraSum sb = {u, dy, a.y_ld, a.N, dB, reinterpret_cast<float*>(base + l.sumB), 1};
-    const int na = dA ? sum_blocks(s.r, a.K) : 0, nb = dB ? sum_blocks(s.r, a.N) : 0;
-    const dim3 grid((unsigned)(s.M_cap / piece + s.L), (unsigned)(na + nb));
-    for_rank_blocks(s.r, [&](auto n) {
-      constexpr int RB = decltype(n)::value;
-      hipLaunchKernelGGL((lora_sum_kernel<RB, RB <= 4 ? 8 : 4>), grid, dim3(256), 0, st, a.g, sa, sb, na, a.scale, s.r,
-                         piece, accumulate);
-    });
-    if (s.M_cap > piece) {
-      const int ja = dA ? div_up((long long)s.r * a.K, 1024) : 0, jb = dB ? div_up((long long)s.r * a.N, 1024) : 0;
-      const int groups = s.M_cap / (piece + 1) < s.L ? s.M_cap / (piece + 1) : s.L;   // of more rows than a piece
-      if (groups > 0)
-        hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)(ja + jb), (unsigned)groups), dim3(256), 0, st, a.g, sa, sb,
-                           ja, s.r, piece, accumulate);
-    }
+  if ((dA || dB) && many_groups(s) > 0) {
+    const int ja = dA ? div_up((long long)s.r * a.K, 1024) : 0, jb = dB ? div_up((long long)s.r * a.N, 1024) : 0;
+    hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)(ja + jb), (unsigned)many_groups(s)), dim3(256), 0, st, a.g, sa, sb,
+                       ja, s.r, piece, accumulate);
   }
   return launched();
 }

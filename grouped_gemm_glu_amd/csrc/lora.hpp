@@ -638,6 +638,109 @@ __global__ __launch_bounds__(256) void lora_few_wide_kernel(LoraGroups g, const 
   }
 }
 
+// Both products in one launch where an adapter's A is small: each workgroup of a
+// tile computes the whole u (its eight waves take runs of 64 columns of K in turn),
+// then a slice of y's columns, 32 at a time for each wave.
+template <int RB>
+__global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint16_t* __restrict__ x, long long x_ld,
+                                                       const uint16_t* __restrict__ A, const uint16_t* __restrict__ B,
+                                                       const float* __restrict__ scale, int r, int K, int N, int slice,
+                                                       const uint16_t* base, uint16_t* y, long long y_ld,
+                                                       float* __restrict__ u_out) {
+  constexpr int RP = 16 * RB, LD = RP + 4, WAVES = 8;
+  __shared__ __attribute__((aligned(16))) float red[WAVES * 16 * LD];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int row16 = lane & 15, q = lane >> 4;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) lora_report(g);
+  const LoraTile t = lora_tile(g, 16, blockIdx.x);
+  if (t.e < 0) return;
+  const int n_end = min(N, (int)(blockIdx.y + 1) * slice);
+  int n0 = blockIdx.y * slice + 32 * wave;
+  int from[RB];
+#pragma unroll
+  for (int k = 0; k < RB; ++k) {
+    const int c = 8 * (4 * k + q);
+    from[k] = c < r ? c : c < 2 * r ? c - r : -1;
+  }
+  bf16x8 bv[RB][2];
+  const auto load_b = [&]() {
+#pragma unroll
+    for (int k = 0; k < RB; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int n = min(n0 + 8 * (row16 >> 2) + (row16 & 3) + 4 * j, N - 1);
+        bv[k][j] = load8(B + ((long long)t.e * N + n) * r + max(from[k], 0));
+      }
+  };
+  load_b();
+  const uint16_t* Ae = A + (long long)t.e * r * K;
+  const float s = scale ? scale[t.e] : 1.0f;
+  const int row = lora_row(g, t.row + row16, row16 < t.rows);
+  const uint16_t* xr = x + (long long)max(row, 0) * x_ld;
+  const long long yo = (long long)max(row, 0) * y_ld;
+  u32x4 old = {0, 0, 0, 0};
+  const auto load_base = [&]() {
+    const int n = n0 + 8 * q;
+    if (base && row >= 0 && n < n_end) old = *reinterpret_cast<const u32x4*>(base + yo + n);
+  };
+  load_base();
+  f32x4 acc[RB] = {};
+  for (int k0 = 64 * wave; k0 < K; k0 += 64 * WAVES) {
+    bf16x8 av[2][RB], xv[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int k = min(k0 + 32 * j + 8 * q, K - 8);
+#pragma unroll
+      for (int b = 0; b < RB; ++b) av[j][b] = load8(Ae + (long long)min(16 * b + row16, r - 1) * K + k);
+      xv[j] = load8(xr + k);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const bool in = k0 + 32 * j + 8 * q < K;
+#pragma unroll
+      for (int b = 0; b < RB; ++b) acc[b] = mfma16(in ? av[j][b] : zero8(), in ? xv[j] : zero8(), acc[b]);
+    }
+  }
+  if (row < 0)
+#pragma unroll
+    for (int b = 0; b < RB; ++b) acc[b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int b = 0; b < RB; ++b) *reinterpret_cast<f32x4*>(&red[(wave * 16 + row16) * LD + 16 * b + 4 * q]) = acc[b];
+  __syncthreads();
+  // the waves' sums, in the place of the first one's
+  const int quads = r / 4;
+  for (int i = tid; i < 16 * quads; i += 512) {
+    const int at = i / quads, c = 4 * (i - at * quads);
+    f32x4 v = *reinterpret_cast<const f32x4*>(&red[at * LD + c]);
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) v += *reinterpret_cast<const f32x4*>(&red[(w * 16 + at) * LD + c]);
+    *reinterpret_cast<f32x4*>(&red[at * LD + c]) = v;
+    if (u_out && blockIdx.y == 0 && at < t.rows) *reinterpret_cast<f32x4*>(u_out + (long long)(t.row + at) * r + c) = v;
+  }
+  __syncthreads();
+  bf16x8 uv[RB];
+#pragma unroll
+  for (int k = 0; k < RB; ++k) uv[k] = u_fragment(&red[row16 * LD], 0, 1, r, 8 * (4 * k + q), s, true, nullptr);
+  while (n0 < n_end) {
+    f32x4 out[2] = {};
+#pragma unroll
+    for (int k = 0; k < RB; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) out[j] = mfma16(from[k] >= 0 ? bv[k][j] : zero8(), uv[k], out[j]);
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = out[i >> 2][i & 3];
+    const u32x4 w = add_base(o, old);
+    const int n = n0 + 8 * q;
+    n0 += 32 * WAVES;
+    if (n0 < n_end) {
+      load_b();
+      load_base();
+    }
+    if (row >= 0 && n < n_end) *reinterpret_cast<u32x4*>(y + yo + n) = w;
+  }
+}
+
 // ---------------------------------------------------------------- dA, dB
 // The sums over a group's rows of (s u_i) v_i^T, u fp32 [M_cap][r], v bf16 rows of
 // C columns: dA from w and x, dB from u and dy.  A piece of a group's rows and 64 CW

@@ -597,7 +597,8 @@ typedef struct {
  * group holds, and grouped rows whose src lies outside [0, T), are left as they
  * were.  u: fp32 [M_cap][r] or NULL, kept for the backward pass (0 in rows whose
  * src lies outside).  All sums are fp32; the product with B takes u to 2^-17 of
- * its value.  workspace: moe_lora_fwd_workspace_bytes(M_cap, E, r, K, N) bytes,
+ * its value.  workspace: moe_lora_fwd_workspace_bytes(M_cap, E, r, K, N) bytes (0
+ * where one launch does it: few rows of a small adapter; then NULL will do),
  * 16-byte aligned, contents of no meaning before or after; calls that may run at
  * the same time, replays of captured ones too, need one each.  Requires M_cap <=
  * 2^25; x, A, B, base, y, u 16-byte, src and scale 4-byte aligned.  T = 0 does

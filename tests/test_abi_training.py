@@ -23,7 +23,7 @@ def _lora(G, A=F, B=2 * F, r=16, K=64, N=72, scale=NULL, x_ld=0, y_ld=0):
     return G.LoraT(A, B, scale, r, K, N, x_ld, y_ld)
 
 
-def _groups(G, counts=3 * F, E=4, M=100):
+def _groups(G, counts=3 * F, E=4, M=5000):
     return G.GroupsT(counts, E, M, None, None)
 
 
@@ -31,10 +31,10 @@ def test_lora_refusals():
     import grouped_gemm_glu_amd as G
     B = ctypes.byref
 
-    def fwd(x=4 * F, T=100, src=5 * F, g=None, lo=None, base=6 * F, y=7 * F, u=8 * F, ws=9 * F, n=BIG):
+    def fwd(x=4 * F, T=5000, src=5 * F, g=None, lo=None, base=6 * F, y=7 * F, u=8 * F, ws=9 * F, n=BIG):
         return G.raw_call("moe_lora_fwd", x, T, src, B(g or _groups(G)), B(lo or _lora(G)), base, y, u, ws, n, NULL)
 
-    def bwd(dy=4 * F, x=5 * F, T=100, src=6 * F, g=None, lo=None, u=7 * F, base=8 * F, dx=9 * F, dA=10 * F, dB=11 * F,
+    def bwd(dy=4 * F, x=5 * F, T=5000, src=6 * F, g=None, lo=None, u=7 * F, base=8 * F, dx=9 * F, dA=10 * F, dB=11 * F,
             acc=0, ws=12 * F, n=BIG):
         return G.raw_call("moe_lora_bwd", dy, x, T, src, B(g or _groups(G)), B(lo or _lora(G)), u, base, dx, dA, dB, acc,
                           ws, n, NULL)
@@ -52,13 +52,13 @@ def test_lora_refusals():
         assert call(T=-1) == SHAPE and call(ws=NULL) == NULL_ and call(ws=9 * F + 8) == ALIGN
     assert fwd(x=NULL) == NULL_ and fwd(y=NULL) == NULL_
     assert fwd(x=4 * F + 2) == ALIGN and fwd(y=7 * F + 8) == ALIGN and fwd(base=6 * F + 8) == ALIGN and fwd(u=8 * F + 4) == ALIGN
-    need = G.moe_lora_fwd_workspace_bytes(100, 4, 16, 64, 72)
+    need = G.moe_lora_fwd_workspace_bytes(5000, 4, 16, 64, 72)
     assert need > 0 and fwd(n=need - 1) == SHAPE
     assert bwd(dy=NULL) == NULL_ and bwd(x=NULL) == NULL_ and bwd(u=NULL) == NULL_ and bwd(dx=NULL, dA=NULL, dB=NULL) == NULL_
     for name in ("dy", "x", "u", "base", "dx", "dA", "dB"):
         assert bwd(**{name: 13 * F + 8}) == ALIGN, name
     assert bwd(acc=2) == UNSUP and bwd(acc=-1) == UNSUP
-    need = G.moe_lora_bwd_workspace_bytes(100, 4, 16, 64, 72)
+    need = G.moe_lora_bwd_workspace_bytes(5000, 4, 16, 64, 72)
     assert need > 0 and bwd(n=need - 1) == SHAPE
     assert G.raw_call("moe_lora_fwd", F, 4, NULL, NULL, B(_lora(G)), NULL, 2 * F, NULL, 3 * F, BIG, NULL) == NULL_
     assert G.raw_call("moe_lora_fwd", F, 4, NULL, B(_groups(G)), NULL, NULL, 2 * F, NULL, 3 * F, BIG, NULL) == NULL_
@@ -79,11 +79,21 @@ def test_lora_empty():
         assert st in (OK, DEVICE), (T, M, st)
 
 
+def test_lora_few_rows_need_no_workspace():
+    import grouped_gemm_glu_amd as G
+    B = ctypes.byref
+    assert G.moe_lora_fwd_workspace_bytes(100, 4, 16, 64, 72) == 0 < G.moe_lora_fwd_workspace_bytes(100, 4, 16, 8192, 72)
+    for K, want in ((64, (OK, DEVICE)), (8192, (NULL_,))):
+        T = 0 if K == 64 else 100      # with rows and a device it would launch with addresses that are none
+        st = G.raw_call("moe_lora_fwd", F, T, NULL, B(_groups(G, M=100)), B(_lora(G, K=K)), NULL, 7 * F, NULL, NULL, 0, NULL)
+        assert st in want, (K, st)
+
+
 def test_lora_overlaps():
     _no_gpu()
     import grouped_gemm_glu_amd as G
     B = ctypes.byref
-    E, M, T, r, K, N = 3, 20, 24, 16, 40, 56
+    E, M, T, r, K, N = 3, 2400, 2404, 16, 40, 56
     for x_ld, y_ld in ((0, 0), (48, 64)):
         xb, yb = ((T - 1) * (x_ld or K) + K) * 2, ((T - 1) * (y_ld or N) + N) * 2
         size = dict(x=xb, src=M * 4, counts=E * 4, A=E * r * K * 2, B_=E * r * N * 2, scale=E * 4, base=yb, y=yb, u=M * r * 4,

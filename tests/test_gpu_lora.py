@@ -76,9 +76,15 @@ class Case:
 
 
 def workspace(n):
-    """Just as large as needed, with values that are not numbers in it."""
+    """Just as large as needed, with values that are not numbers in it and more of them behind."""
     import torch
-    return torch.full((max(16, n),), 0xFF, dtype=torch.uint8, device="cuda")
+    return torch.full((n + 4096,), 0xFF, dtype=torch.uint8, device="cuda")[:n]
+
+
+def check_behind(ws):
+    import torch
+    whole = torch.empty(0, dtype=torch.uint8, device="cuda").set_(ws.untyped_storage())
+    assert whole.numel() == ws.numel() + 4096 and torch.all(whole[ws.numel():] == 0xFF)
 
 
 def check(got, want, tol, what):
@@ -98,6 +104,7 @@ def forward(G, c, base="other", keep_u=True, src=True):
     ws = workspace(G.moe_lora_fwd_workspace_bytes(c.M_cap, c.L, c.r, c.K, c.N))
     G.moe_lora_fwd(x, c.T, grp, lo, y, base=b, src=d_src, u=u, workspace=ws)
     torch.cuda.synchronize()
+    check_behind(ws)
     got_u, got_y = None if u is None else u.cpu().numpy().astype(np.float64), host_bits(y)
     want_u, want_y = P.lora_fwd(c.x, c.A, c.B, c.scale, c.counts, c.M_cap, c.src, None if base is None else c.base)
     abs_s = None if c.scale is None else np.abs(c.scale)
@@ -138,6 +145,7 @@ def backward(G, c, dx="other", want_dA=True, want_dB=True, accumulate=False):
     G.moe_lora_bwd(dy, x if want_dA else None, c.T, grp, lo, torch.from_numpy(u32).cuda() if want_dB else None, dx=out,
                    dx_base=base, dA=dA, dB=dB, accumulate=accumulate, src=d_src, workspace=ws)
     torch.cuda.synchronize()
+    check_behind(ws)
     b = None if dx == "none" else c.dx_base
     want_dx, want_a, want_b, want_w = P.lora_bwd(c.dy, c.x, c.A, c.B, c.scale, c.counts, c.M_cap, u32, c.src, b)
     s_abs = None if c.scale is None else np.abs(c.scale)
@@ -186,6 +194,11 @@ CASES = {
     "many rows, rank 32": ([1, 900, 200, 300], 1500, 32, 1032, 1544),
     "many small groups": ([17, 3, 64, 65, 0, 30, 1, 20, 70, 66, 127, 128] * 4, 2400, 16, 392, 264),
     "many small groups, rank 24": ([17, 3, 64, 65, 0, 30, 1, 20, 70, 66, 100, 128] * 4, 2300, 24, 136, 520),
+    "few rows, long": ([3, 0, 9, 16, 1, 17], 50, 16, 7168, 264),
+    "few rows, long, rank 24": ([1, 0, 2, 5], 9, 24, 2888, 776),
+    "few rows, rank 128": ([7, 30, 1], 40, 128, 1032, 136),
+    "one row in 100 groups, long": ([1] * 100, 100, 8, 8200, 72),
+    "a tile more than one launch takes": ([2040], 2040, 8, 264, 136),
     "65 groups": ([i % 3 for i in range(65)], 70, 16, 72, 40),
     "1024 groups": ([1 if i % 11 == 5 else 0 for i in range(1024)], 100, 8, 64, 64),
 }
