@@ -77,8 +77,7 @@ class AdamwTensorT(ctypes.Structure):
 
 
 class AdamwPlanT(ctypes.Structure):
-    _fields_ = [("table", ctypes.c_void_p), ("n_tensors", ctypes.c_int32), ("chunk", ctypes.c_int32),
-                ("n_chunks", ctypes.c_int64), ("n_chunks8", ctypes.c_int64)]
+    _fields_ = [("table", ctypes.c_void_p), ("n_chunks", ctypes.c_int64), ("n_chunks8", ctypes.c_int64)]
 
 
 class AdamwT(ctypes.Structure):

@@ -11,17 +11,17 @@ moe_status_t launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_
 moe_status_t launch_adamw(const AdamwArgs& a, int cus, hipStream_t s) {
   const long long n32 = a.n_chunks - a.n_chunks8;
   // Workgroups per compute unit, striding over the rest.  32 bits: 5 to 8 streams,
-  // which more workgroups scatter over memory (531M elements: 2 3.43 ms, 3 3.10, 4
-  // 3.16, 8 3.16 to 3.6); 8 bits: its 64-bit arithmetic wants the waves (265M: 2
-  // 1.63 ms, 4 1.34, 8 1.01 to 1.26).
+  // which more workgroups scatter over memory (531M elements: 2 3.18 ms, 3 3.13, 4
+  // 3.21; 3 is 5.1 TB/s); 8 bits: its 64-bit arithmetic wants the waves (265M: 4 1.34
+  // ms, 8 0.99, of which memory takes 0.39 at the same rate).
   const auto grid = [&](long long n, int per_cu) {
     const long long most = (long long)per_cu * cus;
     return dim3((unsigned)(n < most ? n : most));
   };
   if (n32 > 0)
-    hipLaunchKernelGGL(adamw_kernel<false>, grid(n32, 3), dim3(256), 0, s, a, 0LL, n32);
+    hipLaunchKernelGGL(adamw_kernel<false>, grid(n32, 3), dim3(256), 0, s, a, a.chunks, 0LL, n32);
   if (a.n_chunks8 > 0)
-    hipLaunchKernelGGL(adamw_kernel<true>, grid(a.n_chunks8, 8), dim3(256), 0, s, a, n32, a.n_chunks);
+    hipLaunchKernelGGL(adamw_kernel<true>, grid(a.n_chunks8, 8), dim3(256), 0, s, a, a.chunks, n32, a.n_chunks);
   return launched();
 }
 
@@ -34,12 +34,12 @@ moe_status_t launch_adamw_unpack(const int8_t* m, const float* m_scale, const ui
   return launched();
 }
 
-moe_status_t launch_grad_norm(const AdamwTensor* tensors, const AdamwChunk* chunks, int chunk, long long n_chunks,
-                              float max_norm, float* out, double* part, hipStream_t s) {
+moe_status_t launch_grad_norm(const AdamwChunk* chunks, long long n_chunks, float max_norm, float* out, double* part,
+                              hipStream_t s) {
+  // (531M bf16 gradients: 1024 workgroups 165 us, 6.4 TB/s; 768 the same, 512 218)
   const int parts = (int)(n_chunks < kNormParts ? n_chunks : kNormParts);
   if (parts > 0)
-    hipLaunchKernelGGL(grad_norm_kernel, dim3((unsigned)parts), dim3(256), 0, s, tensors, chunks, chunk, n_chunks,
-                       part);
+    hipLaunchKernelGGL(grad_norm_kernel, dim3((unsigned)parts), dim3(256), 0, s, chunks, n_chunks, part);
   hipLaunchKernelGGL(grad_norm_final_kernel, dim3(1), dim3(256), 0, s, part, parts, max_norm, out);
   return launched();
 }

@@ -2,9 +2,9 @@
 // gradients.  Each element's parameter, master, gradient and states are read and
 // written once: the kernels are bound by memory.
 //
-// A table on the device lists the tensors and cuts them into chunks of 4096 elements
-// (2048 where there are few), so that a workgroup finds its elements with two
-// dependent loads however many tensors there are.  A thread takes four consecutive elements of
+// A table on the device lists chunks of 4096 elements of the tensors (2048 where there
+// are few), each with all that its workgroup needs, so that one load leads to the
+// elements however many tensors there are.  A thread takes four consecutive elements of
 // each 1024: 16 bytes of fp32, 8 of bf16, 4 of 8-bit codes.
 #pragma once
 
@@ -172,7 +172,7 @@ struct AdamwFour<true> {
 // elements i .. i + n of the tensor, n <= 4 (WHOLE: n = 4, with nothing skipped, so
 // that the compiler can count the loads on their way)
 template <int PARAM, bool GRAD16, bool STATE8, bool WHOLE>
-__device__ __forceinline__ void adamw_load(const AdamwTensor& t, long long i, int n, AdamwFour<STATE8>& f) {
+__device__ __forceinline__ void adamw_load(const AdamwChunk& t, int i, int n, AdamwFour<STATE8>& f) {
   if constexpr (WHOLE) n = 4;
   load4<GRAD16>(t.grad, i, n, f.g);
   if constexpr (PARAM == 1) load4<true>(t.param, i, n, f.p);
@@ -188,7 +188,7 @@ __device__ __forceinline__ void adamw_load(const AdamwTensor& t, long long i, in
   }
 }
 template <int PARAM, bool STATE8, bool WHOLE>
-__device__ __forceinline__ void adamw_update(const AdamwTensor& t, long long i, int n, const AdamwHyper& h,
+__device__ __forceinline__ void adamw_update(const AdamwChunk& t, int i, int n, const AdamwHyper& h,
                                              const AdamwFour<STATE8>& f) {
   if constexpr (WHOLE) n = 4;
   float m[4], v[4], p[4];
@@ -236,21 +236,33 @@ __device__ __forceinline__ void adamw_update(const AdamwTensor& t, long long i, 
     // outside of these the ratios below leave the normal numbers of 32 bits
     const bool m_in = ma > 1e-25f && ma < 1e30f, v_in = va > 1e-25 && va < 1e30;
     const float im = __builtin_amdgcn_rcpf(ma), iv = __builtin_amdgcn_rcpf((float)va);
+    float x[4], y[4];
     int om[4], ov[4];
     bool unsure = false;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float x = 127.0f * __builtin_amdgcn_sqrtf(fabsf(m[k]) * im);
-      const float y = 255.0f * __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(v[k] * iv));
-      unsure = unsure || near_border(x, kNearM) || near_border(y, kNearRoot);
-      om[k] = (int)fminf(rintf(x), 127.0f);
-      ov[k] = (int)fminf(rintf(y), 255.0f);
+      x[k] = fminf(127.0f * __builtin_amdgcn_sqrtf(fabsf(m[k]) * im), 127.0f);
+      y[k] = fminf(255.0f * __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(v[k] * iv)), 255.0f);
+      unsure = unsure || near_border(x[k], kNearM) || near_border(y[k], kNearRoot);
+      om[k] = (int)rintf(x[k]);
+      ov[k] = (int)rintf(y[k]);
     }
-    if (unsure || !m_in || !v_in) {
+    if (!m_in || !v_in) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         om[k] = m_scale > 0.0f ? code_m_exact(fabs(md[k]), (double)m_scale) : 0;
         ov[k] = v_scale > 0.0f ? code_root_exact(vd[k], (double)v_scale) : 0;
+      }
+    } else if (unsure) {
+      // above the middle between floor and the code after it?
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = (int)x[k], d = (int)y[k];
+        om[k] = c + (fabs(md[k]) * 64516.0 > (double)((2 * c + 1) * (2 * c + 1)) * (double)m_scale);
+        const double d2 = (double)((2 * d + 1) * (2 * d + 1));
+        ov[k] = d + (vd[k] * 67652010000.0 > d2 * d2 * ((double)v_scale * (double)v_scale));
+        om[k] = min(om[k], 127);
+        ov[k] = min(ov[k], 255);
       }
     }
     uint32_t wm = 0, wv = 0;
@@ -284,25 +296,22 @@ __device__ __forceinline__ void adamw_update(const AdamwTensor& t, long long i, 
 
 // One chunk: its whole steps two at a time, their loads together, then what is left.
 template <int PARAM, bool GRAD16, bool STATE8>
-__device__ __forceinline__ void adamw_chunk(const AdamwTensor& t, long long first, int chunk, const AdamwHyper& h) {
+__device__ __forceinline__ void adamw_chunk(const AdamwChunk& t, const AdamwHyper& h) {
   constexpr int STEPS = 2;
-  const long long left = min(t.n - first, (long long)chunk);
-  const int whole = (int)left / kAdamwStep;
-  const long long i = first + 4 * threadIdx.x;
-  int s = 0;
-  for (; s + STEPS <= whole; s += STEPS) {
+  const int i = 4 * threadIdx.x;
+  int at = 0;
+  for (; at + STEPS * kAdamwStep <= t.n; at += STEPS * kAdamwStep) {
     AdamwFour<STATE8> f[STEPS];
 #pragma unroll
-    for (int k = 0; k < STEPS; ++k) adamw_load<PARAM, GRAD16, STATE8, true>(t, i + kAdamwStep * (s + k), 4, f[k]);
+    for (int k = 0; k < STEPS; ++k) adamw_load<PARAM, GRAD16, STATE8, true>(t, at + i + kAdamwStep * k, 4, f[k]);
 #pragma unroll
-    for (int k = 0; k < STEPS; ++k) adamw_update<PARAM, STATE8, true>(t, i + kAdamwStep * (s + k), 4, h, f[k]);
+    for (int k = 0; k < STEPS; ++k) adamw_update<PARAM, STATE8, true>(t, at + i + kAdamwStep * k, 4, h, f[k]);
   }
-  for (; kAdamwStep * s < left; ++s) {
-    const long long at = (long long)kAdamwStep * s + 4 * threadIdx.x;
-    const int n = at >= left ? 0 : left - at < 4 ? (int)(left - at) : 4;
+  for (; at < t.n; at += kAdamwStep) {
+    const int n = max(0, min(4, t.n - at - i));
     AdamwFour<STATE8> f;
-    adamw_load<PARAM, GRAD16, STATE8, false>(t, first + at, n, f);
-    adamw_update<PARAM, STATE8, false>(t, first + at, n, h, f);
+    adamw_load<PARAM, GRAD16, STATE8, false>(t, at + i, n, f);
+    adamw_update<PARAM, STATE8, false>(t, at + i, n, h, f);
   }
 }
 
@@ -310,7 +319,8 @@ __device__ __forceinline__ void adamw_chunk(const AdamwTensor& t, long long firs
 // (m' / (1 - b1^t)) / (sqrt(v' / (1 - b2^t)) + eps).  The chunks of 32-bit and of
 // 8-bit states lie apart, each with a kernel of its own.
 template <bool STATE8>
-__global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a, long long first_chunk, long long end_chunk) {
+__global__ __launch_bounds__(256, 4) void adamw_kernel(AdamwArgs a, const AdamwChunk* __restrict__ chunks,
+                                                    long long first_chunk, long long end_chunk) {
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
   if (gs != gs) return;                        // gradients without a norm: no step
   const double lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
@@ -333,22 +343,21 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a, long long first
   h.exact_root = a.eps < 1e-15;
   h.root_scale = (float)(1.0 / bias2);
   h.grad_scale = gs;
-  AdamwChunk ch = a.chunks[first_chunk + blockIdx.x];   // (a workgroup has one chunk at least)
+  AdamwChunk next = chunks[first_chunk + blockIdx.x];   // (a workgroup has one chunk at least)
   for (long long c = first_chunk + blockIdx.x; c < end_chunk; c += gridDim.x) {
-    const AdamwTensor t = a.tensors[ch.tensor];
-    const long long first = (long long)ch.index * a.chunk;
-    if (c + gridDim.x < end_chunk) ch = a.chunks[c + gridDim.x];
+    const AdamwChunk t = next;
+    next = chunks[min(c + gridDim.x, end_chunk - 1)];
     if (!t.param) continue;
     h.step_size = (float)(lr * (double)t.lr_scale / bias1);
     h.shrink = (float)(1.0 - lr * (double)t.lr_scale * (double)t.decay);
     if (t.grad_bf16) {
-      if (t.master) adamw_chunk<2, true, STATE8>(t, first, a.chunk, h);
-      else if (t.param_bf16) adamw_chunk<1, true, STATE8>(t, first, a.chunk, h);
-      else adamw_chunk<0, true, STATE8>(t, first, a.chunk, h);
+      if (t.master) adamw_chunk<2, true, STATE8>(t, h);
+      else if (t.param_bf16) adamw_chunk<1, true, STATE8>(t, h);
+      else adamw_chunk<0, true, STATE8>(t, h);
     } else {
-      if (t.master) adamw_chunk<2, false, STATE8>(t, first, a.chunk, h);
-      else if (t.param_bf16) adamw_chunk<1, false, STATE8>(t, first, a.chunk, h);
-      else adamw_chunk<0, false, STATE8>(t, first, a.chunk, h);
+      if (t.master) adamw_chunk<2, false, STATE8>(t, h);
+      else if (t.param_bf16) adamw_chunk<1, false, STATE8>(t, h);
+      else adamw_chunk<0, false, STATE8>(t, h);
     }
   }
 }
@@ -394,29 +403,36 @@ __device__ __forceinline__ double block_sum(double v, double* tmp) {   // tmp: 4
   return tmp[0] + tmp[1] + tmp[2] + tmp[3];
 }
 template <bool BF16>
-__device__ __forceinline__ void add_squares(const AdamwTensor& t, long long first, int chunk, double* sum) {
-  const long long left = min(t.n - first, (long long)chunk);
-#pragma unroll 4
-  for (int s = 0; s * kAdamwStep < chunk; ++s) {
-    const long long at = (long long)kAdamwStep * s + 4 * threadIdx.x;
-    const int n = at >= left ? 0 : left - at < 4 ? (int)(left - at) : 4;
-    float g[4];
-    load4<BF16>(t.grad, first + at, n, g);
+__device__ __forceinline__ void add_squares(const AdamwChunk& t, double* sum) {
+  const auto add = [&](const float* g) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) sum[k] = fma((double)g[k], (double)g[k], sum[k]);
+  };
+  const int i = 4 * threadIdx.x;
+  int at = 0;
+  for (; at + 2 * kAdamwStep <= t.n; at += 2 * kAdamwStep) {
+    float g[2][4];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) load4<BF16>(t.grad, at + kAdamwStep * s + i, 4, g[s]);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) add(g[s]);
+  }
+  for (; at < t.n; at += kAdamwStep) {
+    float g[4];
+    load4<BF16>(t.grad, at + i, max(0, min(4, t.n - at - i)), g);
+    add(g);
   }
 }
-__global__ __launch_bounds__(256) void grad_norm_kernel(const AdamwTensor* __restrict__ tensors,
-                                                        const AdamwChunk* __restrict__ chunks, int chunk, long long n_chunks,
+__global__ __launch_bounds__(256) void grad_norm_kernel(const AdamwChunk* __restrict__ chunks, long long n_chunks,
                                                         double* __restrict__ part) {
   __shared__ double tmp[4];
   double sum[4] = {};
+  AdamwChunk next = chunks[blockIdx.x];
   for (long long c = blockIdx.x; c < n_chunks; c += gridDim.x) {
-    const AdamwChunk ch = chunks[c];
-    const AdamwTensor t = tensors[ch.tensor];
-    const long long first = (long long)ch.index * chunk;
-    if (t.grad_bf16) add_squares<true>(t, first, chunk, sum);
-    else add_squares<false>(t, first, chunk, sum);
+    const AdamwChunk t = next;
+    next = chunks[min(c + gridDim.x, n_chunks - 1)];
+    if (t.grad_bf16) add_squares<true>(t, sum);
+    else add_squares<false>(t, sum);
   }
   const double s = block_sum((sum[0] + sum[1]) + (sum[2] + sum[3]), tmp);
   if (threadIdx.x == 0) part[blockIdx.x] = s;

@@ -1023,7 +1023,7 @@ size_t moe_adamw_plan_bytes(const moe_adamw_tensor_t* tensors, int n_tensors) {
   const int chunk = adamw_chunk(tensors, n_tensors);
   size_t chunks = 0;
   for (int i = 0; i < n_tensors; ++i) chunks += (size_t)adamw_chunks(tensors[i], chunk);
-  return (size_t)n_tensors * sizeof(AdamwTensor) + chunks * sizeof(AdamwChunk);
+  return chunks * sizeof(AdamwChunk);
 }
 
 // Whether an output of the tensors shares bytes with any other buffer of them:
@@ -1082,39 +1082,41 @@ moe_status_t moe_adamw_plan(const moe_adamw_tensor_t* tensors, int n_tensors, vo
     const moe_status_t st = adamw_overlap(tensors, n_tensors);
     if (st != MOE_OK) return st;
   }
-  AdamwTensor* out = static_cast<AdamwTensor*>(table);
-  AdamwChunk* chunk = reinterpret_cast<AdamwChunk*>(out + n_tensors);
-  long long total = 0;
-  for (int i = 0; i < n_tensors; ++i) {
-    const moe_adamw_tensor_t& t = tensors[i];
-    memset(&out[i], 0, sizeof(out[i]));
-    out[i].param = t.param;
-    out[i].grad = t.grad;
-    out[i].master = t.master;
-    out[i].m = t.m;
-    out[i].v = t.v;
-    out[i].m_scale = t.m_scale;
-    out[i].v_scale = t.v_scale;
-    out[i].n = t.n;
-    out[i].lr_scale = t.lr_scale;
-    out[i].decay = t.weight_decay;
-    out[i].param_bf16 = t.param_dtype == MOE_DT_BF16;
-    out[i].grad_bf16 = t.grad_dtype == MOE_DT_BF16;
-    out[i].state8 = t.state_bits == 8;
-  }
-  // first the chunks of 32-bit states (and of gradients alone), then those of 8-bit
-  long long total8 = 0;
+  AdamwChunk* out = static_cast<AdamwChunk*>(table);
   const int size = adamw_chunk(tensors, n_tensors);
+  const auto from = [](const void* p, long long bytes) {
+    return p ? const_cast<char*>(static_cast<const char*>(p)) + bytes : nullptr;
+  };
+  // first the chunks of 32-bit states (and of gradients alone), then those of 8-bit
+  long long total = 0, total8 = 0;
   for (int bits8 = 0; bits8 < 2; ++bits8)
     for (int i = 0; i < n_tensors; ++i) {
-      if ((tensors[i].param && tensors[i].state_bits == 8) != (bits8 != 0)) continue;
-      const long long n = adamw_chunks(tensors[i], size);
-      for (long long c = 0; c < n; ++c) chunk[total++] = {i, (int)c};
-      if (bits8) total8 += n;
+      const moe_adamw_tensor_t& t = tensors[i];
+      if ((t.param && t.state_bits == 8) != (bits8 != 0)) continue;
+      const int param = t.param_dtype == MOE_DT_BF16 ? 2 : 4, grad = t.grad_dtype == MOE_DT_BF16 ? 2 : 4;
+      const int state = t.state_bits / 8;
+      for (long long at = 0; at < t.n; at += size) {
+        AdamwChunk& c = out[total++];
+        memset(&c, 0, sizeof(c));
+        c.grad = from(t.grad, at * grad);
+        c.grad_bf16 = grad == 2;
+        c.n = (int)(t.n - at < size ? t.n - at : size);
+        if (!t.param) continue;
+        c.param = from(t.param, at * param);
+        c.master = reinterpret_cast<float*>(from(t.master, at * 4));
+        c.m = from(t.m, at * state);
+        c.v = from(t.v, at * state);
+        if (bits8) {
+          c.m_scale = t.m_scale + at / kAdamwBlock;
+          c.v_scale = t.v_scale + at / kAdamwBlock;
+        }
+        c.lr_scale = t.lr_scale;
+        c.decay = t.weight_decay;
+        c.param_bf16 = param == 2;
+        total8 += bits8;
+      }
     }
   plan->table = nullptr;
-  plan->n_tensors = n_tensors;
-  plan->chunk = size;
   plan->n_chunks = total;
   plan->n_chunks8 = total8;
   return MOE_OK;
@@ -1122,8 +1124,7 @@ moe_status_t moe_adamw_plan(const moe_adamw_tensor_t* tensors, int n_tensors, vo
 
 static moe_status_t check_plan(const moe_adamw_plan_t* plan) {
   if (!plan) return MOE_ERR_NULL;
-  if (plan->n_tensors < 0 || plan->n_chunks8 < 0 || plan->n_chunks < plan->n_chunks8) return MOE_ERR_SHAPE;
-  if (plan->n_chunks > 0 && (plan->chunk < kAdamwStep || plan->chunk % kAdamwStep != 0)) return MOE_ERR_SHAPE;
+  if (plan->n_chunks8 < 0 || plan->n_chunks < plan->n_chunks8) return MOE_ERR_SHAPE;
   if (plan->n_chunks > 0 && !plan->table) return MOE_ERR_NULL;
   if (!aligned16(plan->table)) return MOE_ERR_ALIGN;
   return MOE_OK;
@@ -1140,9 +1141,7 @@ moe_status_t moe_adamw_step(const moe_adamw_plan_t* plan, const moe_adamw_t* h, 
   int cus;
   if ((st = ensure_init(&cus)) != MOE_OK) return st;
   AdamwArgs a;
-  a.tensors = static_cast<const AdamwTensor*>(plan->table);
-  a.chunks = reinterpret_cast<const AdamwChunk*>(a.tensors + plan->n_tensors);
-  a.chunk = plan->chunk;
+  a.chunks = static_cast<const AdamwChunk*>(plan->table);
   a.n_chunks = plan->n_chunks;
   a.n_chunks8 = plan->n_chunks8;
   a.lr = h->lr;
@@ -1186,9 +1185,7 @@ moe_status_t moe_grad_norm(const moe_adamw_plan_t* plan, float max_norm, float* 
   if (overlap({{out, 8}, {workspace, moe_grad_norm_workspace_bytes()}}, {})) return MOE_ERR_UNSUPPORTED;
   int cus;
   if ((st = ensure_init(&cus)) != MOE_OK) return st;
-  const AdamwTensor* t = static_cast<const AdamwTensor*>(plan->table);
-  return launch_grad_norm(t, reinterpret_cast<const AdamwChunk*>(t + plan->n_tensors), plan->chunk, plan->n_chunks, max_norm,
-                          out,
+  return launch_grad_norm(static_cast<const AdamwChunk*>(plan->table), plan->n_chunks, max_norm, out,
                           static_cast<double*>(workspace), (hipStream_t)stream);
 }
 

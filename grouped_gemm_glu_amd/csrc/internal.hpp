@@ -82,8 +82,8 @@ moe_status_t launch_lora_bwd(const LoraArgs& a, const uint16_t* dy, const uint16
 moe_status_t launch_adamw(const AdamwArgs& a, int cus, hipStream_t s);
 moe_status_t launch_adamw_unpack(const int8_t* m, const float* m_scale, const uint8_t* v, const float* v_scale,
                                  long long n, float* m_out, float* v_out, hipStream_t s);
-moe_status_t launch_grad_norm(const AdamwTensor* tensors, const AdamwChunk* chunks, int chunk, long long n_chunks,
-                              float max_norm, float* out, double* part, hipStream_t s);
+moe_status_t launch_grad_norm(const AdamwChunk* chunks, long long n_chunks, float max_norm, float* out, double* part,
+                              hipStream_t s);
 
 // MXFP4 (mxfp4.hip); a4: e2m1 rows, else e4m3
 moe_status_t launch_mx4_rows(const uint16_t* v, int R, int C, const int* counts, int E, uint8_t* q,

@@ -86,31 +86,26 @@ struct LoraArgs {
   long long x_ld, y_ld;
 };
 
-// One tensor of an AdamW step, as the device's table holds it.
-struct AdamwTensor {
-  void* param;              // null: the tensor takes part in the norm alone
+// A piece of a tensor of an AdamW step, as the device's table holds it: everything
+// that its workgroup needs, so that one load leads to the elements.
+struct AdamwChunk {
+  void* param;              // its first element; null: the tensor takes part in the norm alone
   const void* grad;
   float* master;            // null: the parameter is its own
   void* m;
   void* v;
   float* m_scale;           // 8-bit states: one of each per kAdamwBlock elements
   float* v_scale;
-  long long n;
   float lr_scale, decay;
-  int param_bf16, grad_bf16, state8, pad;
-};
-// A piece of a tensor: elements chunk * index .. of it.
-struct AdamwChunk {
-  int tensor, index;
+  int n;                    // elements
+  uint16_t param_bf16, grad_bf16;
 };
 constexpr int kAdamwBlock = 128;
 constexpr int kAdamwStep = 1024;            // elements of a workgroup's step; a chunk is 2 or 4 of them
 constexpr int kNormParts = 1024;            // workgroups, at most, of the gradients' norm
 
 struct AdamwArgs {
-  const AdamwTensor* tensors;
   const AdamwChunk* chunks;
-  int chunk;                // elements of a chunk
   long long n_chunks, n_chunks8;   // all, those of 8-bit states (the last ones)
   double lr, beta1, beta2, eps;
   double bias1, bias2;      // 1 - beta^step, where the step is not the device's

@@ -663,8 +663,6 @@ typedef struct {
  * MOE_ERR_UNSUPPORTED.  (host struct) */
 typedef struct {
   const void* table;        /* device */
-  int32_t n_tensors;
-  int32_t chunk;            /* elements of a piece */
   int64_t n_chunks;         /* pieces of the tensors, as the table lists them */
   int64_t n_chunks8;        /* of them, the last ones: those of tensors with 8-bit states */
 } moe_adamw_plan_t;

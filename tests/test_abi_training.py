@@ -153,7 +153,7 @@ def test_plan_refusals():
     assert G.raw_call("moe_adamw_plan", None, (1 << 24) + 1, None, 0, ctypes.byref(G.AdamwPlanT())) == SHAPE
     assert G.raw_call("moe_adamw_plan", None, 3, F, 0, ctypes.byref(G.AdamwPlanT())) == NULL_
     st, plan, _, size = _plan(G, [])
-    assert st == OK and size == 0 and plan.n_tensors == plan.n_chunks == 0
+    assert st == OK and size == 0 and plan.n_chunks == plan.n_chunks8 == 0
 
 
 def test_plan_overlaps():
@@ -189,29 +189,22 @@ def test_plan_overlaps():
 
 
 def test_plan_table():
-    """Chunks of 2048 elements (4096 from 2^22 on), in order, and each tensor as it was given."""
+    """Pieces of 2048 elements (4096 from 2^22 on) in the tensors' order, those of 8-bit states last; each begins where
+    its tensor's piece does (the first words of an entry are the parameter's and the gradient's address)."""
     import grouped_gemm_glu_amd as G
     ns = [1, 0, 4096, 4097, 10000]
     ts = [_tensor(G, param=(20 * i + 1) * F, grad=(20 * i + 2) * F, m=(20 * i + 3) * F, v=(20 * i + 4) * F, n=n, lr=0.5 + i,
                   wd=0.1 * i, gd=G.DT_BF16) for i, n in enumerate(ns)]
+    ts[2] = _tensor(G, param=41 * F, grad=42 * F, m=43 * F, v=44 * F, ms=45 * F, vs=46 * F, n=4096, bits=8, pd=G.DT_BF16)
     st, plan, buf, size = _plan(G, ts)
-    chunks = [(i, c) for i, n in enumerate(ns) for c in range(-(-n // 2048))]
-    assert st == OK and plan.n_tensors == 5 and plan.n_chunks == len(chunks) and plan.table is None and plan.chunk == 2048
-    raw = bytes(buf)[:size]
-    each = (size - 8 * len(chunks)) // 5
-    for i, n in enumerate(ns):
-        words = [int.from_bytes(raw[i * each + 8 * k:i * each + 8 * k + 8], "little") for k in range(8)]
-        assert words[0] == (20 * i + 1) * F and words[1] == (20 * i + 2) * F and words[7] == n
-    got = [(int.from_bytes(raw[5 * each + 8 * k:5 * each + 8 * k + 4], "little"),
-            int.from_bytes(raw[5 * each + 8 * k + 4:5 * each + 8 * k + 8], "little")) for k in range(len(chunks))]
-    assert got == chunks
-    # the chunks of 8-bit states come last
-    ts[2] = _tensor(G, param=41 * F, grad=42 * F, m=43 * F, v=44 * F, ms=45 * F, vs=46 * F, n=4096, bits=8)
-    st, plan, buf, size = _plan(G, ts)
-    assert st == OK and plan.n_chunks == len(chunks) and plan.n_chunks8 == 2
-    assert int.from_bytes(bytes(buf)[size - 8:size - 4], "little") == 2
+    want = [((20 * i + 1) * F + 4 * at, (20 * i + 2) * F + 2 * at) for i in (0, 3, 4) for at in range(0, ns[i], 2048)]
+    want += [(41 * F + 2 * at, 42 * F + 4 * at) for at in (0, 2048)]
+    assert st == OK and plan.table is None and plan.n_chunks == len(want) and plan.n_chunks8 == 2 and size % len(want) == 0
+    each = size // len(want)
+    word = lambda i, k: int.from_bytes(bytes(buf)[i * each + 8 * k:i * each + 8 * k + 8], "little")  # noqa: E731
+    assert [(word(i, 0), word(i, 1)) for i in range(len(want))] == want
     st, plan, _, size = _plan(G, [_tensor(G, grad=64 * F, m=128 * F, v=192 * F, n=(1 << 22) + 1)])
-    assert st == OK and plan.chunk == 4096 and plan.n_chunks == 1025 and size == each + 8 * 1025
+    assert st == OK and plan.n_chunks == 1025 and plan.n_chunks8 == 0 and size == each * 1025
     bad = (G.AdamwTensorT * 1)(_tensor(G, n=-5))
     assert G._lib.moe_adamw_plan_bytes(bad, 1) == 0 and G._lib.moe_adamw_plan_bytes(None, 3) == 0
 
@@ -221,22 +214,20 @@ def test_step_refusals():
     B = ctypes.byref
 
     def step(plan=None, h=None, **k):
-        return G.raw_call("moe_adamw_step", B(plan or G.AdamwPlanT(F, 1, 4096, 1)), B(h or G.adamw(**{**dict(lr=1e-3), **k})), NULL)
+        return G.raw_call("moe_adamw_step", B(plan or G.AdamwPlanT(F, 1)), B(h or G.adamw(**{**dict(lr=1e-3), **k})), NULL)
     assert G.raw_call("moe_adamw_step", NULL, B(G.adamw(1e-3)), NULL) == NULL_
-    assert G.raw_call("moe_adamw_step", B(G.AdamwPlanT(F, 1, 4096, 1)), NULL, NULL) == NULL_
-    assert step(plan=G.AdamwPlanT(None, 1, 4096, 1)) == NULL_ and step(plan=G.AdamwPlanT(F + 8, 1, 4096, 1)) == ALIGN
-    assert step(plan=G.AdamwPlanT(F, -1, 4096, 1)) == SHAPE and step(plan=G.AdamwPlanT(F, 1, 4096, -1)) == SHAPE
-    assert step(plan=G.AdamwPlanT(F, 1, 0, 1)) == SHAPE and step(plan=G.AdamwPlanT(F, 1, 1000, 1)) == SHAPE
-    assert step(plan=G.AdamwPlanT(F, 1, 4096, 1, 2)) == SHAPE and step(plan=G.AdamwPlanT(F, 1, 4096, 1, -1)) == SHAPE
+    assert G.raw_call("moe_adamw_step", B(G.AdamwPlanT(F, 1)), NULL, NULL) == NULL_
+    assert step(plan=G.AdamwPlanT(None, 1)) == NULL_ and step(plan=G.AdamwPlanT(F + 8, 1)) == ALIGN
+    assert step(plan=G.AdamwPlanT(F, -1)) == SHAPE and step(plan=G.AdamwPlanT(F, 1, 2)) == SHAPE and step(plan=G.AdamwPlanT(F, 1, -1)) == SHAPE
     for bad in (dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0), dict(beta2=math.nan), dict(eps=-1e-8), dict(eps=math.inf),
                 dict(lr=math.inf), dict(lr=math.nan), dict(step=0), dict(step=-1)):
         assert step(**bad) == SHAPE, bad
     assert step(step_dev=F + 2) == ALIGN and step(lr_dev=F + 2) == ALIGN and step(grad_scale=F + 2) == ALIGN
-    assert step(plan=G.AdamwPlanT(None, 0, 0, 0)) in (OK, DEVICE)
+    assert step(plan=G.AdamwPlanT(None, 0)) in (OK, DEVICE)
 
     def norm(plan=None, most=1.0, out=2 * F, ws=3 * F, n=BIG):
-        return G.raw_call("moe_grad_norm", B(plan or G.AdamwPlanT(F, 1, 4096, 1)), most, out, ws, n, NULL)
-    assert norm(plan=G.AdamwPlanT(None, 1, 4096, 1)) == NULL_ and norm(out=NULL) == NULL_ and norm(ws=NULL) == NULL_
+        return G.raw_call("moe_grad_norm", B(plan or G.AdamwPlanT(F, 1)), most, out, ws, n, NULL)
+    assert norm(plan=G.AdamwPlanT(None, 1)) == NULL_ and norm(out=NULL) == NULL_ and norm(ws=NULL) == NULL_
     assert norm(most=0.0) == SHAPE and norm(most=-1.0) == SHAPE and norm(most=math.nan) == SHAPE
     assert norm(n=G.moe_grad_norm_workspace_bytes() - 1) == SHAPE and norm(out=2 * F + 2) == ALIGN and norm(ws=3 * F + 8) == ALIGN
     assert norm(out=3 * F + 8) == UNSUP
