@@ -301,6 +301,9 @@ def adamw_tensor(param, grad, m, v, master=None, m_scale=None, v_scale=None, wei
                               ("m_scale", m_scale, blocks), ("v_scale", v_scale, blocks)):
             if t is not None and t.numel() != size:
                 raise ValueError(f"{name} has {t.numel()} elements, not {size}")
+        for name, t in (("m_scale", m_scale), ("v_scale", v_scale)):
+            if t is not None and str(t.dtype) != "torch.float32":
+                raise TypeError(f"{name} is float32, not {t.dtype}")
     for t in (param, grad, m, v, master, m_scale, v_scale):
         if t is not None and not t.is_contiguous():
             raise ValueError("the tensors of a step are contiguous")
@@ -311,16 +314,20 @@ def adamw_tensor(param, grad, m, v, master=None, m_scale=None, v_scale=None, wei
 
 
 def adamw_plan(tensors, device=None) -> AdamwPlanT:
-    """Lays out the tensors of a step (adamw_tensor structs) once, with the table in the memory of ``device`` (the
-    current one), copied before the call returns.  The plan keeps the tensors alive."""
+    """Lays out the tensors of a step (adamw_tensor structs) once, with the table in the memory of their device (or
+    ``device``, where they are none), copied before the call returns.  The plan keeps the tensors alive."""
     import torch
     tensors = list(tensors)
+    devices = {str(t.device) for s in tensors for t in s._keep if t is not None}
+    if len(devices) > 1 or not all(d.startswith("cuda") for d in devices):
+        raise ValueError(f"the tensors of a plan are on one GPU, not on {', '.join(sorted(devices))}")
+    device = devices.pop() if devices else "cuda" if device is None else device
     array = (AdamwTensorT * max(1, len(tensors)))(*tensors)
     size = _lib.moe_adamw_plan_bytes(array, len(tensors))
     host = torch.zeros(max(8, size), dtype=torch.uint8)
     plan = AdamwPlanT()
     _check("moe_adamw_plan", _lib.moe_adamw_plan(array, len(tensors), host.data_ptr(), size, ctypes.byref(plan)))
-    table = host.to("cuda" if device is None else device)
+    table = host.to(device)
     torch.cuda.current_stream(table.device).synchronize()
     plan.table = table.data_ptr()
     return _keep(plan, table, tensors)

@@ -15,7 +15,7 @@ namespace moe {
 
 struct AdamwHyper {
   float beta1, c1, beta2, c2, eps, step_size, root_scale, shrink, grad_scale;
-  bool exact_root;             // an eps so small that denormal roots count
+  bool exact_root;             // an eps so small that roots of denormals count (1.1e-19 at most: 2^-26 of 1e-11)
   double beta1d, c1d, beta2d, c2d;   // 64-bit forms; c1d and c2d take the gradient's factor in
 };
 
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(256, 4) void adamw_kernel(AdamwArgs a, const AdamwC
   h.beta2 = (float)a.beta2;
   h.c2 = (float)(1.0 - a.beta2);
   h.eps = (float)a.eps;
-  h.exact_root = a.eps < 1e-15;
+  h.exact_root = a.eps < 1e-11;
   h.root_scale = (float)(1.0 / bias2);
   h.grad_scale = gs;
   AdamwChunk next = chunks[first_chunk + blockIdx.x];   // (a workgroup has one chunk at least)

@@ -921,6 +921,7 @@ static moe_status_t check_lora(int T, const int32_t* src, const moe_groups_t* gr
   const long long x_ld = lora->x_ld ? lora->x_ld : lora->K, y_ld = lora->y_ld ? lora->y_ld : lora->N;
   if (x_ld < lora->K || x_ld % 8 != 0 || x_ld > (1LL << 32) || y_ld < lora->N || y_ld % 8 != 0 || y_ld > (1LL << 32))
     return MOE_ERR_SHAPE;
+  if (std::max(x_ld, y_ld) * T > (1LL << 48)) return MOE_ERR_SHAPE;   // more than memory has addresses for
   if (!aligned16(lora->A) || !aligned16(lora->B) || !aligned4(lora->scale) || !aligned4(src)) return MOE_ERR_ALIGN;
   out->g = {groups->counts, groups->E, groups->M_cap, groups->offsets_out, groups->status_out, src, T};
   out->A = static_cast<const uint16_t*>(lora->A);
@@ -1011,7 +1012,7 @@ static moe_status_t check_adamw_tensor(const moe_adamw_tensor_t& t) {
 // bits: 17.1 and 15.0; 531M: 3.10 ms and 3.14).
 static int adamw_chunk(const moe_adamw_tensor_t* tensors, int n_tensors) {
   long long total = 0;
-  for (int i = 0; i < n_tensors; ++i) total += tensors[i].n;
+  for (int i = 0; i < n_tensors && total < (4 << 20); ++i) total += tensors[i].n;   // (each is 2^42 at most)
   return total < (4 << 20) ? 2 * kAdamwStep : 4 * kAdamwStep;
 }
 static long long adamw_chunks(const moe_adamw_tensor_t& t, int chunk) { return (t.n + chunk - 1) / chunk; }
@@ -1182,7 +1183,9 @@ moe_status_t moe_grad_norm(const moe_adamw_plan_t* plan, float max_norm, float* 
   if (!out || !workspace) return MOE_ERR_NULL;
   if (workspace_bytes < moe_grad_norm_workspace_bytes() || !(max_norm > 0.0f)) return MOE_ERR_SHAPE;
   if (!aligned4(out) || !aligned16(workspace)) return MOE_ERR_ALIGN;
-  if (overlap({{out, 8}, {workspace, moe_grad_norm_workspace_bytes()}}, {})) return MOE_ERR_UNSUPPORTED;
+  if (overlap({{out, 8}, {workspace, moe_grad_norm_workspace_bytes()}},
+              {{plan->table, (size_t)plan->n_chunks * sizeof(AdamwChunk)}}))
+    return MOE_ERR_UNSUPPORTED;
   int cus;
   if ((st = ensure_init(&cus)) != MOE_OK) return st;
   return launch_grad_norm(static_cast<const AdamwChunk*>(plan->table), plan->n_chunks, max_norm, out,

@@ -580,7 +580,8 @@ moe_status_t moe_pack_weight_mxfp4(const void* src, int E, int N, int K, int src
  * x_ld, y_ld: elements from one row of x (and dx) and of y (base, dy) to the
  * next, 0 = K and N; more than that for columns of a wider matrix.  Requires r
  * % 8 == 0, 8 <= r <= 128, K and N % 8 == 0, 8 <= K, N <= 2^17, x_ld >= K and
- * y_ld >= N multiples of 8.  (host struct) */
+ * y_ld >= N multiples of 8, x_ld and y_ld <= 2^32 and T rows of them within
+ * 2^48 elements.  (host struct) */
 typedef struct {
   const void* A;
   const void* B;
@@ -597,10 +598,11 @@ typedef struct {
  * group holds, and grouped rows whose src lies outside [0, T), are left as they
  * were.  u: fp32 [M_cap][r] or NULL, kept for the backward pass (0 in rows whose
  * src lies outside).  All sums are fp32; the product with B takes u to 2^-17 of
- * its value.  workspace: moe_lora_fwd_workspace_bytes(M_cap, E, r, K, N) bytes (0
- * where one launch does it: few rows of a small adapter; then NULL will do),
- * 16-byte aligned, contents of no meaning before or after; calls that may run at
- * the same time, replays of captured ones too, need one each.  Requires M_cap <=
+ * its value, in two parts, so that an infinity of B may give NaN.  workspace:
+ * moe_lora_fwd_workspace_bytes(M_cap, E, r, K, N) bytes (0 where one launch does
+ * it: few rows of a small adapter; then NULL will do), 16-byte aligned, contents
+ * of no meaning before or after; calls that may run at the same time, replays of
+ * captured ones too, need one each.  Requires M_cap <=
  * 2^25; x, A, B, base, y, u 16-byte, src and scale 4-byte aligned.  T = 0 does
  * nothing but report the groups. */
 size_t moe_lora_fwd_workspace_bytes(int M_cap, int E, int r, int K, int N);
@@ -615,7 +617,8 @@ moe_status_t moe_lora_fwd(const void* x, int T, const int32_t* src, const moe_gr
  *   dB_e = scale_e sum_i dy_i u_i^T                 fp32 [E][N][r], nullable
  * dy has y's row distance, dx and dx_base x's.  accumulate = 1 adds to dA and
  * dB; 0 writes them (0 for a group without rows; T = 0 too).  x is needed for dA
- * only, u for dB only.  Sums are fp32, in a fixed order.  The workspace (of
+ * only, u for dB only.  Sums are fp32, in a fixed order; an infinity of A (for
+ * dx), of x (for dA) or of dy (for dB) may give NaN.  The workspace (of
  * moe_lora_bwd_workspace_bytes) and the rest as above; rows of dx that no group
  * holds are left as they were. */
 size_t moe_lora_bwd_workspace_bytes(int M_cap, int E, int r, int K, int N);

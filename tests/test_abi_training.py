@@ -49,6 +49,7 @@ def test_lora_refusals():
             assert call(lo=_lora(G, **bad)) == SHAPE, bad
         assert call(lo=_lora(G, A=F + 8)) == ALIGN and call(lo=_lora(G, B=F + 2)) == ALIGN
         assert call(lo=_lora(G, scale=F + 2)) == ALIGN and call(src=F + 2) == ALIGN
+        assert call(T=1 << 20, lo=_lora(G, x_ld=(1 << 28) + 8)) == call(T=1 << 20, lo=_lora(G, y_ld=(1 << 28) + 8)) == SHAPE
         assert call(T=-1) == SHAPE and call(ws=NULL) == NULL_ and call(ws=9 * F + 8) == ALIGN
     assert fwd(x=NULL) == NULL_ and fwd(y=NULL) == NULL_
     assert fwd(x=4 * F + 2) == ALIGN and fwd(y=7 * F + 8) == ALIGN and fwd(base=6 * F + 8) == ALIGN and fwd(u=8 * F + 4) == ALIGN
@@ -206,6 +207,9 @@ def test_plan_table():
     st, plan, _, size = _plan(G, [_tensor(G, grad=64 * F, m=128 * F, v=192 * F, n=(1 << 22) + 1)])
     assert st == OK and plan.n_chunks == 1025 and plan.n_chunks8 == 0 and size == each * 1025
     bad = (G.AdamwTensorT * 1)(_tensor(G, n=-5))
+    # the largest sizes
+    huge = (G.AdamwTensorT * 5)(*[_tensor(G, n=1 << 42)] * 5)
+    assert G._lib.moe_adamw_plan_bytes(huge, 5) == 5 * each << 30
     assert G._lib.moe_adamw_plan_bytes(bad, 1) == 0 and G._lib.moe_adamw_plan_bytes(None, 3) == 0
 
 
@@ -229,6 +233,7 @@ def test_step_refusals():
         return G.raw_call("moe_grad_norm", B(plan or G.AdamwPlanT(F, 1)), most, out, ws, n, NULL)
     assert norm(plan=G.AdamwPlanT(None, 1)) == NULL_ and norm(out=NULL) == NULL_ and norm(ws=NULL) == NULL_
     assert norm(most=0.0) == SHAPE and norm(most=-1.0) == SHAPE and norm(most=math.nan) == SHAPE
+    assert norm(out=F) == UNSUP and norm(ws=F) == UNSUP and norm(ws=2 * F, out=2 * F + 8) == UNSUP
     assert norm(n=G.moe_grad_norm_workspace_bytes() - 1) == SHAPE and norm(out=2 * F + 2) == ALIGN and norm(ws=3 * F + 8) == ALIGN
     assert norm(out=3 * F + 8) == UNSUP
     assert G.raw_call("moe_grad_norm", NULL, 1.0, F, 2 * F, BIG, NULL) == NULL_
@@ -263,8 +268,11 @@ def test_binding_checks():
             G.adamw_tensor(**{**dict(param=t(5), grad=t(5), m=t(5), v=t(5)), **bad})
     with pytest.raises(ValueError):
         G.adamw_tensor(t(10)[::2], t(5), t(5), t(5))
+    with pytest.raises(ValueError):
+        G.adamw_plan([G.adamw_tensor(t(5), t(5), t(5), t(5))])        # not on a GPU
     for bad in (dict(m=t(5, torch.int8)), dict(grad=t(5, torch.float16)), dict(param=t(5, torch.float16)),
-                dict(master=t(5, torch.bfloat16), param=t(5, torch.bfloat16))):
+                dict(master=t(5, torch.bfloat16), param=t(5, torch.bfloat16)),
+                dict(m=t(5, torch.int8), v=t(5, torch.uint8), m_scale=t(1), v_scale=t(1, torch.float64))):
         with pytest.raises(TypeError):
             G.adamw_tensor(**{**dict(param=t(5), grad=t(5), m=t(5), v=t(5)), **bad})
 

@@ -230,6 +230,28 @@ def test_large_and_small_values(G):  # noqa: F811
         assert np.array_equal(to_host(t.d["m_scale"]), ms) and np.array_equal(to_host(t.d["v_scale"]), vs)
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-18, 1e-15, 1e-12])
+def test_small_roots(G, eps):  # noqa: F811
+    """Second moments below fp32's normal numbers, beside an eps that they still change (v' keeps 10 bits there, its
+    root 2^-11 of an eighth of eps or less; with eps 0 they are normal)."""
+    import torch
+    std = 1e-19 if eps else 1e-16
+    t = Tensor(G, 10, 1000, "fp32", fresh=True)
+    t.h["param"][:] = 0
+    t.h["grad"] = (np.sign(t.h["grad"]) * (std + np.abs(t.h["grad"]) * std)).astype(np.float32)
+    t.d["param"].zero_()
+    t.d["grad"].copy_(torch.from_numpy(t.h["grad"]))
+    G.moe_adamw_step(G.adamw_plan([t.struct]), G.adamw(**{**HYPER, "eps": eps}))
+    torch.cuda.synchronize()
+    v = 0.01 * t.f64("grad") ** 2 / (1 - 0.99 ** 7)
+    if 0 < eps <= 1e-18:                       # what v' loses below 2^-126: half of 2^-149
+        got, m = to_host(t.d["param"]), 0.1 * t.f64("grad") / (1 - 0.9 ** 7)
+        want = -2e-3 * m / (np.sqrt(v) + eps)
+        assert np.all(np.abs(got - want) <= (24 * U + 2.0 ** -150 / (0.01 * t.f64("grad") ** 2)) * np.abs(want))
+    else:
+        t.check({"eps": eps})
+
+
 @pytest.mark.parametrize("n", [0, 1, 5, 127, 128, 130, 1000, 5000])
 def test_unpack(G, n):  # noqa: F811
     import torch

@@ -196,6 +196,8 @@ CASES = {
     "many small groups, rank 24": ([17, 3, 64, 65, 0, 30, 1, 20, 70, 66, 100, 128] * 4, 2300, 24, 136, 520),
     "few rows, long": ([3, 0, 9, 16, 1, 17], 50, 16, 7168, 264),
     "few rows, long, rank 24": ([1, 0, 2, 5], 9, 24, 2888, 776),
+    "one launch, rank 128": ([7, 30, 1, 0, 16], 60, 128, 512, 520),
+    "one launch, rank 72": ([1, 17], 18, 72, 904, 264),
     "few rows, rank 128": ([7, 30, 1], 40, 128, 1032, 136),
     "one row in 100 groups, long": ([1] * 100, 100, 8, 8200, 72),
     "a tile more than one launch takes": ([2040], 2040, 8, 264, 136),
