@@ -1,4 +1,6 @@
 // Launchers of the adapter kernels.
+#include <algorithm>
+
 #include "internal.hpp"
 #include "lora.hpp"
 
@@ -20,17 +22,31 @@ int slice_of(int cols, int tiles, int target) {
   const int n = target / (tiles > 0 ? tiles : 1);
   return div_up(div_up(cols, n > 0 ? n : 1), 128) * 128;
 }
-int narrow_slice(const LoraShape& s, int K) { return slice_of(K, tile_guess(s.M_cap, s.L, 64 * narrow_blocks(s)), 640); }
+// About 640 workgroups, in 8 slices at most, which every workgroup of the wide kernel adds
+// up (us of the two kernels, N 4096: 256 rows, r 64, K 7168: 56 slices 6.9 + 21.2, 24 6.8 +
+// 12.7, 8 11.4 + 9.8; 4096 rows, r 8, K 7168: 19 slices 20.2 + 19.5, 8 20.2 + 16.6; 2048 rows,
+// r 64, K and N 2880: 23 slices 9.5 + 18.6, 8 10.1 + 15.4).
+int narrow_slice(const LoraShape& s, int K) {
+  const int most = div_up(div_up(K, 8), 128) * 128;
+  return std::max(most, slice_of(K, tile_guess(s.M_cap, s.L, 64 * narrow_blocks(s)), 640));
+}
+// About 832 workgroups (512 of the larger LDS of r > 64), of three steps at least where
+// there are tiles enough (2048 rows in 64 groups, r 16, N 2880: slices of 128 columns 12.7
+// us, 384 10.2, 512 11.3; 256 rows, r 64, N 4096: 9.8, 12.3, 14.2; 16384 rows, r 64, N 4096:
+// 3 slices 53.8, 2 61.5, 4 64.7).
 int wide_slice(const LoraShape& s, int N) {
-  return slice_of(N, tile_guess(s.M_cap, s.L, 64), s.r > 64 ? 512 : 832);
+  const int tiles = tile_guess(s.M_cap, s.L, 64);
+  return std::max(tiles < 32 ? 128 : 384, slice_of(N, tiles, s.r > 64 ? 512 : 832));
 }
 size_t partial_bytes(const LoraShape& s, int K) {
   return aligned((size_t)div_up(K, narrow_slice(s, K)) * (size_t)s.M_cap * (size_t)s.r * 4);
 }
 int sum_blocks(int r, int C) { return div_up(C, r <= 64 ? 512 : 256); }
-// Rows per workgroup of the sums, a multiple of 64, for about 512 workgroups.
+// Rows per workgroup of the sums, a multiple of 64, for about 448 workgroups beside the
+// groups' last pieces; two or three run on a compute unit (16384 rows, K 7168, N 4096, 32
+// groups of r 32: 320 142 us, 448 127, 512 130; 8 groups of r 64: 122, 120, 142).
 int sum_piece(const LoraShape& s) {
-  const long long p = (long long)s.M_cap * (sum_blocks(s.r, s.K) + sum_blocks(s.r, s.N)) / 512;
+  const long long p = (long long)s.M_cap * (sum_blocks(s.r, s.K) + sum_blocks(s.r, s.N)) / 448;
   return p <= 128 ? 128 : p >= kLoraPiece ? kLoraPiece : div_up(p, 64) * 64;
 }
 // Groups of more rows than a piece, at most, and their pieces: ceil(m / p) <= m / p + 1.
@@ -160,15 +176,15 @@ moe_status_t launch_lora_bwd(const LoraArgs& a, const uint16_t* dy, const uint16
   char* base = static_cast<char*>(ws);
   float* w = reinterpret_cast<float*>(base + l.w);
   const int piece = sum_piece(s);
-  const LoraSum sa = {w, x, a.x_ld, a.K, dA, reinterpret_cast<float*>(base + l.sumA), 0};
-  const LoraSum sb = {u, dy, a.y_ld, a.N, dB, reinterpret_cast<float*>(base + l.sumB), 1};
+  const LoraSum sa = {w, x, a.x_ld, a.K, dA, reinterpret_cast<float*>(base + l.sumA)};
+  const LoraSum sb = {u, dy, a.y_ld, a.N, dB, reinterpret_cast<float*>(base + l.sumB)};
   const auto sums = [&](bool wa, bool wb) {
     const int na = wa ? sum_blocks(s.r, a.K) : 0, nb = wb ? sum_blocks(s.r, a.N) : 0;
     if (na + nb == 0) return;
-    const dim3 grid((unsigned)(s.M_cap / piece + s.L), (unsigned)(na + nb));
+    const dim3 grid((unsigned)((s.M_cap / piece + s.L) * (na + nb)));
     for_rank_blocks(s.r, [&](auto n) {
       constexpr int RB = decltype(n)::value;
-      hipLaunchKernelGGL((lora_sum_kernel<RB, RB <= 4 ? 8 : 4>), grid, dim3(256), 0, st, a.g, sa, sb, na, a.scale, s.r,
+      hipLaunchKernelGGL((lora_sum_kernel<RB, RB <= 4 ? 8 : 4>), grid, dim3(256), 0, st, a.g, sa, sb, na, na + nb, a.scale, s.r,
                          piece, accumulate);
     });
   };

@@ -477,14 +477,48 @@ __global__ __launch_bounds__(256, KS <= 4 ? 3 : 2) void lora_wide_kernel(LoraGro
   u32x4 ba[4], bb[4];
   load_base(n_begin, ba);
   const float s = scale ? scale[t.e] : 1.0f;
+  // the slices' sums of the tile, a thread taking every 256th four of its values, through
+  // LDS: each wave adding up its own fragments reads everything twice, in KS loops one
+  // after the other (2048 rows, r 64, K and N 2880, 23 slices: 70.5 us; so 21.4)
   bf16x8 uv[KS];
   {
-    const int at = wave_row + row16;
-    const long long p = (long long)(t.row + at) * r;
+    float* us = reinterpret_cast<float*>(ws);
+    constexpr int ULD = RP + 4, AT_ONCE = KS >= 8 ? 1 : 8 / KS;
+    const long long len = (long long)g.M_cap * r;
+    const float* p = u_in + (long long)t.row * r;
+    const int n = t.rows * r;                    // >= 8
+    int at[KS];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) at[k] = min(4 * (tid + 256 * k), n - 4);
+    f32x4 v[KS] = {};
+    int i = 0;
+    for (; i + AT_ONCE <= slices; i += AT_ONCE) {
+      f32x4 w[AT_ONCE][KS];
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j)
+#pragma unroll
+        for (int k = 0; k < KS; ++k) w[j][k] = *reinterpret_cast<const f32x4*>(p + (i + j) * len + at[k]);
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j)
+#pragma unroll
+        for (int k = 0; k < KS; ++k) v[k] += w[j][k];
+    }
+    for (; i < slices; ++i)
+#pragma unroll
+      for (int k = 0; k < KS; ++k) v[k] += *reinterpret_cast<const f32x4*>(p + i * len + at[k]);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const int row = at[k] / r;
+      if (4 * (tid + 256 * k) < n) {
+        *reinterpret_cast<f32x4*>(us + row * ULD + (at[k] - row * r)) = v[k];
+        if (u_out && blockIdx.y == 0) *reinterpret_cast<f32x4*>(u_out + (long long)t.row * r + at[k]) = v[k];
+      }
+    }
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < KS; ++k)
-      uv[k] = u_fragment(u_in + p, (long long)g.M_cap * r, slices, r, 8 * (4 * k + q), s, at < t.rows,
-                         u_out && blockIdx.y == 0 ? u_out + p : nullptr);
+      uv[k] = u_fragment(us + (wave_row + row16) * ULD, 0, 1, r, 8 * (4 * k + q), s, wave_row + row16 < t.rows, nullptr);
+    __syncthreads();
   }
   int from[KS];           // this lane's place in a weight row at each step; -1: past both parts
 #pragma unroll
@@ -744,42 +778,42 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint1
 // ---------------------------------------------------------------- dA, dB
 // The sums over a group's rows of (s u_i) v_i^T, u fp32 [M_cap][r], v bf16 rows of
 // C columns: dA from w and x, dB from u and dy.  A piece of a group's rows and 64 CW
-// columns per workgroup, 16 CW for each wave, 32 rows at a time.  The MFMA wants
-// eight rows of one column per lane where memory has columns side by side: a lane
-// loads CW columns of its eight rows and takes them apart with byte permutations,
-// one MFMA for each (CW 8, 4 where eight ranks' sums would not fit the registers).  u goes in as three bf16 parts, 24 bits of it,
-// so that the sums are those of fp32 products; the parts of 32 rows are made once
-// for the four waves, in LDS (two stages).
+// columns per workgroup, 16 CW for each wave, 32 rows at a time, the next ones on their
+// way.  The MFMA wants eight rows of one column per lane where memory has columns side
+// by side: a wave puts its rows into a piece of LDS of its own and reads them crosswise.
+// u goes in as three bf16 parts, 24 bits of it, so that the sums are those of fp32
+// products; the parts of 32 rows are made once for the four waves, in LDS (two stages).
+// The operand that comes first gives a lane four consecutive places of the product: the
+// columns for [r][C], the ranks for [C][r].
 struct LoraSum {
   const float* u;
   const uint16_t* v;
   long long v_ld;
   int C;
-  float* out;        // [L][r][C], or [L][C][r] with turned
+  float* out;        // [L][r][C], or [L][C][r] for dB
   float* part;       // [slots][r][C] likewise, of groups of more than one piece
-  int turned;
 };
-constexpr int kLoraPiece = 2048;   // rows of a piece, at most
+constexpr int kLoraPiece = 1024;   // rows of a piece, at most
+
+// The parts of u: rank k of one of them holds 32 rows, 16-byte piece c at c ^ (k / 4).
+__device__ __forceinline__ int lora_part(int k, int c) { return 32 * k + 8 * (c ^ (k >> 2 & 3)); }
 
 template <int RB, int CW>
-__global__ __launch_bounds__(256, RB <= 2 ? 2 : 1) void lora_sum_kernel(LoraGroups g, LoraSum a, LoraSum b, int a_blocks,
-                                                       const float* __restrict__ scale, int r, int piece,
-                                                       int accumulate) {
-  constexpr int RP = 16 * RB, LD = 40, PART = RP * LD, STAGE = 3 * PART;
-  __shared__ __attribute__((aligned(16))) int rows[kLoraPiece + 32];
-  __shared__ __attribute__((aligned(16))) uint16_t us[2 * STAGE];
+struct LoraSumLds {
+  static constexpr int XLD = 16 * CW + 16;       // four rows of 32 bytes, read crosswise, in different banks
+  int rows[kLoraPiece + 32];
+  alignas(16) uint16_t us[2 * 3 * 16 * RB * 32], xs[4 * 32 * XLD];
+};
+template <int RB, int CW, bool TURNED>
+__device__ __forceinline__ void lora_sum(const LoraTile& t, const LoraGroups& g, const LoraSum& p, int block, float s, int r,
+                                         int accumulate, LoraSumLds<RB, CW>& lds) {
+  constexpr int RP = 16 * RB, PART = RP * 32, STAGE = 3 * PART, XLD = LoraSumLds<RB, CW>::XLD;
+  constexpr int KT = 16 * CW, PIECES = KT / 8, RL = 64 / PIECES, NL = 32 / RL;   // RL rows a load, NL loads
+  int* rows = lds.rows;
+  uint16_t *us = lds.us, *xs = lds.xs;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int row16 = lane & 15, q = lane >> 4;
-  const LoraTile t = lora_piece(g, piece, accumulate ? 0 : 1, blockIdx.x);
-  if (t.e < 0) return;
-  const bool first = (int)blockIdx.y < a_blocks;
-  const float* u = first ? a.u : b.u;
-  const uint16_t* vp = first ? a.v : b.v;
-  const long long v_ld = first ? a.v_ld : b.v_ld;
-  const int C = first ? a.C : b.C;
-  const int c = ((first ? blockIdx.y : blockIdx.y - a_blocks) * 64 + 16 * wave + row16) * CW;
-  const bool col_in = c < C;                     // C is a multiple of 8
-  const float s = scale ? scale[t.e] : 1.0f;
+  const int C = p.C, c0 = block * (4 * KT) + KT * wave;
   for (int i = tid; i < t.rows + 32; i += 256) rows[i] = lora_row(g, t.row + i, i < t.rows);
   __syncthreads();
   // thread: value ri of row pairs
@@ -791,111 +825,128 @@ __global__ __launch_bounds__(256, RB <= 2 ? 2 : 1) void lora_sum_kernel(LoraGrou
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int at = min(i0 + 2 * (pair0 + k * (256 / RP)) + h, t.rows - 1);
-        uv[k][h] = u[(long long)(t.row + at) * r + min(ri, r - 1)];
+        uv[k][h] = p.u[(long long)(t.row + at) * r + min(ri, r - 1)];
       }
   };
   const auto store_u = [&](int stage, int i0) {
-    uint16_t* d = us + stage * STAGE + ri * LD;
 #pragma unroll
     for (int k = 0; k < RB; ++k) {
-      const int at = i0 + 2 * (pair0 + k * (256 / RP));
+      const int pair = pair0 + k * (256 / RP), at = i0 + 2 * pair;
       const float v0 = rows[at] >= 0 ? s * uv[k][0] : 0.0f, v1 = rows[at + 1] >= 0 ? s * uv[k][1] : 0.0f;
       const float r0 = rest_of(v0), r1 = rest_of(v1);
-      uint32_t* o = reinterpret_cast<uint32_t*>(d) + pair0 + k * (256 / RP);
+      uint32_t* o = reinterpret_cast<uint32_t*>(us + stage * STAGE + lora_part(ri, pair >> 2)) + (pair & 3);
       o[0] = upper_half(v0) | upper_half(v1) << 16;
       o[PART / 2] = upper_half(r0) | upper_half(r1) << 16;
       o[PART] = pack_bf16x2(rest_of(r0), rest_of(r1));
     }
   };
-  typedef uint32_t cols_t __attribute__((ext_vector_type(CW / 2)));
-  const uint16_t* vc = vp + min(c, C - CW);
-  const auto load_v = [&](int i0, cols_t (&v)[8]) {
+  uint16_t* mine = xs + wave * (32 * XLD);
+  const int sub = lane / PIECES, piece = lane % PIECES;
+  const uint16_t* vc = p.v + min(c0 + 8 * piece, C - 8);
+  const auto load_v = [&](int i0, u32x4 (&v)[NL]) {   // (columns past the last one: their sums are dropped)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = *reinterpret_cast<const cols_t*>(vc + (long long)max(rows[min(i0, t.rows - 1) + 8 * q + i], 0) * v_ld);
+    for (int i = 0; i < NL; ++i)
+      v[i] = *reinterpret_cast<const u32x4*>(vc + (long long)max(rows[min(i0, t.rows - 1) + RL * i + sub], 0) * p.v_ld);
+  };
+  const auto store_v = [&](int i0, const u32x4 (&v)[NL]) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int row = RL * i + sub;
+      *reinterpret_cast<u32x4*>(mine + row * XLD + 8 * piece) = rows[i0 + row] >= 0 ? v[i] : u32x4{0, 0, 0, 0};
+    }
   };
   f32x4 acc[RB][CW] = {};
-  const auto compute = [&](int stage, int i0, const cols_t (&w)[8]) {
-    bf16x8 col[CW];
-    cols_t v[8];
+  const auto compute = [&](int stage) {
+    const uint16_t* d = us + stage * STAGE + lora_part(row16, q);
+    const uint16_t* c = mine + (8 * q + (row16 >> 2)) * XLD + 4 * (row16 & 3);
+    const auto column = [&](int j) { return read_crosswise(c + 16 * j, c + 16 * j + 4 * XLD); };
+    const auto part_of_u = [&](int k, int part) { return load8(d + part * PART + 16 * 32 * k); };
+    // what fewer registers hold stays over the loop, the lowest parts come first
+    if constexpr (RB <= 2) {
+      bf16x8 uf[RB][3];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = rows[i0 + 8 * q + i] >= 0 ? w[i] : cols_t(0);
+      for (int k = 0; k < RB; ++k)
 #pragma unroll
-    for (int j = 0; j < CW; ++j) {
-      u32x4 f;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) f[d] = pick16(v[2 * d][j / 2], v[2 * d + 1][j / 2], j & 1);
-      col[j] = __builtin_bit_cast(bf16x8, f);
-    }
-    const uint16_t* d = us + stage * STAGE + row16 * LD + 8 * q;
-#pragma unroll
-    for (int k = 0; k < RB; ++k)
-#pragma unroll
-      for (int part = 2; part >= 0; --part) {
-        const bf16x8 uf = load8(d + part * PART + 16 * k * LD);
-#pragma unroll
-        for (int j = 0; j < CW; ++j) acc[k][j] = mfma16(uf, col[j], acc[k][j]);
-      }
-  };
-  if (t.rows > 0) {
-    cols_t va[8], vb[8];
-    load_u(0);
-    load_v(0, va);
-    store_u(0, 0);
-    load_u(32);
-    // while 32 rows are computed: the next ones' v and the parts of u after them;
-    // true: they were the last
-    const auto step = [&](int i0, int stage, const cols_t (&v)[8], cols_t (&next)[8]) {
-      __syncthreads();
-      if (i0 + 32 >= t.rows) {                   // the same for the whole workgroup
-        compute(stage, i0, v);
-        return true;
-      }
-      store_u(stage ^ 1, i0 + 32);
-      load_u(i0 + 64);
-      load_v(i0 + 32, next);
-      compute(stage, i0, v);
-      return false;
-    };
-    for (int i0 = 0;; i0 += 64) {
-      if (step(i0, 0, va, vb)) break;
-      if (step(i0 + 32, 1, vb, va)) break;
-    }
-  }
-  if (!col_in) return;
-  const bool whole = t.pieces == 1;
-  float* o = whole ? (first ? a.out : b.out) + (long long)t.e * r * C : (first ? a.part : b.part) + (long long)t.slot * r * C;
-  const bool add = whole && accumulate;
-#pragma unroll
-  for (int k = 0; k < RB; ++k) {
-    const int rk = 16 * k + 4 * q;               // r is a multiple of 8: all four or none
-    if (rk >= r) continue;
-    if (first ? a.turned : b.turned) {
+        for (int part = 0; part < 3; ++part) uf[k][part] = part_of_u(k, part);
 #pragma unroll
       for (int j = 0; j < CW; ++j) {
-        f32x4* d = reinterpret_cast<f32x4*>(o + (long long)(c + j) * r + rk);
-        *d = add ? *d + acc[k][j] : acc[k][j];
+        const bf16x8 col = column(j);
+#pragma unroll
+        for (int part = 2; part >= 0; --part)
+#pragma unroll
+          for (int k = 0; k < RB; ++k)
+            acc[k][j] = TURNED ? mfma16(uf[k][part], col, acc[k][j]) : mfma16(col, uf[k][part], acc[k][j]);
       }
     } else {
+      bf16x8 col[CW];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < CW; ++j) col[j] = column(j);
 #pragma unroll
-        for (int j = 0; j < CW; j += 4) {
-          f32x4* d = reinterpret_cast<f32x4*>(o + (long long)(rk + i) * C + c + j);
-          const f32x4 v = {acc[k][j][i], acc[k][j + 1][i], acc[k][j + 2][i], acc[k][j + 3][i]};
-          *d = add ? *d + v : v;
+      for (int k = 0; k < RB; ++k)
+#pragma unroll
+        for (int part = 2; part >= 0; --part) {
+          const bf16x8 uf = part_of_u(k, part);
+#pragma unroll
+          for (int j = 0; j < CW; ++j)
+            acc[k][j] = TURNED ? mfma16(uf, col[j], acc[k][j]) : mfma16(col[j], uf, acc[k][j]);
         }
     }
+  };
+  if (t.rows > 0) {
+    u32x4 v[NL];
+    load_u(0);
+    load_v(0, v);
+    store_u(0, 0);
+    load_u(32);
+    for (int i0 = 0, stage = 0;; i0 += 32, stage ^= 1) {
+      store_v(i0, v);
+      load_v(i0 + 32, v);                        // while these 32 rows are computed
+      __syncthreads();
+      if (i0 + 32 < t.rows) {
+        store_u(stage ^ 1, i0 + 32);
+        load_u(i0 + 64);
+      }
+      compute(stage);
+      if (i0 + 32 >= t.rows) break;              // the same for the whole workgroup
+    }
   }
+  const bool whole = t.pieces == 1;
+  float* o = whole ? p.out + (long long)t.e * r * C : p.part + (long long)t.slot * r * C;
+  const bool add = whole && accumulate;
+#pragma unroll
+  for (int k = 0; k < RB; ++k)
+#pragma unroll
+    for (int j = 0; j < CW; ++j) {
+      // (r and C are multiples of 8: all four or none)
+      const int rk = 16 * k + (TURNED ? 4 * q : row16), c = c0 + 16 * j + (TURNED ? row16 : 4 * q);
+      if (rk >= r || c >= C) continue;
+      f32x4* d = reinterpret_cast<f32x4*>(o + (TURNED ? (long long)c * r + rk : (long long)rk * C + c));
+      *d = add ? *d + acc[k][j] : acc[k][j];
+    }
+}
+template <int RB, int CW>
+__global__ __launch_bounds__(256, RB <= 2 ? 3 : 2) void lora_sum_kernel(LoraGroups g, LoraSum a, LoraSum b, int a_blocks,
+                                                                        int blocks, const float* __restrict__ scale, int r,
+                                                                        int piece, int accumulate) {
+  __shared__ LoraSumLds<RB, CW> lds;
+  // neighbouring workgroups take the columns of the same rows, so that whole rows are on
+  // their way at once (with the pieces as neighbours r 16 takes 28 us for 29, but r 32 134
+  // for 128, r 128 166 for 150)
+  const int block = blockIdx.x % blocks;
+  const LoraTile t = lora_piece(g, piece, accumulate ? 0 : 1, blockIdx.x / blocks);
+  if (t.e < 0) return;
+  const float s = scale ? scale[t.e] : 1.0f;
+  if (block < a_blocks) lora_sum<RB, CW, false>(t, g, a, block, s, r, accumulate, lds);
+  else lora_sum<RB, CW, true>(t, g, b, block - a_blocks, s, r, accumulate, lds);
 }
 
 // The pieces of the groups that have more than one, added in their order: a
 // workgroup takes 1024 values of the blockIdx.y-th such group.
 __global__ __launch_bounds__(256) void lora_join_kernel(LoraGroups g, LoraSum a, LoraSum b, int a_blocks, int r,
                                                         int piece, int accumulate) {
+  const bool first = (int)blockIdx.x < a_blocks;
   const LoraTile t = lora_many(g, piece, blockIdx.y);
   if (t.e < 0) return;
-  const bool first = (int)blockIdx.x < a_blocks;
   const LoraSum& p = first ? a : b;
   const long long size = (long long)r * p.C;
   const long long i = 4 * ((long long)(first ? blockIdx.x : blockIdx.x - a_blocks) * 256 + threadIdx.x);
