@@ -13,7 +13,7 @@ moe_status_t launch_adamw(const AdamwArgs& a, int cus, hipStream_t s) {
   // Workgroups per compute unit, striding over the rest.  32 bits: 5 to 8 streams,
   // which more workgroups scatter over memory (531M elements: 2 3.18 ms, 3 3.13, 4
   // 3.21; 3 is 5.1 TB/s); 8 bits: its 64-bit arithmetic wants the waves (265M: 4 1.34
-  // ms, 8 0.99, of which memory takes 0.39 at the same rate).
+  // ms, 8 0.99, 4.9 TB/s).
   const auto grid = [&](long long n, int per_cu) {
     const long long most = (long long)per_cu * cus;
     return dim3((unsigned)(n < most ? n : most));
@@ -36,7 +36,7 @@ moe_status_t launch_adamw_unpack(const int8_t* m, const float* m_scale, const ui
 
 moe_status_t launch_grad_norm(const AdamwChunk* chunks, long long n_chunks, float max_norm, float* out, double* part,
                               hipStream_t s) {
-  // (531M bf16 gradients: 1024 workgroups 165 us, 6.4 TB/s; 768 the same, 512 218)
+  // (265M fp32 gradients: 1024 workgroups 165 us, 6.4 TB/s; 768 the same, 512 218)
   const int parts = (int)(n_chunks < kNormParts ? n_chunks : kNormParts);
   if (parts > 0)
     hipLaunchKernelGGL(grad_norm_kernel, dim3((unsigned)parts), dim3(256), 0, s, chunks, n_chunks, part);

@@ -145,8 +145,9 @@ moe_status_t launch_lora_fwd(const LoraArgs& a, const uint16_t* x, const uint16_
       constexpr int RB = decltype(n)::value;
       hipLaunchKernelGGL((lora_few_narrow_kernel<RB>), dim3(tiles, (unsigned)slices), dim3(256), 0, st, a.g, x, a.x_ld,
                          a.A, a.r, a.K, part);
-      hipLaunchKernelGGL((lora_few_wide_kernel<RB, RB <= 2 ? 2 : 1>), dim3(tiles, (unsigned)div_up(a.N, RB <= 2 ? 256 : 128)), dim3(256), 0, st, a.g,
-                         part, slices, part == u ? nullptr : u, a.B, a.scale, a.r, a.N, base, y, a.y_ld);
+      constexpr int NB = RB <= 2 ? 2 : 1;
+      hipLaunchKernelGGL((lora_few_wide_kernel<RB, NB>), dim3(tiles, (unsigned)div_up(a.N, 128 * NB)), dim3(256), 0, st,
+                         a.g, part, slices, part == u ? nullptr : u, a.B, a.scale, a.r, a.N, base, y, a.y_ld);
     });
     return launched();
   }

@@ -218,10 +218,16 @@ __device__ __forceinline__ bf16x8 read_crosswise(const uint16_t* rows0, const ui
 // backward's w = dy B), whose fragments are read crosswise.  The slices' sums go
 // to out + slice * M_cap * r (one slice: the result itself); the next kernel adds
 // them in that order.  Rows that src does not name get 0.
+//
+// Measured: 14746 rows, r 64, K 7168 62 us (51 where nothing else uses the memory, 4.1
+// TB/s); 16384 rows in 32 groups, r 32 69 us, 3.4 TB/s, of which a fifth is what the kernel
+// before it wrote on its way to memory; 8191 rows, r 16, K 2880 17 us, a third of it the
+// start (counts, src, the first rows).  Blocks of 256 or 512 columns gained nothing.
 template <int RB, int MB, bool TURNED>
-__global__ __launch_bounds__(256, RB <= 4 ? 2 : 1) void lora_narrow_kernel(LoraGroups g, const uint16_t* __restrict__ x, long long x_ld,
-                                                          const uint16_t* __restrict__ W, int r, int K, int slice,
-                                                          float* __restrict__ out) {
+__global__ __launch_bounds__(256, RB <= 4 ? 2 : 1) void lora_narrow_kernel(LoraGroups g, const uint16_t* __restrict__ x,
+                                                                           long long x_ld,
+                                                                           const uint16_t* __restrict__ W, int r, int K,
+                                                                           int slice, float* __restrict__ out) {
   constexpr int BM = 64 * MB, RP = 16 * RB, KT = 128;
   constexpr int LD = TURNED ? RP + 8 : KT + 8, STAGE = (TURNED ? KT : RP) * LD;
   __shared__ __attribute__((aligned(16))) uint16_t ws[2 * STAGE];
@@ -410,11 +416,17 @@ __device__ __forceinline__ uint32_t pick16(uint32_t lo, uint32_t hi, bool upper)
 // = w A) taken apart by byte permutations.  Column 8 i + j of a step lies in row 16
 // j + i of LDS: MFMA j then gives a lane column j of its eight, so that 16 lanes
 // load and store 256 bytes of a row.
+//
+// Measured: 14746 rows, r 64, N 4096 54 us, 4.4 TB/s; 16384 rows in 32 groups, r 32, N 7168
+// (dx) 103 us, 4.5 TB/s; 8191 rows, r 16, N 5760 39 us, 4.8 TB/s.  Tiles of 32 rows per wave
+// spill at r 128; the weights turned by a kernel of their own cost 9 us more than they save.
 template <int KS, bool TURNED>
-__global__ __launch_bounds__(256, KS <= 4 ? 3 : 2) void lora_wide_kernel(LoraGroups g, const float* __restrict__ u_in, int slices,
-                                                        float* __restrict__ u_out, const uint16_t* __restrict__ W,
-                                                        const float* __restrict__ scale, int r, int N, int slice,
-                                                        const uint16_t* base, uint16_t* y, long long y_ld) {
+__global__ __launch_bounds__(256, KS <= 4 ? 3 : 2) void lora_wide_kernel(LoraGroups g, const float* __restrict__ u_in,
+                                                                         int slices, float* __restrict__ u_out,
+                                                                         const uint16_t* __restrict__ W,
+                                                                         const float* __restrict__ scale, int r, int N,
+                                                                         int slice, const uint16_t* base, uint16_t* y,
+                                                                         long long y_ld) {
   constexpr int BM = 64, RP = 16 * KS, NT = 128, LD = RP + 8, STAGE = NT * LD;
   __shared__ __attribute__((aligned(16))) uint16_t ws[2 * STAGE];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -568,7 +580,8 @@ __global__ __launch_bounds__(256, KS <= 4 ? 3 : 2) void lora_wide_kernel(LoraGro
 // The same two products for a decoding batch, where what counts is how soon every
 // weight is on its way: tiles of 16 rows whose operands go straight from memory to
 // the MFMA.  The narrow one: 512 columns of K per workgroup, whose four waves' sums
-// meet in LDS.
+// meet in LDS.  Measured: 1 row, r 16, K 7168, N 4096 3.6 and 5.1 us for the wide one,
+// beside 3.2 us of the host for each launch.
 template <int RB>
 __global__ __launch_bounds__(256) void lora_few_narrow_kernel(LoraGroups g, const uint16_t* __restrict__ x,
                                                               long long x_ld, const uint16_t* __restrict__ A, int r,
@@ -674,7 +687,9 @@ __global__ __launch_bounds__(256) void lora_few_wide_kernel(LoraGroups g, const 
 
 // Both products in one launch where an adapter's A is small: each workgroup of a
 // tile computes the whole u (its eight waves take runs of 64 columns of K in turn),
-// then a slice of y's columns, 32 at a time for each wave.
+// then a slice of y's columns, 32 at a time for each wave.  Measured: 58 rows in 32 groups,
+// r 16, K 2880, N 5760 9.6 us for 10.5 MB: the products one after the other, each a trip to
+// memory (two to six runs of columns at once: 9.6 to 11.4).
 template <int RB>
 __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint16_t* __restrict__ x, long long x_ld,
                                                        const uint16_t* __restrict__ A, const uint16_t* __restrict__ B,
@@ -785,6 +800,13 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint1
 // products; the parts of 32 rows are made once for the four waves, in LDS (two stages).
 // The operand that comes first gives a lane four consecutive places of the product: the
 // columns for [r][C], the ranks for [C][r].
+//
+// Measured (K 7168, N 4096): 8191 rows, r 16, K 2880, N 5760 30 us, 4.8 TB/s; 16384 rows in
+// 32 groups, r 32 127 us, 2.9 TB/s beside 235 MB of dx that go to memory meanwhile; 14746
+// rows, r 64 120 us.  With the rows in registers, taken apart there, r 32 took 119 and r 16
+// 28, but r 64 178 and r 128 197 for 152.  dB in the pass that makes w (dy read once, two
+// barriers a step): all of the backward 263 for 279 us at r 32, 85 for 83 at r 16, 271 for
+// 264 at r 64.
 struct LoraSum {
   const float* u;
   const uint16_t* v;
