@@ -57,14 +57,19 @@ int many_groups(const LoraShape& s) {
 size_t sum_slots(const LoraShape& s) { return (size_t)(s.M_cap / sum_piece(s)) + (size_t)many_groups(s); }
 // Whether one launch does both products of the forward: every workgroup of a tile
 // reads the whole A, which pays while that is short beside a launch (3.2 us on the
-// host).  Two launches against one, N 4096: 1 row, r 16: K 512 9.5 / 7.0 us, K 2880 9.5 /
-// 6.9, K 7168 9.2 / 10.9; r 64: K 512 9.5 / 7.7, K 1024 10.1 / 9.6; 64 rows in 32 groups,
-// r 16: K 2880 9.3 / 8.7, K 7168 9.9 / 14.7; r 32, K 2880 11.4 / 12.4; and N 2880, 4 groups,
-// r 16, K 2880: 1024 rows 16.3 / 11.6, 4096 22.7 / 24.9; r 64, K 512: 1024 rows 20.3 / 15.6,
-// 4096 35.2 / 52.4.
-bool fused_rows(const LoraShape& s) { return s.r * s.K <= (1 << 16) && tile_bound(s.M_cap, s.L, 16) <= 128; }
-// Else, whether it goes by tiles of 16 rows (64 rows in 32 groups, r 16, K 2880, N 5760:
-// 9.6 us; 2048 rows in 64 groups, K and N 2880: 30.5 us, with tiles of 64 rows 22.3).
+// host) and the tiles leave more than one workgroup for few compute units alone; the LDS
+// of a larger r holds one or two workgroups on each.  Us of two launches against one, N
+// 4096: 1 row, r 16: K 2880 9.5 / 5.9, K 7168 9.3 / 7.8, K 16384 9.6 / 13.0; r 32, K 4096 9.6
+// / 7.8; r 64, K 2048 10.3 / 9.2; 64 rows in 32 groups, r 128, K 1024 29.2 / 21.8; 1024 rows
+// in 4 groups (68 tiles): r 16, K 7168 18.0 / 13.3; r 64, K 2048 21.8 / 21.1; r 128, K 1024
+// 29.1 / 33.5; 3000 rows in 8 groups (195): r 16, K 2880 20.0 / 17.4; r 32 24.1 / 23.3; r 64,
+// K 1024 28.1 / 40.0; 4096 rows (264), r 16, K 2880 23.3 / 27.3.
+bool fused_rows(const LoraShape& s) {
+  const unsigned most = s.r <= 32 ? 256 : s.r <= 64 ? 128 : 64;
+  return s.r * s.K <= (1 << 17) && tile_bound(s.M_cap, s.L, 16) <= most;
+}
+// Else, whether it goes by tiles of 16 rows (2048 rows in 64 groups, r 16, K and N 2880: 30.5
+// us, with tiles of 64 rows 22.3).
 bool few_rows(const LoraShape& s) { return s.M_cap <= 64 || s.M_cap <= 4LL * s.L; }
 
 template <typename F>
@@ -131,10 +136,20 @@ moe_status_t launch_lora_fwd(const LoraArgs& a, const uint16_t* x, const uint16_
   if (a.g.M_cap == 0 || a.g.T == 0) return report(a.g, st);
   const unsigned tiles = tile_bound(s.M_cap, s.L, 16);
   if (fused_rows(s)) {
-    const int slice = div_up(div_up(a.N, (int)(256 / tiles)), 256) * 256;   // (128 tiles at most)
+    // columns for 256 workgroups (512: 64 rows in 32 groups 9.4 us for 7.4); where there are
+    // more than eight waves take at once, they take two runs at a time
+    const int slice = div_up(div_up(a.N, (int)(256 / tiles)), 256) * 256;
+    const dim3 grid(tiles, (unsigned)div_up(a.N, slice));
+    const auto go = [&](auto rb, auto nb) {
+      constexpr int RB = decltype(rb)::value, NB = decltype(nb)::value;
+      hipLaunchKernelGGL((lora_few_kernel<RB, RB <= 2 ? 2 : 1, NB>), grid, dim3(512), 0, st, a.g, x, a.x_ld, a.A, a.B,
+                         a.scale, a.r, a.K, a.N, slice, base, y, a.y_ld, u);
+    };
     for_rank_blocks(s.r, [&](auto n) {
-      hipLaunchKernelGGL((lora_few_kernel<decltype(n)::value>), dim3(tiles, (unsigned)div_up(a.N, slice)), dim3(512), 0, st,
-                         a.g, x, a.x_ld, a.A, a.B, a.scale, a.r, a.K, a.N, slice, base, y, a.y_ld, u);
+      if constexpr (decltype(n)::value <= 2) {
+        if (slice > 256) return go(n, std::integral_constant<int, 2>{});
+      }
+      go(n, std::integral_constant<int, 1>{});
     });
     return launched();
   }

@@ -686,18 +686,22 @@ __global__ __launch_bounds__(256) void lora_few_wide_kernel(LoraGroups g, const 
 }
 
 // Both products in one launch where an adapter's A is small: each workgroup of a
-// tile computes the whole u (its eight waves take runs of 64 columns of K in turn),
-// then a slice of y's columns, 32 at a time for each wave.  Measured: 58 rows in 32 groups,
-// r 16, K 2880, N 5760 9.6 us for 10.5 MB: the products one after the other, each a trip to
-// memory (two to six runs of columns at once: 9.6 to 11.4).
-template <int RB>
+// tile computes the whole u (its eight waves take runs of 64 columns of K in turn,
+// AT_ONCE of them on their way), then a slice of y's columns, NB runs of 32 at a time
+// for each wave.  Measured: 58 rows in 32 groups, r 16, K 2880, N 5760 7.4 us for 10.5 MB,
+// 1 row, K 7168, N 4096 8.4: the products one after the other, each a few trips to memory
+// of 0.7 us (A and x loaded as the MFMA takes them 9.6; one, three or more runs at once 8.4
+// to 9.0 at NB 1 for 8.1; y's columns one run at a time 8.0).
+template <int RB, int AT_ONCE, int NB>
 __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint16_t* __restrict__ x, long long x_ld,
                                                        const uint16_t* __restrict__ A, const uint16_t* __restrict__ B,
                                                        const float* __restrict__ scale, int r, int K, int N, int slice,
                                                        const uint16_t* base, uint16_t* y, long long y_ld,
                                                        float* __restrict__ u_out) {
   constexpr int RP = 16 * RB, LD = RP + 4, WAVES = 8;
+  constexpr int XLD = 64 + 8, ROWS = 16 * XLD;   // a wave's 64 columns of 16 rows
   __shared__ __attribute__((aligned(16))) float red[WAVES * 16 * LD];
+  __shared__ __attribute__((aligned(16))) uint16_t xs[WAVES * 2 * ROWS];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int row16 = lane & 15, q = lane >> 4;
   if (blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) lora_report(g);
@@ -711,43 +715,72 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint1
     const int c = 8 * (4 * k + q);
     from[k] = c < r ? c : c < 2 * r ? c - r : -1;
   }
-  bf16x8 bv[RB][2];
+  bf16x8 bv[NB][RB][2];
   const auto load_b = [&]() {
 #pragma unroll
-    for (int k = 0; k < RB; ++k)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int n = min(n0 + 8 * (row16 >> 2) + (row16 & 3) + 4 * j, N - 1);
-        bv[k][j] = load8(B + ((long long)t.e * N + n) * r + max(from[k], 0));
-      }
+      for (int k = 0; k < RB; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int n = min(n0 + 32 * WAVES * b + 8 * (row16 >> 2) + (row16 & 3) + 4 * j, N - 1);
+          bv[b][k][j] = load8(B + ((long long)t.e * N + n) * r + max(from[k], 0));
+        }
   };
   load_b();
   const uint16_t* Ae = A + (long long)t.e * r * K;
   const float s = scale ? scale[t.e] : 1.0f;
   const int row = lora_row(g, t.row + row16, row16 < t.rows);
-  const uint16_t* xr = x + (long long)max(row, 0) * x_ld;
+  // eight lanes load 128 bytes of a row: the MFMA's operands, of which neighbouring lanes
+  // hold different rows, come through LDS (read from memory, each of them visits 64 lines)
+  const int sub = lane >> 3, piece = lane & 7;
+  const uint16_t* xr[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) xr[i] = x + (long long)max(__shfl(row, 8 * i + sub, 64), 0) * x_ld;
+  uint16_t* mine = xs + wave * (2 * ROWS);
   const long long yo = (long long)max(row, 0) * y_ld;
-  u32x4 old = {0, 0, 0, 0};
+  u32x4 old[NB] = {};
   const auto load_base = [&]() {
-    const int n = n0 + 8 * q;
-    if (base && row >= 0 && n < n_end) old = *reinterpret_cast<const u32x4*>(base + yo + n);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int n = n0 + 32 * WAVES * b + 8 * q;
+      if (base && row >= 0 && n < n_end) old[b] = *reinterpret_cast<const u32x4*>(base + yo + n);
+    }
   };
   load_base();
   f32x4 acc[RB] = {};
-  for (int k0 = 64 * wave; k0 < K; k0 += 64 * WAVES) {
-    bf16x8 av[2][RB], xv[2];
+  for (int k0 = 64 * wave; k0 < K; k0 += 64 * WAVES * AT_ONCE) {
+    u32x4 av[AT_ONCE][RB][2], xv[AT_ONCE][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int k = min(k0 + 32 * j + 8 * q, K - 8);
+    for (int n = 0; n < AT_ONCE; ++n) {
+      const int c = min(k0 + 64 * WAVES * n + 8 * piece, K - 8);
 #pragma unroll
-      for (int b = 0; b < RB; ++b) av[j][b] = load8(Ae + (long long)min(16 * b + row16, r - 1) * K + k);
-      xv[j] = load8(xr + k);
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+          av[n][b][i] = *reinterpret_cast<const u32x4*>(Ae + (long long)min(16 * b + 8 * i + sub, r - 1) * K + c);
+        xv[n][i] = *reinterpret_cast<const u32x4*>(xr[i] + c);
+      }
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const bool in = k0 + 32 * j + 8 * q < K;
+    for (int n = 0; n < AT_ONCE; ++n) {
+      const bool in = k0 + 64 * WAVES * n + 8 * piece < K;
+      const auto turned = [&](uint16_t* lds, const u32x4 (&v)[2], bf16x8 (&f)[2]) {
 #pragma unroll
-      for (int b = 0; b < RB; ++b) acc[b] = mfma16(in ? av[j][b] : zero8(), in ? xv[j] : zero8(), acc[b]);
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<u32x4*>(lds + (8 * i + sub) * XLD + 8 * piece) = in ? v[i] : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) f[j] = load8(lds + row16 * XLD + 8 * (4 * j + q));
+      };
+      bf16x8 xf[2];
+      turned(mine, xv[n], xf);
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        bf16x8 af[2];
+        turned(mine + ROWS, av[n][b], af);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[b] = mfma16(af[j], xf[j], acc[b]);
+      }
     }
   }
   if (row < 0)
@@ -771,22 +804,30 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint1
 #pragma unroll
   for (int k = 0; k < RB; ++k) uv[k] = u_fragment(&red[row16 * LD], 0, 1, r, 8 * (4 * k + q), s, true, nullptr);
   while (n0 < n_end) {
-    f32x4 out[2] = {};
+    u32x4 w[NB];
 #pragma unroll
-    for (int k = 0; k < RB; ++k)
+    for (int b = 0; b < NB; ++b) {
+      f32x4 out[2] = {};
 #pragma unroll
-      for (int j = 0; j < 2; ++j) out[j] = mfma16(from[k] >= 0 ? bv[k][j] : zero8(), uv[k], out[j]);
-    float o[8];
+      for (int k = 0; k < RB; ++k)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = out[i >> 2][i & 3];
-    const u32x4 w = add_base(o, old);
-    const int n = n0 + 8 * q;
-    n0 += 32 * WAVES;
+        for (int j = 0; j < 2; ++j) out[j] = mfma16(from[k] >= 0 ? bv[b][k][j] : zero8(), uv[k], out[j]);
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = out[i >> 2][i & 3];
+      w[b] = add_base(o, old[b]);
+    }
+    const int n1 = n0 + 8 * q;
+    n0 += 32 * WAVES * NB;
     if (n0 < n_end) {
       load_b();
       load_base();
     }
-    if (row >= 0 && n < n_end) *reinterpret_cast<u32x4*>(y + yo + n) = w;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int n = n1 + 32 * WAVES * b;
+      if (row >= 0 && n < n_end) *reinterpret_cast<u32x4*>(y + yo + n) = w[b];
+    }
   }
 }
 

@@ -198,6 +198,11 @@ CASES = {
     "few rows, long, rank 24": ([1, 0, 2, 5], 9, 24, 2888, 776),
     "one launch, rank 128": ([7, 30, 1, 0, 16], 60, 128, 512, 520),
     "one launch, rank 72": ([1, 17], 18, 72, 904, 264),
+    "few rows, rank 16": ([1, 0, 17], 20, 16, 8200, 520),
+    "few rows, rank 24, slices": ([2, 0, 5, 1], 9, 24, 5496, 136),
+    "few rows, rank 64": ([3, 16], 21, 64, 2056, 264),
+    "one launch, 200 tiles": ([17] * 90 + [0] * 20, 1600, 16, 264, 520),
+    "one launch, rank 32": ([40, 3], 50, 32, 4096, 1032),
     "few rows, rank 128": ([7, 30, 1], 40, 128, 1032, 136),
     "one row in 100 groups, long": ([1] * 100, 100, 8, 8200, 72),
     "a tile more than one launch takes": ([2040], 2040, 8, 264, 136),
