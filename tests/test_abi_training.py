@@ -84,7 +84,7 @@ def test_lora_few_rows_need_no_workspace():
     import grouped_gemm_glu_amd as G
     B = ctypes.byref
     assert G.moe_lora_fwd_workspace_bytes(100, 4, 16, 64, 72) == 0 < G.moe_lora_fwd_workspace_bytes(100, 4, 16, 8200, 72)
-    for K, want in ((64, (OK, DEVICE)), (8192, (NULL_,))):
+    for K, want in ((64, (OK, DEVICE)), (8200, (NULL_,))):
         T = 0 if K == 64 else 100      # with rows and a device it would launch with addresses that are none
         st = G.raw_call("moe_lora_fwd", F, T, NULL, B(_groups(G, M=100)), B(_lora(G, K=K)), NULL, 7 * F, NULL, NULL, 0, NULL)
         assert st in want, (K, st)
