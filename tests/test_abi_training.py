@@ -94,7 +94,7 @@ def test_lora_overlaps():
     _no_gpu()
     import grouped_gemm_glu_amd as G
     B = ctypes.byref
-    E, M, T, r, K, N = 3, 2400, 2404, 16, 40, 56
+    E, M, T, r, K, N = 3, 4800, 4804, 16, 40, 56
     for x_ld, y_ld in ((0, 0), (48, 64)):
         xb, yb = ((T - 1) * (x_ld or K) + K) * 2, ((T - 1) * (y_ld or N) + N) * 2
         size = dict(x=xb, src=M * 4, counts=E * 4, A=E * r * K * 2, B_=E * r * N * 2, scale=E * 4, base=yb, y=yb, u=M * r * 4,
