@@ -68,6 +68,14 @@ bool fused_rows(const LoraShape& s) {
   const unsigned most = s.r <= 32 ? 256 : s.r <= 64 ? 128 : 64;
   return s.r * s.K <= (1 << 17) && tile_bound(s.M_cap, s.L, 16) <= most;
 }
+// The same for the backward's w and dx, whose weights of r > 32 do not fit the LDS.  Us of a
+// forward and a backward, w and dx in two launches against one, K 4096: 16 rows, r 16, N 1024
+// 18.1 / 15.7; 100 rows in 4 groups, r 32, N 1024 25.7 / 21.9; 1024 rows, r 16, N 2880 35.8 /
+// 32.1; 1500 rows in 96 groups (189 tiles), r 16, N 1024 65.7 / 54.7; 3000 rows in 8 groups
+// (195), r 16, N 2880 62.9 / 63.7.
+bool fused_back(const LoraShape& s) {
+  return s.r <= 32 && s.r * s.N <= (1 << 17) && tile_bound(s.M_cap, s.L, 16) <= 256;
+}
 // Else, whether it goes by tiles of 16 rows (2048 rows in 64 groups, r 16, K and N 2880: 30.5
 // us, with tiles of 64 rows 22.3).
 bool few_rows(const LoraShape& s) { return s.M_cap <= 64 || s.M_cap <= 4LL * s.L; }
@@ -118,6 +126,28 @@ void wide(const LoraGroups& g, const LoraShape& s, const float* u, int slices, f
   });
 }
 
+// Both products in one launch: W1 has K columns, W2 N.
+template <bool TURNED>
+void few(const LoraGroups& g, const LoraShape& s, const uint16_t* x, long long x_ld, const uint16_t* W1, const uint16_t* W2,
+         int K, int N, const float* scale, const uint16_t* base, uint16_t* y, long long y_ld, float* u, hipStream_t st) {
+  const unsigned tiles = tile_bound(s.M_cap, s.L, 16);
+  // columns for 256 workgroups (512: 64 rows in 32 groups 9.4 us for 7.4); where there are
+  // more than eight waves take at once, they take two runs at a time
+  const int slice = div_up(div_up(N, (int)(256 / tiles)), 256) * 256;
+  const dim3 grid(tiles, (unsigned)div_up(N, slice));
+  const auto go = [&](auto rb, auto nb) {
+    constexpr int RB = decltype(rb)::value, NB = decltype(nb)::value;
+    hipLaunchKernelGGL((lora_few_kernel<RB, RB <= 2 ? 2 : 1, NB, TURNED>), grid, dim3(512), 0, st, g, x, x_ld, W1, W2, scale,
+                       s.r, K, N, slice, base, y, y_ld, u);
+  };
+  for_rank_blocks(s.r, [&](auto n) {
+    if constexpr (decltype(n)::value <= 2) {
+      if (slice > 256) return go(n, std::integral_constant<int, 2>{});
+    }
+    if constexpr (decltype(n)::value <= 2 || !TURNED) go(n, std::integral_constant<int, 1>{});
+  });
+}
+
 moe_status_t report(const LoraGroups& g, hipStream_t st) {
   if (g.offsets_out || g.status_out) hipLaunchKernelGGL(lora_report_kernel, dim3(1), dim3(64), 0, st, g);
   return launched();
@@ -134,25 +164,11 @@ moe_status_t launch_lora_fwd(const LoraArgs& a, const uint16_t* x, const uint16_
                              void* ws, hipStream_t st) {
   const LoraShape s = {a.g.M_cap, a.g.L, a.r, a.K, a.N};
   if (a.g.M_cap == 0 || a.g.T == 0) return report(a.g, st);
-  const unsigned tiles = tile_bound(s.M_cap, s.L, 16);
   if (fused_rows(s)) {
-    // columns for 256 workgroups (512: 64 rows in 32 groups 9.4 us for 7.4); where there are
-    // more than eight waves take at once, they take two runs at a time
-    const int slice = div_up(div_up(a.N, (int)(256 / tiles)), 256) * 256;
-    const dim3 grid(tiles, (unsigned)div_up(a.N, slice));
-    const auto go = [&](auto rb, auto nb) {
-      constexpr int RB = decltype(rb)::value, NB = decltype(nb)::value;
-      hipLaunchKernelGGL((lora_few_kernel<RB, RB <= 2 ? 2 : 1, NB>), grid, dim3(512), 0, st, a.g, x, a.x_ld, a.A, a.B,
-                         a.scale, a.r, a.K, a.N, slice, base, y, a.y_ld, u);
-    };
-    for_rank_blocks(s.r, [&](auto n) {
-      if constexpr (decltype(n)::value <= 2) {
-        if (slice > 256) return go(n, std::integral_constant<int, 2>{});
-      }
-      go(n, std::integral_constant<int, 1>{});
-    });
+    few<false>(a.g, s, x, a.x_ld, a.A, a.B, a.K, a.N, a.scale, base, y, a.y_ld, u, st);
     return launched();
   }
+  const unsigned tiles = tile_bound(s.M_cap, s.L, 16);
   if (few_rows(s)) {
     const int slices = div_up(a.K, 512);
     float* part = slices == 1 && u ? u : static_cast<float*>(ws);
@@ -204,7 +220,10 @@ moe_status_t launch_lora_bwd(const LoraArgs& a, const uint16_t* dy, const uint16
                          piece, accumulate);
     });
   };
-  if (dx || dA) {
+  if (dx && fused_back(s)) {
+    few<true>(a.g, s, dy, a.y_ld, a.B, a.A, a.N, a.K, a.scale, dx_base, dx, a.x_ld, dA ? w : nullptr, st);
+    sums(dA != nullptr, dB != nullptr);
+  } else if (dx || dA) {
     int slice = narrow_slice(s, a.N);
     if (!dx) slice = div_up(a.N, 128) * 128;    // nothing adds slices up: one
     const int slices = div_up(a.N, slice);

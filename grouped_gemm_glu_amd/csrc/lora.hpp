@@ -688,20 +688,25 @@ __global__ __launch_bounds__(256) void lora_few_wide_kernel(LoraGroups g, const 
 // Both products in one launch where an adapter's A is small: each workgroup of a
 // tile computes the whole u (its eight waves take runs of 64 columns of K in turn,
 // AT_ONCE of them on their way), then a slice of y's columns, NB runs of 32 at a time
-// for each wave.  Measured: 58 rows in 32 groups, r 16, K 2880, N 5760 7.4 us for 10.5 MB,
+// for each wave.  With TURNED both weights lie the other way round (the backward's w and
+// dx) and are read crosswise from LDS.  Measured: 58 rows in 32 groups, r 16, K 2880, N 5760 7.4 us for 10.5 MB,
 // 1 row, K 7168, N 4096 8.4: the products one after the other, each a few trips to memory
 // of 0.7 us (A and x loaded as the MFMA takes them 9.6; one, three or more runs at once 8.4
 // to 9.0 at NB 1 for 8.1; y's columns one run at a time 8.0).
-template <int RB, int AT_ONCE, int NB>
+template <int RB, int AT_ONCE, int NB, bool TURNED>
 __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint16_t* __restrict__ x, long long x_ld,
                                                        const uint16_t* __restrict__ A, const uint16_t* __restrict__ B,
                                                        const float* __restrict__ scale, int r, int K, int N, int slice,
                                                        const uint16_t* base, uint16_t* y, long long y_ld,
                                                        float* __restrict__ u_out) {
   constexpr int RP = 16 * RB, LD = RP + 4, WAVES = 8;
-  constexpr int XLD = 64 + 8, ROWS = 16 * XLD;   // a wave's 64 columns of 16 rows
+  // a wave's piece of LDS: 64 columns of x's 16 rows, then what it needs of the weights
+  // (the first ones of 64 columns, 16 ranks or with TURNED all; with TURNED the second ones
+  // of 32 columns, from the start)
+  constexpr int XLD = 64 + 8, ROWS = 16 * XLD, WLD = RP + 8, BLD = 32 + 8;
+  constexpr int MINE = ROWS + (TURNED ? 64 * WLD : ROWS);
   __shared__ __attribute__((aligned(16))) float red[WAVES * 16 * LD];
-  __shared__ __attribute__((aligned(16))) uint16_t xs[WAVES * 2 * ROWS];
+  __shared__ __attribute__((aligned(16))) uint16_t xs[WAVES * MINE];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int row16 = lane & 15, q = lane >> 4;
   if (blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) lora_report(g);
@@ -715,17 +720,25 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint1
     const int c = 8 * (4 * k + q);
     from[k] = c < r ? c : c < 2 * r ? c - r : -1;
   }
-  bf16x8 bv[NB][RB][2];
+  // as they lie in memory: fragments, or with TURNED rows of 32 columns, 16 a load
+  u32x4 bv[NB][TURNED ? RB : 2 * RB];
   const auto load_b = [&]() {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int k = 0; k < RB; ++k)
+      for (int k = 0; k < RB; ++k) {
+        const int first = n0 + 32 * WAVES * b;
+        if constexpr (TURNED) {
+          const uint16_t* row = B + ((long long)t.e * r + min(16 * k + (lane >> 2), r - 1)) * N;
+          bv[b][k] = *reinterpret_cast<const u32x4*>(row + min(first + 8 * (lane & 3), N - 8));
+        } else {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int n = min(n0 + 32 * WAVES * b + 8 * (row16 >> 2) + (row16 & 3) + 4 * j, N - 1);
-          bv[b][k][j] = load8(B + ((long long)t.e * N + n) * r + max(from[k], 0));
+          for (int j = 0; j < 2; ++j) {
+            const int n = min(first + 8 * (row16 >> 2) + (row16 & 3) + 4 * j, N - 1);
+            bv[b][2 * k + j] = *reinterpret_cast<const u32x4*>(B + ((long long)t.e * N + n) * r + max(from[k], 0));
+          }
         }
+      }
   };
   load_b();
   const uint16_t* Ae = A + (long long)t.e * r * K;
@@ -737,7 +750,7 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint1
   const uint16_t* xr[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) xr[i] = x + (long long)max(__shfl(row, 8 * i + sub, 64), 0) * x_ld;
-  uint16_t* mine = xs + wave * (2 * ROWS);
+  uint16_t* mine = xs + wave * MINE;
   const long long yo = (long long)max(row, 0) * y_ld;
   u32x4 old[NB] = {};
   const auto load_base = [&]() {
@@ -750,34 +763,54 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint1
   load_base();
   f32x4 acc[RB] = {};
   for (int k0 = 64 * wave; k0 < K; k0 += 64 * WAVES * AT_ONCE) {
-    u32x4 av[AT_ONCE][RB][2], xv[AT_ONCE][2];
+    u32x4 av[AT_ONCE][2 * RB], xv[AT_ONCE][2];
 #pragma unroll
     for (int n = 0; n < AT_ONCE; ++n) {
-      const int c = min(k0 + 64 * WAVES * n + 8 * piece, K - 8);
+      const int first = k0 + 64 * WAVES * n, c = min(first + 8 * piece, K - 8);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-          av[n][b][i] = *reinterpret_cast<const u32x4*>(Ae + (long long)min(16 * b + 8 * i + sub, r - 1) * K + c);
-        xv[n][i] = *reinterpret_cast<const u32x4*>(xr[i] + c);
+      for (int i = 0; i < 2 * RB; ++i) {
+        if constexpr (TURNED) {
+          const int at = lane + 64 * i, col = at / (2 * RB), rc = 8 * (at - col * (2 * RB));
+          av[n][i] = *reinterpret_cast<const u32x4*>(Ae + (long long)min(first + col, K - 1) * r + min(rc, r - 8));
+        } else {
+          av[n][i] = *reinterpret_cast<const u32x4*>(Ae + (long long)min(8 * i + sub, r - 1) * K + c);
+        }
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) xv[n][i] = *reinterpret_cast<const u32x4*>(xr[i] + c);
     }
 #pragma unroll
     for (int n = 0; n < AT_ONCE; ++n) {
-      const bool in = k0 + 64 * WAVES * n + 8 * piece < K;
-      const auto turned = [&](uint16_t* lds, const u32x4 (&v)[2], bf16x8 (&f)[2]) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<u32x4*>(lds + (8 * i + sub) * XLD + 8 * piece) = in ? v[i] : u32x4{0, 0, 0, 0};
+      const int first = k0 + 64 * WAVES * n;
+      const u32x4 none = {0, 0, 0, 0};
+      const auto through = [&](uint16_t* lds, const u32x4& v0, const u32x4& v1, bf16x8 (&f)[2]) {
+        const bool in = first + 8 * piece < K;
+        *reinterpret_cast<u32x4*>(lds + sub * XLD + 8 * piece) = in ? v0 : none;
+        *reinterpret_cast<u32x4*>(lds + (8 + sub) * XLD + 8 * piece) = in ? v1 : none;
 #pragma unroll
         for (int j = 0; j < 2; ++j) f[j] = load8(lds + row16 * XLD + 8 * (4 * j + q));
       };
       bf16x8 xf[2];
-      turned(mine, xv[n], xf);
+      through(mine, xv[n][0], xv[n][1], xf);
+      if constexpr (TURNED) {
+#pragma unroll
+        for (int i = 0; i < 2 * RB; ++i) {
+          const int at = lane + 64 * i, col = at / (2 * RB), rc = 8 * (at - col * (2 * RB));
+          *reinterpret_cast<u32x4*>(mine + ROWS + col * WLD + rc) = first + col < K ? av[n][i] : none;
+        }
+      }
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
         bf16x8 af[2];
-        turned(mine + ROWS, av[n][b], af);
+        if constexpr (TURNED) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint16_t* p = mine + ROWS + (32 * j + 8 * q + (row16 >> 2)) * WLD + 16 * b + 4 * (row16 & 3);
+            af[j] = read_crosswise(p, p + 4 * WLD);
+          }
+        } else {
+          through(mine + ROWS, av[n][2 * b], av[n][2 * b + 1], af);
+        }
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[b] = mfma16(af[j], xf[j], acc[b]);
       }
@@ -808,10 +841,23 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint1
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       f32x4 out[2] = {};
+      if constexpr (TURNED)
+#pragma unroll
+        for (int k = 0; k < RB; ++k)
+          *reinterpret_cast<u32x4*>(mine + (16 * k + (lane >> 2)) * BLD + 8 * (lane & 3)) = bv[b][k];
 #pragma unroll
       for (int k = 0; k < RB; ++k)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) out[j] = mfma16(from[k] >= 0 ? bv[b][k][j] : zero8(), uv[k], out[j]);
+        for (int j = 0; j < 2; ++j) {
+          bf16x8 bf;
+          if constexpr (TURNED) {
+            const uint16_t* p = mine + (max(from[k], 0) + (row16 >> 2)) * BLD + 8 * (row16 & 3) + 4 * j;
+            bf = read_crosswise(p, p + 4 * BLD);
+          } else {
+            bf = __builtin_bit_cast(bf16x8, bv[b][2 * k + j]);
+          }
+          out[j] = mfma16(from[k] >= 0 ? bf : zero8(), uv[k], out[j]);
+        }
       float o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = out[i >> 2][i & 3];
