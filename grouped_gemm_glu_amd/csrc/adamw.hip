@@ -36,10 +36,15 @@ moe_status_t launch_adamw_unpack(const int8_t* m, const float* m_scale, const ui
 
 moe_status_t launch_grad_norm(const AdamwChunk* chunks, long long n_chunks, float max_norm, float* out, double* part,
                               hipStream_t s) {
+  // One workgroup for few chunks (us against two launches: 16 chunks of 2048 4.0 / 6.9, 32 5.5 /
+  // 7.0, 48 7.4 / 7.0, 64 9.1 / 6.9).
+  if (n_chunks <= 32) {
+    hipLaunchKernelGGL(grad_norm_few_kernel, dim3(1), dim3(1024), 0, s, chunks, n_chunks, max_norm, out);
+    return launched();
+  }
   // (265M fp32 gradients: 1024 workgroups 165 us, 6.4 TB/s; 768 the same, 512 218)
   const int parts = (int)(n_chunks < kNormParts ? n_chunks : kNormParts);
-  if (parts > 0)
-    hipLaunchKernelGGL(grad_norm_kernel, dim3((unsigned)parts), dim3(256), 0, s, chunks, n_chunks, part);
+  hipLaunchKernelGGL(grad_norm_kernel, dim3((unsigned)parts), dim3(256), 0, s, chunks, n_chunks, part);
   hipLaunchKernelGGL(grad_norm_final_kernel, dim3(1), dim3(256), 0, s, part, parts, max_norm, out);
   return launched();
 }

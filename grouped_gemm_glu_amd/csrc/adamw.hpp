@@ -397,22 +397,27 @@ __global__ __launch_bounds__(256) void adamw_unpack_kernel(const int8_t* __restr
 // ---------------------------------------------------------------- norm of the gradients
 // Squares summed in 64 bits (their range too: the squares of fp32 values do not
 // fit fp32), each workgroup over chunks in a fixed order.  Bound by reading: 265M fp32
-// gradients 164 us, 6.5 TB/s; a second launch adds the workgroups' sums (one launch would
-// need a counter that each call finds at 0).
-__device__ __forceinline__ double block_sum(double v, double* tmp) {   // tmp: 4 of LDS; the result in thread 0
+// gradients 164 us, 6.5 TB/s; a second launch adds the workgroups' sums (one launch of
+// many would need a counter that each call finds at 0).
+template <int WAVES>
+__device__ __forceinline__ double block_sum(double v, double* tmp) {   // tmp: WAVES of LDS
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
   if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
   __syncthreads();
-  return tmp[0] + tmp[1] + tmp[2] + tmp[3];
+  v = 0.0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) v += tmp[w];
+  return v;
 }
+// by 256 threads, of which this is the tid-th
 template <bool BF16>
-__device__ __forceinline__ void add_squares(const AdamwChunk& t, double* sum) {
+__device__ __forceinline__ void add_squares(const AdamwChunk& t, int tid, double* sum) {
   const auto add = [&](const float* g) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) sum[k] = fma((double)g[k], (double)g[k], sum[k]);
   };
-  const int i = 4 * threadIdx.x;
+  const int i = 4 * tid;
   int at = 0;
   for (; at + 2 * kAdamwStep <= t.n; at += 2 * kAdamwStep) {
     float g[2][4];
@@ -427,34 +432,49 @@ __device__ __forceinline__ void add_squares(const AdamwChunk& t, double* sum) {
     add(g);
   }
 }
-__global__ __launch_bounds__(256) void grad_norm_kernel(const AdamwChunk* __restrict__ chunks, long long n_chunks,
-                                                        double* __restrict__ part) {
-  __shared__ double tmp[4];
+// chunks first, first + step, .. below n_chunks, the next one's table entry on its way
+__device__ __forceinline__ double squares_of(const AdamwChunk* __restrict__ chunks, long long first, long long step,
+                                             long long n_chunks, int tid) {
   double sum[4] = {};
-  AdamwChunk next = chunks[blockIdx.x];
-  for (long long c = blockIdx.x; c < n_chunks; c += gridDim.x) {
+  AdamwChunk next = chunks[min(first, n_chunks - 1)];
+  for (long long c = first; c < n_chunks; c += step) {
     const AdamwChunk t = next;
-    next = chunks[min(c + gridDim.x, n_chunks - 1)];
-    if (t.grad_bf16) add_squares<true>(t, sum);
-    else add_squares<false>(t, sum);
+    next = chunks[min(c + step, n_chunks - 1)];
+    if (t.grad_bf16) add_squares<true>(t, tid, sum);
+    else add_squares<false>(t, tid, sum);
   }
-  const double s = block_sum((sum[0] + sum[1]) + (sum[2] + sum[3]), tmp);
-  if (threadIdx.x == 0) part[blockIdx.x] = s;
+  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 // out[0] = the norm, out[1] = min(1, max_norm / (norm + 1e-6)), NaN where the
 // norm is not finite.
-__global__ __launch_bounds__(256) void grad_norm_final_kernel(const double* __restrict__ part, int parts,
-                                                              float max_norm, float* __restrict__ out) {
-  __shared__ double tmp[4];
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < parts; i += 256) sum += part[i];
-  sum = block_sum(sum, tmp);
-  if (threadIdx.x != 0) return;
+__device__ __forceinline__ void norm_out(double sum, float max_norm, float* out) {
   const double norm = sqrt(sum);
   const double f = (double)max_norm / (norm + 1e-6);
   const float n32 = (float)norm;
   out[0] = n32;
   out[1] = n32 < INFINITY ? (f > 1.0 ? 1.0f : (float)f) : __uint_as_float(0x7FC00000u);
+}
+__global__ __launch_bounds__(256) void grad_norm_kernel(const AdamwChunk* __restrict__ chunks, long long n_chunks,
+                                                        double* __restrict__ part) {
+  __shared__ double tmp[4];
+  const double s = block_sum<4>(squares_of(chunks, blockIdx.x, gridDim.x, n_chunks, threadIdx.x), tmp);
+  if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+__global__ __launch_bounds__(256) void grad_norm_final_kernel(const double* __restrict__ part, int parts,
+                                                              float max_norm, float* __restrict__ out) {
+  __shared__ double tmp[4];
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < parts; i += 256) sum += part[i];
+  sum = block_sum<4>(sum, tmp);
+  if (threadIdx.x == 0) norm_out(sum, max_norm, out);
+}
+// A plan of few chunks in one launch, four of them at a time.
+__global__ __launch_bounds__(1024) void grad_norm_few_kernel(const AdamwChunk* __restrict__ chunks, long long n_chunks,
+                                                             float max_norm, float* __restrict__ out) {
+  __shared__ double tmp[16];
+  const double s = n_chunks > 0 ? squares_of(chunks, threadIdx.x >> 8, 4, n_chunks, threadIdx.x & 255) : 0.0;
+  const double sum = block_sum<16>(s, tmp);
+  if (threadIdx.x == 0) norm_out(sum, max_norm, out);
 }
 
 }  // namespace moe

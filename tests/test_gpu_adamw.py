@@ -295,6 +295,20 @@ def test_norm(G, sizes, bf16):  # noqa: F811
         assert abs(got[0] - norm) <= 1.01 * U * norm and abs(got[1] - factor) <= 2.01 * U * factor
 
 
+@pytest.mark.parametrize("sizes", [[40000, 3, 20000], [2048] * 31, [65536], [65537], [1] * 32, [1] * 33])
+def test_norm_of_few_pieces(G, sizes):  # noqa: F811
+    """One workgroup's plans and the ones after them, to their extremes."""
+    import torch
+    test_norm(G, sizes, False)
+    test_norm(G, sizes, True)
+    for bad in (float("nan"), float("inf"), 3e38):
+        t = [torch.ones(n, device="cuda") for n in sizes]
+        t[-1][-1] = bad
+        t[0][0] = 3e38 if bad == 3e38 else 1
+        got = _norm(G, t)
+        assert not np.isfinite(got[0]) and np.isnan(got[1])
+
+
 def test_norm_extremes(G):  # noqa: F811
     import torch
     got = _norm(G, [torch.full((1000,), 1e30, device="cuda")])
