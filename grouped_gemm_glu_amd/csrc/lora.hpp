@@ -184,11 +184,24 @@ __device__ __forceinline__ bf16x8 zero8() {
   return __builtin_bit_cast(bf16x8, z);
 }
 
-// fp32 as a sum of bf16 values: the upper half of its bits (no rounding, so that
-// nothing overflows), then what is left.  An infinity is its first part alone.
+// fp32 as a sum of three bf16 values: the upper half of its bits, the same of what is
+// left, and the rest, 8 bits each.  An infinity is its first part alone.
 __device__ __forceinline__ uint32_t upper_half(float v) { return __float_as_uint(v) >> 16; }
 __device__ __forceinline__ float rest_of(float v) {
   const float hi = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+  return v == hi ? 0.0f : v - hi;
+}
+// As a sum of two: the nearest bf16 value, then what is left, half a step at most and
+// rounded in its turn, 2^-17 of v (the upper half first would leave up to a whole step:
+// 2^-16).  Where the nearest would be an infinity that v is not it is the upper half.  A
+// NaN is in the second part at least.
+__device__ __forceinline__ uint32_t nearest_half(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const uint32_t up = (b & 0x7FFFFFFFu) - 0x7F7F8000u < 0x8000u ? 0u : 0x8000u;
+  return (b + up) >> 16;
+}
+__device__ __forceinline__ float rest_of_nearest(float v) {
+  const float hi = __uint_as_float(nearest_half(v) << 16);
   return v == hi ? 0.0f : v - hi;
 }
 
@@ -352,9 +365,8 @@ __global__ __launch_bounds__(256, RB <= 4 ? 2 : 1) void lora_narrow_kernel(LoraG
 }
 
 // The u of a row from value c (of 8) of its two parts, as a fragment: the slices'
-// sums added in order, times s; the upper half of their bits for c < r, what is left
-// for c < 2 r, else 0.  Two parts hold u to 2^-17 of its value, far below the
-// rounding of y.  out (nullable): where the sum itself goes.
+// sums added in order, times s; the nearest bf16 value for c < r, what is left for c <
+// 2 r, else 0.  Two parts hold u to 2^-17 of its value, far below the rounding of y.  out (nullable): where the sum itself goes.
 __device__ __forceinline__ bf16x8 u_fragment(const float* u, long long slice_len, int slices, int r, int c, float s,
                                              bool inside, float* out) {
   f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
@@ -390,8 +402,8 @@ __device__ __forceinline__ bf16x8 u_fragment(const float* u, long long slice_len
   u32x4 f;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    f[i] = c < r ? upper_half(v[2 * i]) | upper_half(v[2 * i + 1]) << 16
-                 : pack_bf16x2(rest_of(v[2 * i]), rest_of(v[2 * i + 1]));
+    f[i] = c < r ? nearest_half(v[2 * i]) | nearest_half(v[2 * i + 1]) << 16
+                 : pack_bf16x2(rest_of_nearest(v[2 * i]), rest_of_nearest(v[2 * i + 1]));
   if (c >= 2 * r) f = u32x4{0, 0, 0, 0};          // (an infinite s)
   return __builtin_bit_cast(bf16x8, f);
 }
@@ -410,7 +422,7 @@ __device__ __forceinline__ uint32_t pick16(uint32_t lo, uint32_t hi, bool upper)
 // ---------------------------------------------------------------- y = base + s u W^T
 // A tile of 64 rows and a slice of N per workgroup, 128 columns at a time, the next
 // step's base and the weights after it in flight.  A wave holds its 16 rows' u as
-// two bf16 parts, [upper r | rest r | zeros], one reduction of KS MFMA steps against
+// two bf16 parts, [nearest r | rest r | zeros], one reduction of KS MFMA steps against
 // the weights taken twice.  The weights come through LDS (two
 // stages) as [column][r], W [N][r] as it is or with TURNED [r][N] (the backward's dx
 // = w A) taken apart by byte permutations.  Column 8 i + j of a step lies in row 16
