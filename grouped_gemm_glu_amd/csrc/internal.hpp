@@ -72,6 +72,12 @@ struct LoraShape {
 };
 size_t lora_fwd_workspace(const LoraShape& s);
 size_t lora_bwd_workspace(const LoraShape& s);
+// Which kernels a call of these sizes takes: out[0] for u and y, out[1] for w and
+// dx (0 one launch, 1 two of 16-row tiles, 2 and 3 two of tiles of 64 and of 128
+// rows), out[2] the most rows of a piece of dA and dB.  Not part of the public
+// interface; a symbol of its own so that a test of a kernel can tell that its
+// sizes reach it.
+extern "C" void moe_lora_takes(int M_cap, int E, int r, int K, int N, int* out);
 moe_status_t launch_lora_fwd(const LoraArgs& a, const uint16_t* x, const uint16_t* base, uint16_t* y, float* u,
                              void* ws, hipStream_t s);
 moe_status_t launch_lora_bwd(const LoraArgs& a, const uint16_t* dy, const uint16_t* x, const float* u,

@@ -160,6 +160,13 @@ size_t lora_fwd_workspace(const LoraShape& s) {
 }
 size_t lora_bwd_workspace(const LoraShape& s) { return bwd_layout(s).end; }
 
+extern "C" void moe_lora_takes(int M_cap, int E, int r, int K, int N, int* out) {
+  const LoraShape s = {M_cap, E, r, K, N};
+  out[0] = fused_rows(s) ? 0 : few_rows(s) ? 1 : 1 + narrow_blocks(s);
+  out[1] = fused_back(s) ? 0 : 1 + narrow_blocks(s);
+  out[2] = sum_piece(s);
+}
+
 moe_status_t launch_lora_fwd(const LoraArgs& a, const uint16_t* x, const uint16_t* base, uint16_t* y, float* u,
                              void* ws, hipStream_t st) {
   const LoraShape s = {a.g.M_cap, a.g.L, a.r, a.K, a.N};
