@@ -169,6 +169,11 @@ struct AdamwFour<true> {
   float g[4], p[4], m_scale, v_scale;
   uint32_t m, v;
 };
+// fp32's largest value for an infinity: what a small correction of a value takes, so
+// that an infinite one stays as it is (a NaN is in the value itself).
+__device__ __forceinline__ float finite_of(float v) {
+  return __builtin_amdgcn_fmed3f(v, -3.402823466e38f, 3.402823466e38f);
+}
 // elements i .. i + n of the tensor, n <= 4 (WHOLE: n = 4, with nothing skipped, so
 // that the compiler can count the loads on their way)
 template <int PARAM, bool GRAD16, bool STATE8, bool WHOLE>
@@ -289,7 +294,7 @@ __device__ __forceinline__ void adamw_update(const AdamwChunk& t, int i, int n, 
                                       : m[k] * h.step_size * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(w) + h.eps);
     // (p times fp32's 1 - lr decay would round every element's decay the same way, to a
     // multiple of 2^-24: lr decay = 1e-7 acted as 1.19e-7, below 3e-8 as 0)
-    p[k] = f.p[k] - fmaf(h.decay, f.p[k], update);
+    p[k] = f.p[k] - fmaf(h.decay, finite_of(f.p[k]), update);
   }
   if constexpr (PARAM == 2) store4<false>(t.master, i, n, p);
   if constexpr (PARAM == 0) store4<false>(t.param, i, n, p);

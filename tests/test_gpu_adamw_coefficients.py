@@ -52,3 +52,23 @@ def test_small_decay(G, kind, bits, decay):  # noqa: F811
     got = to_host(d["param"] if master is None else master).astype(np.float64)
     assert abs(np.mean(got - want.astype(np.float32))) <= MEAN
     assert np.all(np.abs(got - want) <= 2.0 ** -23 * 1.01)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("decay", [0.0, 0.1, -0.1])
+def test_infinite_parameters_stay(G, decay, bits):  # noqa: F811
+    """A parameter that left fp32 stays infinite, with or without a decay, and a NaN a NaN."""
+    import torch
+    inf = float("inf")
+    start = torch.tensor([inf, -inf, float("nan"), 3.4e38, -3.4e38], device="cuda")
+    for grad in (1.0, 0.0, -1.0):
+        param, g = start.clone(), torch.full((5,), grad, device="cuda")
+        if bits == 32:
+            t = G.adamw_tensor(param, g, torch.zeros(5, device="cuda"), torch.zeros(5, device="cuda"), weight_decay=decay)
+        else:
+            t = G.adamw_tensor(param, g, torch.zeros(5, dtype=torch.int8, device="cuda"), torch.zeros(5, dtype=torch.uint8, device="cuda"),
+                               m_scale=torch.zeros(1, device="cuda"), v_scale=torch.zeros(1, device="cuda"), weight_decay=decay)
+        G.moe_adamw_step(G.adamw_plan([t]), G.adamw(1e-3))
+        torch.cuda.synchronize()
+        assert param[0] == inf and param[1] == -inf and torch.isnan(param[2])
+        assert abs(float(param[3]) / 3.4e38 - (1 - 1e-3 * decay)) <= 1e-6 and param[4] == -param[3]
