@@ -1,5 +1,5 @@
 """The step's coefficients, whose errors are the same for every element and add up
-over the steps: weight decay far below an fp32 rounding of 1.
+over the steps: weight decay far below an fp32 rounding of 1, and betas near 1.
 
 A single fp32 result is off by up to half a step, which hides them; the mean over n
 elements is not.  The results lie in [1, 2) (some at its ends' other sides, with
@@ -52,6 +52,46 @@ def test_small_decay(G, kind, bits, decay):  # noqa: F811
     got = to_host(d["param"] if master is None else master).astype(np.float64)
     assert abs(np.mean(got - want.astype(np.float32))) <= MEAN
     assert np.all(np.abs(got - want) <= 2.0 ** -23 * 1.01)
+
+
+@pytest.mark.parametrize("beta1,beta2", [(0.9, 0.999), (0.95, 0.99999), (1 - 1e-5, 1 - 2e-8), (1 - 1e-6, 1 - 2.0 ** -30)])
+def test_betas_near_one(G, beta1, beta2):  # noqa: F811
+    """The moments of 32 bits: beta and 1 - beta add up to 1, also where fp32's beta is 1 itself."""
+    import torch
+    rng = np.random.default_rng(2)
+    m, v = one_to_two(rng), one_to_two(rng)
+    # gradients of either sign whose squares add between 0 and 64 steps to v, each as likely
+    g = np.sqrt(rng.random(N) * 2.0 ** -17 / (1 - beta2)) * rng.choice([-1.0, 1.0], N)
+    g = g.astype(np.float32)
+    dm, dv = to_dev(m), to_dev(v)
+    param = torch.zeros(N, device="cuda")
+    G.moe_adamw_step(G.adamw_plan([G.adamw_tensor(param, to_dev(g), dm, dv)]), G.adamw(1e-3, beta1, beta2, 1e-8, step=100))
+    torch.cuda.synchronize()
+    _, want_m, want_v = P.adamw(np.zeros(N), g, m, v, 1e-3, beta1, beta2, 1e-8, 100)
+    for got, want, old, add in ((to_host(dm), want_m, m, (1 - beta1) * g.astype(np.float64)),
+                                (to_host(dv), want_v, v, (1 - beta2) * g.astype(np.float64) ** 2)):
+        err = got.astype(np.float64) - want
+        # (1 - beta's own rounding, 2^-24 of the term, is the same for all too)
+        assert abs(np.mean(err)) <= MEAN + 2.0 ** -24 * abs(np.mean(add)), (np.mean(err), np.mean(add))
+        assert np.all(np.abs(err) <= 2.0 ** -23 * (np.abs(old) + 4 * np.abs(add)))
+
+
+@pytest.mark.parametrize("beta1,beta2", [(0.9, 0.999), (0.95, 0.99999), (0.0, 0.0), (0.99, 0.98)])
+def test_infinite_moments_stay(G, beta1, beta2):  # noqa: F811
+    """Moments that left fp32 (a gradient past 1.8e19 leaves an infinite v beside a finite m) stay infinite, whichever
+    way beta rounds, and the parameter of such a v stays put."""
+    import torch
+    inf = float("inf")
+    m, v = torch.tensor([inf, -inf, 1.0, 0.0], device="cuda"), torch.tensor([1.0, 1.0, inf, inf], device="cuda")
+    param = torch.ones(4, device="cuda")
+    plan = G.adamw_plan([G.adamw_tensor(param, torch.ones(4, device="cuda"), m, v)])
+    for step in (1, 2, 3):
+        G.moe_adamw_step(plan, G.adamw(1e-3, beta1, beta2, 1e-8, step=step))
+        torch.cuda.synchronize()
+        if beta1:
+            assert m[0] == inf and m[1] == -inf and param[0] == -inf and param[1] == inf
+        if beta2:
+            assert v[2] == inf and v[3] == inf and param[2] == 1 and param[3] == 1
 
 
 @pytest.mark.parametrize("bits", [32, 8])
