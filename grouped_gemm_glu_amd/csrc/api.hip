@@ -3,11 +3,11 @@
 // host can see and returns before any launch on error; nothing here
 // allocates, synchronises or reads device memory back.
 #include <math.h>
+#include <stddef.h>
 #include <string.h>
 
 #include <algorithm>
 #include <initializer_list>
-#include <new>
 
 #include "aux_kernels.hpp"
 #include "internal.hpp"
@@ -1027,46 +1027,49 @@ size_t moe_adamw_plan_bytes(const moe_adamw_tensor_t* tensors, int n_tensors) {
   return chunks * sizeof(AdamwChunk);
 }
 
+// The buffers of a step's tensor are numbered 8 i + which, in the order of the
+// struct's pointers.
+constexpr uint32_t kAdamwBuffers = 7;
+static_assert(offsetof(moe_adamw_tensor_t, n) == kAdamwBuffers * sizeof(void*), "the pointers come first");
+static uintptr_t adamw_address(const moe_adamw_tensor_t* tensors, uint32_t number) {
+  uintptr_t p;
+  memcpy(&p, reinterpret_cast<const char*>(&tensors[number >> 3]) + (number & 7) * sizeof(p), sizeof(p));
+  return p;
+}
+static size_t adamw_bytes(const moe_adamw_tensor_t& t, uint32_t which) {
+  const size_t n = (size_t)t.n, scales = t.state_bits == 8 ? (n + kAdamwBlock - 1) / kAdamwBlock * 4 : 0;
+  switch (which) {
+    case 0: return n * (t.param_dtype == MOE_DT_BF16 ? 2 : 4);
+    case 1: return n * (t.grad_dtype == MOE_DT_BF16 ? 2 : 4);
+    case 2: return n * 4;
+    case 3: case 4: return n * (t.state_bits / 8);
+    default: return scales;
+  }
+}
 // Whether an output of the tensors shares bytes with any other buffer of them:
-// neighbours by address are looked at, with the furthest end so far.
-static moe_status_t adamw_overlap(const moe_adamw_tensor_t* tensors, int n_tensors) {
-  struct Range {
-    uintptr_t begin, end;
-    bool output;
-  };
-  Range* r = new (std::nothrow) Range[(size_t)n_tensors * 7];
-  if (!r) return MOE_ERR_SHAPE;
-  size_t k = 0;
-  for (int i = 0; i < n_tensors; ++i) {
-    const moe_adamw_tensor_t& t = tensors[i];
-    const auto add = [&](const void* p, size_t bytes, bool output) {
-      const uintptr_t b = reinterpret_cast<uintptr_t>(p);
-      if (p && bytes) r[k++] = {b, b + bytes, output};
-    };
-    const auto width = [&](int dtype) { return (size_t)t.n * (dtype == MOE_DT_BF16 ? 2 : 4); };
-    add(t.grad, width(t.grad_dtype), false);
-    if (!t.param) continue;
-    const size_t scales = (size_t)((t.n + kAdamwBlock - 1) / kAdamwBlock) * 4;
-    const size_t state = (size_t)t.n * (t.state_bits / 8);
-    add(t.param, width(t.param_dtype), true);
-    add(t.master, (size_t)t.n * 4, true);
-    add(t.m, state, true);
-    add(t.v, state, true);
-    if (t.state_bits == 8) {
-      add(t.m_scale, scales, true);
-      add(t.v_scale, scales, true);
+// neighbours by address are looked at, with the furthest end so far.  The buffers'
+// numbers are sorted in the room of the table (4 bytes each, fewer than a tensor's
+// pieces take; a tensor without elements has neither), so that nothing is allocated.
+static moe_status_t adamw_overlap(const moe_adamw_tensor_t* tensors, int n_tensors, void* table) {
+  static_assert(kAdamwBuffers * sizeof(uint32_t) <= sizeof(AdamwChunk), "the numbers of a tensor's buffers");
+  uint32_t* number = static_cast<uint32_t*>(table);
+  size_t n = 0;
+  for (int i = 0; i < n_tensors; ++i)
+    for (uint32_t which = 0; which < kAdamwBuffers; ++which) {
+      const uint32_t k = (uint32_t)i * 8 + which;
+      if ((which == 1 || tensors[i].param) && adamw_address(tensors, k) && adamw_bytes(tensors[i], which)) number[n++] = k;
     }
-  }
-  std::sort(r, r + k, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  std::sort(number, number + n, [&](uint32_t a, uint32_t b) { return adamw_address(tensors, a) < adamw_address(tensors, b); });
   uintptr_t end_all = 0, end_out = 0;           // furthest end of the buffers before, of the outputs before
-  bool bad = false;
-  for (size_t i = 0; i < k; ++i) {
-    bad = bad || r[i].begin < end_out || (r[i].output && r[i].begin < end_all);
-    end_all = std::max(end_all, r[i].end);
-    if (r[i].output) end_out = std::max(end_out, r[i].end);
+  for (size_t i = 0; i < n; ++i) {
+    const uint32_t which = number[i] & 7;
+    const uintptr_t begin = adamw_address(tensors, number[i]);
+    const uintptr_t end = begin + adamw_bytes(tensors[number[i] >> 3], which);
+    if (begin < end_out || (which != 1 && begin < end_all)) return MOE_ERR_UNSUPPORTED;
+    end_all = std::max(end_all, end);
+    if (which != 1) end_out = std::max(end_out, end);
   }
-  delete[] r;
-  return bad ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  return MOE_OK;
 }
 
 moe_status_t moe_adamw_plan(const moe_adamw_tensor_t* tensors, int n_tensors, void* table, size_t table_bytes,
@@ -1080,7 +1083,7 @@ moe_status_t moe_adamw_plan(const moe_adamw_tensor_t* tensors, int n_tensors, vo
   }
   if (table_bytes < moe_adamw_plan_bytes(tensors, n_tensors)) return MOE_ERR_SHAPE;
   if (n_tensors > 0) {
-    const moe_status_t st = adamw_overlap(tensors, n_tensors);
+    const moe_status_t st = adamw_overlap(tensors, n_tensors, table);
     if (st != MOE_OK) return st;
   }
   AdamwChunk* out = static_cast<AdamwChunk*>(table);

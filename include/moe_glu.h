@@ -663,7 +663,8 @@ typedef struct {
  * and sets plan->table.  The plan holds as long as the tensors' addresses do;
  * their contents may change.  An output of a tensor (param, master, m, v,
  * scales) that shares bytes with any other buffer of the plan is
- * MOE_ERR_UNSUPPORTED.  (host struct) */
+ * MOE_ERR_UNSUPPORTED.  Where the call fails the table's contents mean nothing.
+ * (host struct) */
 typedef struct {
   const void* table;        /* device */
   int64_t n_chunks;         /* pieces of the tensors, as the table lists them */
