@@ -191,18 +191,19 @@ __device__ __forceinline__ float rest_of(float v) {
   const float hi = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
   return v == hi ? 0.0f : v - hi;
 }
-// As a sum of two: the nearest bf16 value, then what is left, half a step at most and
-// rounded in its turn, 2^-17 of v (the upper half first would leave up to a whole step:
-// 2^-16).  Where the nearest would be an infinity that v is not it is the upper half.  A
-// NaN is in the second part at least.
-__device__ __forceinline__ uint32_t nearest_half(float v) {
-  const uint32_t b = __float_as_uint(v);
-  const uint32_t up = (b & 0x7FFFFFFFu) - 0x7F7F8000u < 0x8000u ? 0u : 0x8000u;
-  return (b + up) >> 16;
-}
-__device__ __forceinline__ float rest_of_nearest(float v) {
-  const float hi = __uint_as_float(nearest_half(v) << 16);
-  return v == hi ? 0.0f : v - hi;
+// Two values as sums of two each: the nearest bf16 values, then what is left, half a step
+// at most and rounded in its turn, 2^-17 of them (the upper half first would leave up to a
+// whole step: 2^-16).  The first part is cut at bf16's largest value, so that nothing
+// rounds up to an infinity; an infinity or a NaN is in the second.
+struct TwoParts {
+  uint32_t first, rest;
+};
+__device__ __forceinline__ TwoParts two_parts(float v0, float v1) {
+  const float top = __uint_as_float(0x7F7F0000u);
+  TwoParts p;
+  p.first = pack_bf16x2(__builtin_amdgcn_fmed3f(v0, -top, top), __builtin_amdgcn_fmed3f(v1, -top, top));
+  p.rest = pack_bf16x2(v0 - __uint_as_float(p.first << 16), v1 - __uint_as_float(p.first & 0xFFFF0000u));
+  return p;
 }
 
 __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
@@ -401,9 +402,10 @@ __device__ __forceinline__ bf16x8 u_fragment(const float* u, long long slice_len
   for (int i = 0; i < 8; ++i) v[i] = s * (i < 4 ? lo[i] : hi[i - 4]);
   u32x4 f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    f[i] = c < r ? nearest_half(v[2 * i]) | nearest_half(v[2 * i + 1]) << 16
-                 : pack_bf16x2(rest_of_nearest(v[2 * i]), rest_of_nearest(v[2 * i + 1]));
+  for (int i = 0; i < 4; ++i) {
+    const TwoParts p = two_parts(v[2 * i], v[2 * i + 1]);
+    f[i] = c < r ? p.first : p.rest;
+  }
   if (c >= 2 * r) f = u32x4{0, 0, 0, 0};          // (an infinite s)
   return __builtin_bit_cast(bf16x8, f);
 }
