@@ -210,6 +210,17 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// A value that the compiler knows nothing of.  Where the lanes of a wave read one
+// another's values from a piece of LDS that the wave has to itself, LDS works through
+// its accesses in order, so nothing has to be waited for; but the compiler, which sees
+// one lane, may swap a lane's write and read where it can prove them apart.  A read whose
+// place follows from such a value it cannot tell from any write to the piece.  (Fences say
+// the same, but hold loads from memory back too: 1 row, r 16, K 7168 8.1 us for 7.7.)
+__device__ __forceinline__ int hidden(int v) {
+  asm("" : "+v"(v));
+  return v;
+}
+
 // Four consecutive elements of each of four rows of LDS, crosswise: in every 16
 // lanes, lane l gives the address of row l / 4, elements 4 (l % 4) .. + 3, and
 // gets element l of the four rows.
@@ -302,6 +313,7 @@ __global__ __launch_bounds__(256, RB <= 4 ? 2 : 1) void lora_narrow_kernel(LoraG
   u32x4 xa[MB][4], xb[MB][4];
   f32x4 acc[MB][RB] = {};
   uint16_t* mine = xs + wave * (MB * 16 * KT);
+  const int read16 = hidden(row16);
   // 16-byte piece c of row i of a wave's LDS lies at place c ^ i
   const auto compute = [&](int stage, int k0, const u32x4 (&v)[MB][4]) {
     const bool in = k0 + 8 * row16 < k_end;
@@ -317,7 +329,7 @@ __global__ __launch_bounds__(256, RB <= 4 ? 2 : 1) void lora_narrow_kernel(LoraG
     for (int j = 0; j < 4; ++j) {
       bf16x8 xf[MB];
 #pragma unroll
-      for (int m = 0; m < MB; ++m) xf[m] = load8(mine + (16 * m + row16) * KT + 8 * ((4 * j + q) ^ row16));
+      for (int m = 0; m < MB; ++m) xf[m] = load8(mine + (16 * m + read16) * KT + 8 * ((4 * j + q) ^ read16));
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
         bf16x8 wf;
@@ -765,6 +777,7 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint1
 #pragma unroll
   for (int i = 0; i < 2; ++i) xr[i] = x + (long long)max(__shfl(row, 8 * i + sub, 64), 0) * x_ld;
   uint16_t* mine = xs + wave * MINE;
+  const int read16 = hidden(row16);
   const long long yo = (long long)max(row, 0) * y_ld;
   u32x4 old[NB] = {};
   const auto load_base = [&]() {
@@ -802,7 +815,7 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint1
         *reinterpret_cast<u32x4*>(lds + sub * XLD + 8 * piece) = in ? v0 : none;
         *reinterpret_cast<u32x4*>(lds + (8 + sub) * XLD + 8 * piece) = in ? v1 : none;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) f[j] = load8(lds + row16 * XLD + 8 * (4 * j + q));
+        for (int j = 0; j < 2; ++j) f[j] = load8(lds + read16 * XLD + 8 * (4 * j + q));
       };
       bf16x8 xf[2];
       through(mine, xv[n][0], xv[n][1], xf);
@@ -819,7 +832,7 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint1
         if constexpr (TURNED) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint16_t* p = mine + ROWS + (32 * j + 8 * q + (row16 >> 2)) * WLD + 16 * b + 4 * (row16 & 3);
+            const uint16_t* p = mine + ROWS + (32 * j + 8 * q + (read16 >> 2)) * WLD + 16 * b + 4 * (read16 & 3);
             af[j] = read_crosswise(p, p + 4 * WLD);
           }
         } else {
@@ -865,7 +878,7 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint1
         for (int j = 0; j < 2; ++j) {
           bf16x8 bf;
           if constexpr (TURNED) {
-            const uint16_t* p = mine + (max(from[k], 0) + (row16 >> 2)) * BLD + 8 * (row16 & 3) + 4 * j;
+            const uint16_t* p = mine + (max(from[k], 0) + (read16 >> 2)) * BLD + 8 * (read16 & 3) + 4 * j;
             bf = read_crosswise(p, p + 4 * BLD);
           } else {
             bf = __builtin_bit_cast(bf16x8, bv[b][2 * k + j]);
@@ -964,6 +977,7 @@ __device__ __forceinline__ void lora_sum(const LoraTile& t, const LoraGroups& g,
     }
   };
   uint16_t* mine = xs + wave * (32 * XLD);
+  const int read16 = hidden(row16);
   const int sub = lane / PIECES, piece = lane % PIECES;
   const uint16_t* vc = p.v + min(c0 + 8 * piece, C - 8);
   const auto load_v = [&](int i0, u32x4 (&v)[NL]) {   // (columns past the last one: their sums are dropped)
@@ -981,7 +995,7 @@ __device__ __forceinline__ void lora_sum(const LoraTile& t, const LoraGroups& g,
   f32x4 acc[RB][CW] = {};
   const auto compute = [&](int stage) {
     const uint16_t* d = us + stage * STAGE + lora_part(row16, q);
-    const uint16_t* c = mine + (8 * q + (row16 >> 2)) * XLD + 4 * (row16 & 3);
+    const uint16_t* c = mine + (8 * q + (read16 >> 2)) * XLD + 4 * (read16 & 3);
     const auto column = [&](int j) { return read_crosswise(c + 16 * j, c + 16 * j + 4 * XLD); };
     const auto part_of_u = [&](int k, int part) { return load8(d + part * PART + 16 * 32 * k); };
     // what fewer registers hold stays over the loop, the lowest parts come first
