@@ -661,7 +661,10 @@ typedef struct {
  * memory of moe_adamw_plan_bytes(tensors, n_tensors) bytes, 8-byte aligned) and
  * plan's sizes; the caller copies the table to device memory (16-byte aligned)
  * and sets plan->table.  The plan holds as long as the tensors' addresses do;
- * their contents may change.  An output of a tensor (param, master, m, v,
+ * their contents may change.  (A plan of 300 tensors takes 0.1 ms here, copy
+ * apart, and 4 ms from Python, where each tensor's struct is made and checked:
+ * gradients that get new memory every step cost a new plan every step, so keep
+ * their buffers.)  An output of a tensor (param, master, m, v,
  * scales) that shares bytes with any other buffer of the plan is
  * MOE_ERR_UNSUPPORTED.  Where the call fails the table's contents mean nothing.
  * (host struct) */
@@ -684,15 +687,29 @@ typedef struct {
                                factor); where it is NaN the call changes nothing */
 } moe_adamw_t;
 
-/* One AdamW step over every tensor of the plan, in one launch.  With g = grad *
- * grad_scale, a = lr * lr_scale and t the step:
+/* One AdamW step over every tensor of the plan, in one launch for each width of
+ * state among them.  With g = grad * grad_scale, a = lr * lr_scale and t the
+ * step:
  *   m' = beta1 m + (1 - beta1) g,   v' = beta2 v + (1 - beta2) g^2
  *   p' = p (1 - a weight_decay) - a (m' / (1 - beta1^t)) / (sqrt(v' / (1 - beta2^t)) + eps)
  * in fp32.  8-bit states: m' and v' are formed in 64 bits, p' takes them before
  * they are rounded to codes, and the code is the nearest under the square root
  * (the lower of two as near; at least 1 for v' > 0), scales rounded to fp32.  A
  * block in which m' or v' is not finite gets scales NaN and codes 0.  Requires
- * 0 <= beta < 1, eps >= 0, all finite. */
+ * 0 <= beta < 1, eps >= 0, all finite.
+ *
+ * What 8-bit states are worth: codes move by whole codes, a v's falls in a step
+ * without a gradient only where code (1 - beta2^(1/4)) >= 1/2 (beta2 = 0.99: from
+ * 200 on; above (1 - 1/510)^4 = 0.9922 never), else with its block's scale alone,
+ * which follows the block's largest v; an m's where code (1 - beta1^(1/2)) >= 1/2
+ * (beta1 = 0.9: from 10 on).  sqrt(v) over the true one, fifth to 95th percentile
+ * of normally distributed gradients: 0.98 to 1.03 at beta2 = 0.99; at 0.999 0.88
+ * to 1.16 where a block's gradients are of uneven size, 0.98 to 1.42 after 4000
+ * steps and 1.1 to 1.7 in the end where they are of one size; 2.4 to 3.6 and 7.9
+ * to 13.2, 2000 and 6000 steps after its gradients fell tenfold, for an element
+ * beside others whose did not.  Its steps are that much too small.  32 bits for
+ * tensors whose elements' gradients come and go one by one; a beta2 of 0.99 or
+ * less has little of this where gradients are not 0. */
 moe_status_t moe_adamw_step(const moe_adamw_plan_t* plan, const moe_adamw_t* hyper, void* stream);
 
 /* 8-bit states read out as fp32 (to save, inspect or widen them): m_out, v_out
