@@ -315,7 +315,9 @@ def adamw_tensor(param, grad, m, v, master=None, m_scale=None, v_scale=None, wei
 
 def adamw_plan(tensors, device=None) -> AdamwPlanT:
     """Lays out the tensors of a step (adamw_tensor structs) once, with the table in the memory of their device (or
-    ``device``, where they are none), copied before the call returns.  The plan keeps the tensors alive."""
+    ``device``, where they are none), copied before the call returns.  The plan keeps the tensors alive, and holds
+    their addresses: build it once and keep the gradients' memory (fill them with zeros, rather than drop them), as a
+    plan of 300 tensors and their structs takes 4 ms."""
     import torch
     tensors = list(tensors)
     devices = {str(t.device) for s in tensors for t in s._keep if t is not None}
