@@ -1008,8 +1008,8 @@ static moe_status_t check_adamw_tensor(const moe_adamw_tensor_t& t) {
   return MOE_OK;
 }
 // Elements of a chunk: half as many for a plan that would leave compute units without
-// one (1.1M elements, 32 bits: 8.5 us with 4096, 7.3 with 2048; 1.6M in 300 tensors, 8
-// bits: 17.1 and 15.0; 531M: 3.10 ms and 3.14).
+// one (kernel: 1.1M elements, 32 bits: 8.2 us with 4096, 6.6 with 2048; 1.6M in 300
+// tensors, 8 bits: 15.7 and 12.8; 531M: 3.15 ms and 3.30).
 static int adamw_chunk(const moe_adamw_tensor_t* tensors, int n_tensors) {
   long long total = 0;
   for (int i = 0; i < n_tensors && total < (4 << 20); ++i) total += tensors[i].n;   // (each is 2^42 at most)

@@ -59,7 +59,7 @@ size_t sum_slots(const LoraShape& s) { return (size_t)(s.M_cap / sum_piece(s)) +
 // reads the whole A, which pays while that is short beside a launch (3.2 us on the
 // host) and the tiles leave more than one workgroup for few compute units alone; the LDS
 // of a larger r holds one or two workgroups on each.  Us of two launches against one, N
-// 4096: 1 row, r 16: K 2880 9.5 / 5.9, K 7168 9.3 / 7.8, K 16384 9.6 / 13.0; r 32, K 4096 9.6
+// 4096: 1 row, r 16: K 2880 9.5 / 5.9, K 7168 9.3 / 7.7, K 16384 9.6 / 13.0; r 32, K 4096 9.6
 // / 7.8; r 64, K 2048 10.3 / 9.2; 64 rows in 32 groups, r 128, K 1024 29.2 / 21.8; 1024 rows
 // in 4 groups (68 tiles): r 16, K 7168 18.0 / 13.3; r 64, K 2048 21.8 / 21.1; r 128, K 1024
 // 29.1 / 33.5; 3000 rows in 8 groups (195): r 16, K 2880 20.0 / 17.4; r 32 24.1 / 23.3; r 64,
@@ -71,8 +71,10 @@ bool fused_rows(const LoraShape& s) {
 // The same for the backward's w and dx, whose weights of r > 32 do not fit the LDS.  Us of a
 // forward and a backward, w and dx in two launches against one, K 4096: 16 rows, r 16, N 1024
 // 18.1 / 15.7; 100 rows in 4 groups, r 32, N 1024 25.7 / 21.9; 1024 rows, r 16, N 2880 35.8 /
-// 32.1; 1500 rows in 96 groups (189 tiles), r 16, N 1024 65.7 / 54.7; 3000 rows in 8 groups
-// (195), r 16, N 2880 62.9 / 63.7.
+// 32.1; 1500 rows in 96 groups (189 tiles), r 16, N 1024 65.3 / 54.6; 2000 rows in 8 groups
+// (133), r 32, N 1024 48.9 / 47.2, N 4096 72.4 / 74.7; 3000 rows in 8 groups (195), r 16, N
+// 2880 62.8 / 62.5, r 32, N 1024 58.4 / 54.9, N 4096 86.7 / 87.8: no more to gain where both
+// are near their end, 1 to 3% lost.
 bool fused_back(const LoraShape& s) {
   return s.r <= 32 && s.r * s.N <= (1 << 17) && tile_bound(s.M_cap, s.L, 16) <= 256;
 }

@@ -43,7 +43,6 @@ __device__ __forceinline__ int of_lane(uint32_t v, int lane) { return __builtin_
 struct LoraTile {
   int e;        // group; -1: there is no such piece
   int row, rows;
-  int index;    // piece of its group
   int pieces;   // of its group
   int slot;     // pieces before it of groups that have more than one
 };
@@ -52,7 +51,9 @@ struct LoraTile {
 // without rows into `least` of none; with MANY the tile-th of the groups that have
 // more than one piece (its first).  Each wave finds it for itself, without LDS or
 // barriers: the groups' counts are cut so that they fit M_cap (a negative one is
-// none), lanes hold PER of them each.
+// none), lanes hold PER of them each.  With PER 16 (more than 64 groups) the counts are
+// loaded one after the other: a call of 64 rows in 64 groups 8.8 us, in 65 10.9, in 1024
+// 13.2 (r 16, K 2880, N 5760).
 template <int PER, bool MANY, bool EVEN>
 __device__ __forceinline__ LoraTile find_piece(const LoraGroups& g, int bm, int least, uint32_t tile) {
   const int lane = threadIdx.x & 63;
@@ -88,7 +89,7 @@ __device__ __forceinline__ LoraTile find_piece(const LoraGroups& g, int bm, int 
   const int at = __builtin_ctzll(past);
   // the lane that holds the piece walks its groups
   uint32_t before = pi - pieces, slot = mi - many, row = first;
-  int e = 0, rows = 0, index = 0, n_of = 0, start = 0, base = 0;
+  int e = 0, rows = 0, n_of = 0, start = 0, base = 0;
   bool found = false;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -96,7 +97,7 @@ __device__ __forceinline__ LoraTile find_piece(const LoraGroups& g, int bm, int 
     const uint32_t units = MANY ? n > 1 : n;
     if (!found && tile - before < units) {
       found = true;
-      index = MANY ? 0 : (int)(tile - before);
+      const int index = MANY ? 0 : (int)(tile - before);
       e = lane * PER + i;
       n_of = (int)n;
       const int len = EVEN && n > 0 ? ((int)((c[i] + n - 1) / n) + 31) / 32 * 32 : bm;
@@ -111,7 +112,6 @@ __device__ __forceinline__ LoraTile find_piece(const LoraGroups& g, int bm, int 
   t.e = of_lane(e, at);
   t.row = of_lane(start, at);
   t.rows = of_lane(rows, at);
-  t.index = of_lane(index, at);
   t.pieces = of_lane(n_of, at);
   t.slot = of_lane(base, at);
   return t;
@@ -247,7 +247,8 @@ __device__ __forceinline__ bf16x8 read_crosswise(const uint16_t* rows0, const ui
 // Measured: 14746 rows, r 64, K 7168 62 us (51 where nothing else uses the memory, 4.1
 // TB/s); 16384 rows in 32 groups, r 32 69 us, 3.4 TB/s, of which a fifth is what the kernel
 // before it wrote on its way to memory; 8191 rows, r 16, K 2880 17 us, a third of it the
-// start (counts, src, the first rows).  Blocks of 256 or 512 columns gained nothing.
+// start (counts, src, the first rows); 8192 rows, r 128, K 7168 68 us, 1.7 TB/s, where the
+// LDS holds one workgroup to a compute unit.  Blocks of 256 or 512 columns gained nothing.
 template <int RB, int MB, bool TURNED>
 __global__ __launch_bounds__(256, RB <= 4 ? 2 : 1) void lora_narrow_kernel(LoraGroups g, const uint16_t* __restrict__ x,
                                                                            long long x_ld,
@@ -444,8 +445,10 @@ __device__ __forceinline__ uint32_t pick16(uint32_t lo, uint32_t hi, bool upper)
 // load and store 256 bytes of a row.
 //
 // Measured: 14746 rows, r 64, N 4096 54 us, 4.4 TB/s; 16384 rows in 32 groups, r 32, N 7168
-// (dx) 103 us, 4.5 TB/s; 8191 rows, r 16, N 5760 39 us, 4.8 TB/s.  Tiles of 32 rows per wave
-// spill at r 128; the weights turned by a kernel of their own cost 9 us more than they save.
+// (dx) 103 us, 4.5 TB/s; 8191 rows, r 16, N 5760 39 us, 4.8 TB/s; 8192 rows, r 128, N 7168
+// 94 us, 2.5 TB/s: a weight fragment is read from LDS for 16 rows a wave, and again for the
+// second part of u.  Tiles of 32 rows per wave spill at r 128; the weights turned by a kernel
+// of their own cost 9 us more than they save.
 template <int KS, bool TURNED>
 __global__ __launch_bounds__(256, KS <= 4 ? 3 : 2) void lora_wide_kernel(LoraGroups g, const float* __restrict__ u_in,
                                                                          int slices, float* __restrict__ u_out,
@@ -517,7 +520,7 @@ __global__ __launch_bounds__(256, KS <= 4 ? 3 : 2) void lora_wide_kernel(LoraGro
   const float s = scale ? scale[t.e] : 1.0f;
   // the slices' sums of the tile, a thread taking every 256th four of its values, through
   // LDS: each wave adding up its own fragments reads everything twice, in KS loops one
-  // after the other (2048 rows, r 64, K and N 2880, 23 slices: 70.5 us; so 21.4)
+  // after the other (3.3 times the kernel's time at 2048 rows, r 64 and 23 slices)
   bf16x8 uv[KS];
   {
     float* us = reinterpret_cast<float*>(ws);
@@ -607,7 +610,9 @@ __global__ __launch_bounds__(256, KS <= 4 ? 3 : 2) void lora_wide_kernel(LoraGro
 // weight is on its way: tiles of 16 rows whose operands go straight from memory to
 // the MFMA.  The narrow one: 512 columns of K per workgroup, whose four waves' sums
 // meet in LDS.  Measured: 1 row, r 16, K 7168, N 4096 3.6 and 5.1 us for the wide one,
-// beside 3.2 us of the host for each launch.
+// beside 3.2 us of the host for each launch; 64 rows in 32 groups 8.3 and 27.8 us at r 64,
+// 14.6 and 59.2 at r 128, where each wave of the wide one adds up all 14 slices of u for
+// itself.
 template <int RB>
 __global__ __launch_bounds__(256) void lora_few_narrow_kernel(LoraGroups g, const uint16_t* __restrict__ x,
                                                               long long x_ld, const uint16_t* __restrict__ A, int r,
@@ -715,10 +720,12 @@ __global__ __launch_bounds__(256) void lora_few_wide_kernel(LoraGroups g, const 
 // tile computes the whole u (its eight waves take runs of 64 columns of K in turn,
 // AT_ONCE of them on their way), then a slice of y's columns, NB runs of 32 at a time
 // for each wave.  With TURNED both weights lie the other way round (the backward's w and
-// dx) and are read crosswise from LDS.  Measured: 58 rows in 32 groups, r 16, K 2880, N 5760 7.4 us for 10.5 MB,
-// 1 row, K 7168, N 4096 8.4: the products one after the other, each a few trips to memory
-// of 0.7 us (A and x loaded as the MFMA takes them 9.6; one, three or more runs at once 8.4
-// to 9.0 at NB 1 for 8.1; y's columns one run at a time 8.0).
+// dx) and are read crosswise from LDS.  Measured under the profiler: 58 rows in 32 groups, r
+// 16, K 2880, N 5760 7.4 us for 10.5 MB, 1 row, K 7168, N 4096 8.4 (calls one after the other
+// 6.7 and 7.7): the products one after the other, each a few trips to memory of 0.7 us.  A's
+// loads wait for src, though they do not need it, and a run's for the one before.  Calls when
+// it was tuned: A and x loaded as the MFMA takes them 9.6; one, three or more runs at once 8.4
+// to 9.0 at NB 1 for 8.1; y's columns one run at a time 8.0.
 template <int RB, int AT_ONCE, int NB, bool TURNED>
 __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint16_t* __restrict__ x, long long x_ld,
                                                        const uint16_t* __restrict__ A, const uint16_t* __restrict__ B,
@@ -916,9 +923,10 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint1
 // columns for [r][C], the ranks for [C][r].
 //
 // Measured (K 7168, N 4096): 8191 rows, r 16, K 2880, N 5760 30 us, 4.8 TB/s; 16384 rows in
-// 32 groups, r 32 127 us, 2.9 TB/s beside 235 MB of dx that go to memory meanwhile; 14746
-// rows, r 64 120 us.  With the rows in registers, taken apart there, r 32 took 119 and r 16
-// 28, but r 64 178 and r 128 197 for 152.  dB in the pass that makes w (dy read once, two
+// 32 groups, r 32 126 us, 2.9 TB/s beside 235 MB of dx that go to memory meanwhile; 14746
+// rows, r 64 117 us, 2.8 TB/s; 8192 rows, r 128, K and N 7168 155 us, 1.5 TB/s: every column
+// block reads u and makes its parts again.  With the rows in registers, taken apart there, r 32 took 119 and r 16
+// 28, but r 64 178 for 120 and r 128 197 for 152.  dB in the pass that makes w (dy read once, two
 // barriers a step): all of the backward 263 for 279 us at r 32, 85 for 83 at r 16, 271 for
 // 264 at r 64.
 struct LoraSum {
