@@ -41,6 +41,11 @@ PATHS = {
     "pieces of 192": ([7001, 0, 1999], 9000, 16, 2056, 1032, (MB2, MB2, 192)),
     "pieces of 256, rank 96": ([4000, 193, 807], 5000, 96, 2312, 2056, (MB2, MB2, 256)),
     "90 groups": ([66, 0, 53, 71, 1, 90] * 15, 4300, 16, 136, 72, (MB1, MB1, 128)),
+    "few rows of many groups": ([3, 0, 4, 5] * 75, 910, 16, 136, 264, (FEW, MB1, 128)),
+    "few rows of many groups, rank 24": ([3, 0, 4, 5] * 75, 910, 24, 512, 72, (FEW, MB1, 128)),
+    "few rows of many groups, rank 40": ([1, 0, 17, 2] * 60, 1200, 40, 264, 136, (MB1, MB1, 128)),
+    "few rows of many groups, rank 64": ([1, 0, 9, 2] * 60, 720, 64, 504, 136, (FEW, MB1, 128)),
+    "few rows of many groups, rank 128": ([1, 0, 2, 5] * 60, 500, 128, 520, 72, (FEW, MB1, 128)),
     "1000 groups": ([5, 0, 6, 7, 3] * 200, 4300, 8, 72, 136, (MB1, MB1, 128)),
 }
 
@@ -58,6 +63,7 @@ def test_forward(G, name, direct):  # noqa: F811
     forward(G, c)
     forward(G, c, base="same", keep_u=False)
     forward(G, c, base=None)
+    forward(G, c, base=None, keep_u=False)
 
 
 @pytest.mark.parametrize("name", list(PATHS))
