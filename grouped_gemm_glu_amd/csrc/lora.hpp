@@ -4,9 +4,8 @@
 // and their gradients.  With w_i = B_e^T dy_i these are the same two products
 // again (dx_i = base_i + s_e A_e^T w_i) and two sums over a group's rows
 // (dA_e = s_e sum w_i x_i^T, dB_e = s_e sum dy_i u_i^T).  r is 8 to 128 where the
-// rows are thousands long, so all of them are bound by memory: each row of x,
-// y, dy and dx is read or written once a kernel, by MFMA fragments that lanes load
-// and store directly.
+// rows are thousands long, so memory is the floor of all of them (what keeps each
+// above it stands there): a row of x, y, dy and dx is read or written once a kernel.
 //
 // v_mfma_f32_16x16x32_bf16: lane l holds row (or column) l % 16 and the eight k
 // from 8 (l / 16) on of each operand, and of the product column l % 16 and

@@ -44,6 +44,28 @@ def test_codes_that_fall(G, beta2, least):  # noqa: F811
     assert torch.equal(v, want) and torch.all((vs - 0.5).abs() <= 1e-4)
 
 
+@pytest.mark.parametrize("beta1,least", [(0.9, 10), (0.99, 100), (0.999, 128)])
+def test_codes_of_m_that_fall(G, beta1, least):  # noqa: F811
+    """Code c of sqrt(|m| / m_scale) = c / 127 becomes c - 1 where c beta1^(1/2) <= c - 1/2."""
+    import torch
+    assert least > 127 or least - 1 < 0.5 / (1 - beta1 ** 0.5) < least
+    n = 128
+    codes = torch.arange(n, device="cuda").to(torch.int8)
+    codes[::3] *= -1
+    m, v = codes.clone(), torch.ones(n, dtype=torch.uint8, device="cuda")
+    m[0] = 127
+    vs, ms = torch.full((1,), 0.5, device="cuda"), torch.full((1,), 0.25, device="cuda")
+    g, p = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    g[0] = 0.25
+    plan = G.adamw_plan([G.adamw_tensor(p, g, m, v, m_scale=ms, v_scale=vs)])
+    for step in range(1, 1001):
+        G.moe_adamw_step(plan, G.adamw(0.0, beta1, 0.999, step=step))
+    torch.cuda.synchronize()
+    want = codes.int().clamp(min=1 - least, max=least - 1)
+    want[0] = 127
+    assert torch.equal(m.int(), want) and abs(float(ms) - 0.25) <= 1e-4
+
+
 def ratios(G, beta2, size, steps, n=128 * 512):  # noqa: F811
     """sqrt(v) of the states over that of 64 bits, after gradients of N(0, size(t)^2), fifth and 95th percentile of each
     of the elements' halves (even and odd)."""
