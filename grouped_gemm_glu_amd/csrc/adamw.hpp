@@ -85,10 +85,11 @@ __device__ __forceinline__ void store_codes4(void* p, long long i, int n, uint32
 //   sqrt(v) = (c / 255)^2 v_scale          c uint8, at least 1 for v > 0
 // The square spreads the codes: a step is 1.6% of the block's largest value near
 // it and still 16% at a hundredth of it.  An element's second moment never
-// becomes 0 beside a first that did not.  With beta2 above 0.9922 no step without a
-// gradient is half a code: an element's v then falls with its block's scale alone.  The code is the nearest under the square
-// root (the lower of two as near) as 64 bits decide it: it is found in 32 bits, and
-// only where they come near a border (or their range ends) compared with it in 64.
+// becomes 0 beside a first that did not.  With beta2 above 0.9922 no step without
+// a gradient is half a code: an element's v then falls with its block's scale alone.
+// The code is the nearest under the square root (the lower of two as near) as 64
+// bits decide it: it is found in 32 bits, and only where they come near a border (or
+// their range ends) compared with it in 64.
 __device__ __forceinline__ double m_of_code(int c, double scale) {
   return (double)(c * (c < 0 ? -c : c)) * (1.0 / 16129.0) * scale;
 }

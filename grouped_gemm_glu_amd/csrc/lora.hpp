@@ -379,7 +379,8 @@ __global__ __launch_bounds__(256, RB <= 4 ? 2 : 1) void lora_narrow_kernel(LoraG
 
 // The u of a row from value c (of 8) of its two parts, as a fragment: the slices'
 // sums added in order, times s; the nearest bf16 value for c < r, what is left for c <
-// 2 r, else 0.  Two parts hold u to 2^-17 of its value, far below the rounding of y.  out (nullable): where the sum itself goes.
+// 2 r, else 0.  Two parts hold u to 2^-17 of its value, far below the rounding of y.
+// out (nullable): where the sum itself goes.
 __device__ __forceinline__ bf16x8 u_fragment(const float* u, long long slice_len, int slices, int r, int c, float s,
                                              bool inside, float* out) {
   f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
@@ -924,10 +925,10 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraGroups g, const uint1
 // Measured (K 7168, N 4096): 8191 rows, r 16, K 2880, N 5760 30 us, 4.8 TB/s; 16384 rows in
 // 32 groups, r 32 126 us, 2.9 TB/s beside 235 MB of dx that go to memory meanwhile; 14746
 // rows, r 64 117 us, 2.8 TB/s; 8192 rows, r 128, K and N 7168 155 us, 1.5 TB/s: every column
-// block reads u and makes its parts again.  With the rows in registers, taken apart there, r 32 took 119 and r 16
-// 28, but r 64 178 for 120 and r 128 197 for 152.  dB in the pass that makes w (dy read once, two
-// barriers a step): all of the backward 263 for 279 us at r 32, 85 for 83 at r 16, 271 for
-// 264 at r 64.
+// block reads u and makes its parts again.  With the rows in registers, taken apart there,
+// r 32 took 119 and r 16 28, but r 64 178 for 120 and r 128 197 for 152.  dB in the pass that
+// makes w (dy read once, two barriers a step): all of the backward 263 for 279 us at r 32, 85
+// for 83 at r 16, 271 for 264 at r 64.
 struct LoraSum {
   const float* u;
   const uint16_t* v;
